@@ -50,6 +50,14 @@ FD_SCALE_TENSOR = 0
 FD_SCALE_HEAD = 1
 FD_SCALE_TOKEN = 2
 
+FD_ROTARY_PLAIN = 0
+FD_ROTARY_LINEAR = 1
+FD_ROTARY_BY_PARTS = 2
+
+# names of the rotary scalings -> fd_rotary_scaling codes
+ROTARY_SCALINGS = {"none": FD_ROTARY_PLAIN, "linear": FD_ROTARY_LINEAR,
+                   "by_parts": FD_ROTARY_BY_PARTS}
+
 EXPORTED = [
     "fd_workspace_bytes", "fd_decode_attention", "fd_check_device_error", "fd_status_string",
     "fd_set_kernel", "fd_selected_kernel", "fd_selected_kernel_scaled", "fd_set_split_events",
@@ -57,6 +65,8 @@ EXPORTED = [
     "fd_debug_gather_kv", "fd_decode_attention_noalloc", "fd_decode_attention_scaled",
     "fd_append_kv", "fd_decode_attention_append", "fd_decode_attention_multi",
     "fd_debug_set_wait_limit", "fd_debug_plan_segments",
+    "fd_rotary_table", "fd_append_kv_packed", "fd_read_kv", "fd_prefill_workspace_bytes",
+    "fd_prefill_attention",
 ]
 
 
@@ -130,6 +140,22 @@ def load_library(path: Optional[str] = None):
         lib.fd_debug_plan_segments.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
                                                vp, i64, i32, ctypes.POINTER(ctypes.c_int), vp, sz,
                                                vp]
+        f64 = ctypes.c_double
+        lib.fd_rotary_table.restype = i32
+        lib.fd_rotary_table.argtypes = [vp, i64, i32, f64, i32, f64, f64, f64, f64, f32, vp]
+        lib.fd_append_kv_packed.restype = i32
+        lib.fd_append_kv_packed.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp,
+                                            i64, i64, i32, i32, i32, i32, i32, vp, i64, i32, i32,
+                                            f32, f32, i32, vp, vp, i32, i32, vp, sz, vp]
+        lib.fd_read_kv.restype = i32
+        lib.fd_read_kv.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i64, i32, i32, i32, i32, f32,
+                                   f32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        lib.fd_prefill_workspace_bytes.restype = sz
+        lib.fd_prefill_workspace_bytes.argtypes = [i32]
+        lib.fd_prefill_attention.restype = i32
+        lib.fd_prefill_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, vp, vp, i64, i64, i32,
+                                             i32, i32, i32, i32, f32, f32, f32, i32, vp, vp, i32,
+                                             i32, vp, vp, vp, sz, vp]
         if path is None:
             _lib = lib
         return lib
@@ -336,6 +362,96 @@ def fd_decode_attention_noalloc(q, k_cache, v_cache, kv_start_idx, block_table, 
     return st
 
 
+def fd_rotary_table(table, positions: int, rot_dim: int, theta: float, scaling: int,
+                    factor: float, original_positions: float, low_turns: float,
+                    high_turns: float, amplitude: float, stream=None, check: bool = True) -> int:
+    """Fills ``table`` (fp32 [positions, rot_dim]) with the cosines, then the
+    sines of every position's angles."""
+    st = load_library().fd_rotary_table(
+        _ptr(table), int(positions), int(rot_dim), float(theta), int(scaling), float(factor),
+        float(original_positions), float(low_turns), float(high_turns), float(amplitude),
+        _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_rotary_table")
+    return st
+
+
+def fd_append_kv_packed(q, q_stride: int, q_out, k_new, v_new, kv_stride: int, k_cache, v_cache,
+                        kv_start_idx, block_table, q_start, positions, num_tokens: int,
+                        kv_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                        page_size: int, rotary, rot_dim: int, interleaved: bool, k_scale: float,
+                        v_scale: float, scale_kind: int, k_scales, v_scales, workspace,
+                        stream=None, new_dtype: Optional[int] = None,
+                        kv_dtype: Optional[int] = None, check: bool = True) -> int:
+    """Rotates (``rotary``: a table of fd_rotary_table, or None) and writes
+    packed new tokens into the caches; ``q`` (or None) is rotated into
+    ``q_out``."""
+    lib = load_library()
+    stride = int(block_table.shape[1]) if block_table is not None else 0
+    st = lib.fd_append_kv_packed(
+        _ptr(q), int(q_stride), _ptr(q_out), _ptr(k_new), _ptr(v_new), int(kv_stride),
+        _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx), _ptr(block_table), stride,
+        _ptr(q_start), _ptr(positions), int(num_tokens), int(kv_rows), int(positions.shape[0]),
+        int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), _ptr(rotary),
+        int(rotary.shape[0]) if rotary is not None else 0, int(rot_dim), int(bool(interleaved)),
+        float(k_scale), float(v_scale), int(scale_kind), _ptr(k_scales), _ptr(v_scales),
+        _q_dtype(k_new) if new_dtype is None else int(new_dtype),
+        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_append_kv_packed")
+    return st
+
+
+def fd_read_kv(k_cache, v_cache, kv_start_idx, block_table, out_start, first, num_rows: int,
+               kv_rows: int, num_kv_heads: int, head_dim: int, page_size: int, k_scale: float,
+               v_scale: float, scale_kind: int, k_scales, v_scales, k_out, v_out, workspace,
+               stream=None, out_dtype: Optional[int] = None, kv_dtype: Optional[int] = None,
+               check: bool = True) -> int:
+    """Reads cached tokens (from ``first`` on, or from each sequence's start)
+    back into packed 16-bit rows."""
+    lib = load_library()
+    stride = int(block_table.shape[1]) if block_table is not None else 0
+    st = lib.fd_read_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx), _ptr(block_table), stride,
+        _ptr(out_start), _ptr(first), int(num_rows), int(kv_rows), int(out_start.shape[0]) - 1,
+        int(num_kv_heads), int(head_dim), int(page_size), float(k_scale), float(v_scale),
+        int(scale_kind), _ptr(k_scales), _ptr(v_scales),
+        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype),
+        _q_dtype(k_out) if out_dtype is None else int(out_dtype), _ptr(k_out), _ptr(v_out),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_read_kv")
+    return st
+
+
+def fd_prefill_workspace_bytes(head_dim: int) -> int:
+    return int(load_library().fd_prefill_workspace_bytes(int(head_dim)))
+
+
+def fd_prefill_attention(q, q_stride: int, k_cache, v_cache, kv_start_idx, block_table, q_start,
+                         seq_len, num_tokens: int, kv_rows: int, num_q_heads: int,
+                         num_kv_heads: int, head_dim: int, page_size: int, softmax_scale: float,
+                         k_scale: float, v_scale: float, scale_kind: int, k_scales, v_scales, out,
+                         lse, workspace, stream=None, q_dtype: Optional[int] = None,
+                         kv_dtype: Optional[int] = None, check: bool = True) -> int:
+    """Attention of packed new tokens (the last of each sequence's ``seq_len``
+    cached ones) over the caches."""
+    lib = load_library()
+    stride = int(block_table.shape[1]) if block_table is not None else 0
+    st = lib.fd_prefill_attention(
+        _ptr(q), int(q_stride), _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx),
+        _ptr(block_table), stride, _ptr(q_start), _ptr(seq_len), int(num_tokens), int(kv_rows),
+        int(seq_len.shape[0]), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
+        float(softmax_scale), float(k_scale), float(v_scale), int(scale_kind), _ptr(k_scales),
+        _ptr(v_scales), _q_dtype(q) if q_dtype is None else int(q_dtype),
+        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype), _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_prefill_attention")
+    return st
+
+
 def fd_check_device_error(workspace, stream=None):
     """Returns (status, info) and clears the workspace's device-error word."""
     info = ctypes.c_int64(0)
@@ -500,4 +616,280 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         fd_decode_attention_scaled(q, k_cache, v_cache, kv_start_idx, block_table, seq_len,
                                    kv_rows, QH, KVH, D, P, softmax_scale, k_scale, v_scale, kind,
                                    k_scales, v_scales, out, lse, workspace, stream)
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# convenience API of the prompt path
+# ---------------------------------------------------------------------------
+
+def _on(device, stream):
+    """Context in which ``device``, and ``stream`` if one is given, are current:
+    what a call allocates for itself then belongs to the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _heads_rows(name: str, t: torch.Tensor, heads: int, dim: int) -> int:
+    """Checks a packed [tokens, heads, dim] tensor whose tokens may lie apart
+    (a slice of a wider projection) and returns its token stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _cache_sizes(k_cache, v_cache, kv_start_idx, block_table):
+    """(kv_rows, KVH, D, page_size) of a contiguous or paged cache."""
+    if (kv_start_idx is None) == (block_table is None):
+        raise ValueError("give kv_start_idx (contiguous cache) or block_table (paged cache)")
+    want = 4 if block_table is not None else 3
+    if k_cache.dim() != want or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"k_cache and v_cache must be alike and {want}-d, got "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
+    if block_table is not None:
+        pages, P, KVH, D = k_cache.shape
+        return pages * P, KVH, D, P
+    rows, KVH, D = k_cache.shape
+    return rows, KVH, D, 0
+
+
+def _scale_kind(k_scales, v_scales, kv_rows: int, KVH: int) -> int:
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("give k_scales and v_scales, or neither")
+    if k_scales is None:
+        return FD_SCALE_TENSOR
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or \
+                tuple(t.shape) not in ((KVH,), (kv_rows, KVH)) or t.shape != k_scales.shape:
+            raise ValueError(f"{name} must be dense fp32 [{KVH}] or [{kv_rows}, {KVH}], got "
+                             f"{t.dtype} {tuple(t.shape)}")
+    return FD_SCALE_HEAD if k_scales.dim() == 1 else FD_SCALE_TOKEN
+
+
+def _check_index(device, batch: int, **arrays) -> None:
+    """int32 index arrays on the caches' device: ``q_start`` / ``out_start``
+    have batch + 1 entries, the others batch."""
+    for name, t in arrays.items():
+        if t is None:
+            continue
+        n = batch + 1 if name in ("q_start", "out_start") else batch
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != n or \
+                t.dim() != (2 if name == "block_table" else 1):
+            raise ValueError(f"{name} must be dense int32 with {n} entries, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+
+
+def _check_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+
+
+def alloc_prefill_workspace(head_dim: int, device=None) -> torch.Tensor:
+    """Workspace of prefill_attention (and enough for append_kv and read_kv)
+    on ``device``; keep it from call to call."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = fd_prefill_workspace_bytes(head_dim)
+        if n == 0:
+            raise FdError(FD_ERR_INVALID_ARG, "fd_prefill_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:256].zero_()   # the device-error word; the rest is scratch
+    return ws
+
+
+def rotary_table(positions: int, rot_dim: int, *, theta: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_positions: float = 0.0, low_turns: float = 1.0,
+                 high_turns: float = 32.0, amplitude: float = 1.0, device=None,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """cos and sin of rotary positions 0 .. positions - 1: fp32 [positions,
+    rot_dim], cosines then sines of the rot_dim / 2 pairs.  ``scaling``: "none",
+    "linear" (frequencies / ``factor``) or "by_parts" (pairs that turn fewer
+    than ``low_turns`` times over ``original_positions`` are scaled, those that
+    turn more than ``high_turns`` times are not, the others in between)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    if out is not None and (out.dtype != torch.float32 or not out.is_contiguous() or
+                            tuple(out.shape) != (positions, rot_dim)):
+        raise ValueError(f"out must be dense fp32 [{positions}, {rot_dim}]")
+    device = torch.device(device or "cuda") if out is None else out.device
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty((int(positions), int(rot_dim)), dtype=torch.float32, device=device)
+        fd_rotary_table(out, positions, rot_dim, theta, ROTARY_SCALINGS[scaling], factor,
+                        original_positions, low_turns, high_turns, amplitude)
+    return out
+
+
+def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, q_start: torch.Tensor, positions: torch.Tensor, *,
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              rotary: Optional[torch.Tensor] = None, interleaved: bool = False,
+              kv_start_idx: Optional[torch.Tensor] = None,
+              block_table: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+              v_scale: float = 1.0, k_scales: Optional[torch.Tensor] = None,
+              v_scales: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Writes packed new tokens ([tokens, KVH, D], sequence b's at
+    ``q_start[b]`` .. ``q_start[b + 1]`` - 1, the first of them at position
+    ``positions[b]``) into a contiguous or paged cache, quantised for 8-bit
+    caches (per-token scales are written).  With ``rotary`` (a table of
+    ``rotary_table``) the first ``rotary.shape[1]`` dims of every key head, and
+    of every head of ``q`` ([tokens, QH, D]), are turned by their positions
+    first, as pairs half of that apart or, with ``interleaved``, neighbouring
+    ones.  Returns the turned queries (``q_out``, fresh unless given; q itself
+    is allowed), or None without ``q``.  k_new, v_new and q may be slices of
+    one wider projection."""
+    kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
+    dev = k_cache.device
+    n = k_new.shape[0]
+    ks, vs = _heads_rows("k_new", k_new, KVH, D), _heads_rows("v_new", v_new, KVH, D)
+    if v_new.shape[0] != n or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new must be alike")
+    if ks != vs:
+        raise ValueError(f"k_new and v_new must have one token stride, got {ks} and {vs}")
+    _check_index(dev, positions.shape[0], q_start=q_start, positions=positions,
+                 kv_start_idx=kv_start_idx, block_table=block_table)
+    _check_device(dev, k_new=k_new, v_new=v_new, v_cache=v_cache, q=q, q_out=q_out, rotary=rotary,
+                  k_scales=k_scales, v_scales=v_scales, workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    QH = qs = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n or q.dtype != k_new.dtype:
+            raise ValueError(f"q must be [{n}, heads, {D}] of k_new's dtype")
+        QH = q.shape[1]
+        qs = _heads_rows("q", q, QH, D)
+        if q_out is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or
+                                  not q_out.is_contiguous()):
+            raise ValueError("q_out must be dense and like q")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rot = 0
+    if rotary is not None:
+        if rotary.dim() != 2 or rotary.dtype != torch.float32 or not rotary.is_contiguous():
+            raise ValueError("rotary must be a dense fp32 [positions, rot_dim] table")
+        rot = rotary.shape[1]
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        fd_append_kv_packed(q, qs, q_out, k_new, v_new, ks, k_cache, v_cache, kv_start_idx,
+                            block_table, q_start, positions, n, kv_rows, QH, KVH, D, P, rotary,
+                            rot, interleaved, k_scale, v_scale, kind, k_scales, v_scales,
+                            workspace)
+    return q_out
+
+
+def read_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, out_start: torch.Tensor, num_rows: int,
+            *, first: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+            kv_start_idx: Optional[torch.Tensor] = None,
+            block_table: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+            v_scale: float = 1.0, k_scales: Optional[torch.Tensor] = None,
+            v_scales: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+            v_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+            stream=None):
+    """Reads cached tokens back as packed rows: rows ``out_start[b]`` ..
+    ``out_start[b + 1]`` - 1 of the returned (k, v), each [num_rows, KVH, D],
+    are sequence b's tokens from ``first[b]`` (0 without ``first``) on, decoded
+    and scaled.  ``dtype`` defaults to the cache's 16-bit type, or f16."""
+    kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
+    dev = k_cache.device
+    batch = out_start.shape[0] - 1
+    _check_index(dev, batch, out_start=out_start, first=first, kv_start_idx=kv_start_idx,
+                 block_table=block_table)
+    _check_device(dev, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
+                  v_out=v_out, workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else k_cache.dtype if \
+            k_cache.dtype in (torch.float16, torch.bfloat16) else torch.float16
+    shape = (int(num_rows), KVH, D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or
+                              not t.is_contiguous()):
+            raise ValueError(f"{name} must be dense {dtype} {shape}")
+    with _on(dev, stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        if workspace is None:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        fd_read_kv(k_cache, v_cache, kv_start_idx, block_table, out_start, first, num_rows,
+                   kv_rows, KVH, D, P, k_scale, v_scale, kind, k_scales, v_scales, k_out, v_out,
+                   workspace)
+    return k_out, v_out
+
+
+def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      q_start: torch.Tensor, seq_len: torch.Tensor, *,
+                      kv_start_idx: Optional[torch.Tensor] = None,
+                      block_table: Optional[torch.Tensor] = None,
+                      softmax_scale: Optional[float] = None, k_scale: float = 1.0,
+                      v_scale: float = 1.0, k_scales: Optional[torch.Tensor] = None,
+                      v_scales: Optional[torch.Tensor] = None,
+                      k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None,
+                      rotary: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of packed new tokens ``q`` [tokens, QH, D] (sequence b's at
+    ``q_start[b]`` .. ``q_start[b + 1]`` - 1: the last of its ``seq_len[b]``
+    tokens, causal) over a contiguous or paged cache; returns (out, lse).
+    With ``k_new`` / ``v_new`` [tokens, KVH, D] and ``positions`` the new tokens
+    are first written into the caches by ``append_kv`` (queries and keys turned
+    by ``rotary`` if given); ``seq_len`` counts them.  Without ``k_new`` the
+    caches hold them already and ``q`` is taken as it is."""
+    kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
+    dev = k_cache.device
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, {D}], got {tuple(q.shape)}")
+    n, QH = q.shape[0], q.shape[1]
+    qs = _heads_rows("q", q, QH, D)
+    _check_index(dev, seq_len.shape[0], q_start=q_start, seq_len=seq_len,
+                 kv_start_idx=kv_start_idx, block_table=block_table)
+    _check_device(dev, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, out=out,
+                  lse=lse, workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    if (k_new is None) != (v_new is None) or (k_new is None) != (positions is None):
+        raise ValueError("give k_new, v_new and positions, or none of them")
+    if rotary is not None and k_new is None:
+        raise ValueError("rotary turns queries together with new keys: give k_new")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
+                            not out.is_contiguous()):
+        raise ValueError("out must be dense and like q")
+    if lse is not None and (tuple(lse.shape) != (n, QH) or lse.dtype != torch.float32 or
+                            not lse.is_contiguous()):
+        raise ValueError(f"lse must be dense fp32 [{n}, {QH}]")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((n, QH), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = alloc_prefill_workspace(D, dev)
+        if k_new is not None:
+            turned = append_kv(k_new, v_new, k_cache, v_cache, q_start, positions,
+                               q=q if rotary is not None else None, rotary=rotary,
+                               interleaved=interleaved, kv_start_idx=kv_start_idx,
+                               block_table=block_table, k_scale=k_scale, v_scale=v_scale,
+                               k_scales=k_scales, v_scales=v_scales, workspace=workspace)
+            if turned is not None:
+                q, qs = turned, QH * D
+        fd_prefill_attention(q, qs, k_cache, v_cache, kv_start_idx, block_table, q_start, seq_len,
+                             n, kv_rows, QH, KVH, D, P, softmax_scale, k_scale, v_scale, kind,
+                             k_scales, v_scales, out, lse, workspace)
     return out, lse

@@ -51,6 +51,8 @@ constexpr int kMaxDevices = 64;
 std::mutex g_dev_mu;
 int g_dev_sms[kMaxDevices] = {0};
 
+}  // namespace
+
 int current_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
@@ -63,6 +65,13 @@ int current_sms() {
   return g_dev_sms[dev];
 }
 
+unsigned long long wait_limit_ns() {
+  const long long wns = g_wait_ns.load();
+  return wns > 0 ? (unsigned long long)wns : kDefaultWaitNs;
+}
+
+namespace {
+
 struct Config {
   int kernel;   // FD_KERNEL_SIMT or FD_KERNEL_MMA
   int hc, hg, hq, tile, grid;
@@ -70,12 +79,6 @@ struct Config {
 };
 
 constexpr int kSimtTile = 32;
-
-bool dtypes_ok(int q_dtype, int kv_dtype) {
-  if (q_dtype != FD_F16 && q_dtype != FD_BF16) return false;
-  if (kv_dtype == FD_E4M3 || kv_dtype == FD_I8) return true;
-  return kv_dtype == q_dtype;
-}
 
 // Chooses the split kernel and its plan shape; false if unsupported.
 bool choose(int pref, int num_q_heads, int num_kv_heads, int head_dim, int q_dtype, int kv_dtype,
@@ -129,16 +132,6 @@ bool choose(int pref, int num_q_heads, int num_kv_heads, int head_dim, int q_dty
   c->seg_units = 0;
   return true;
 }
-
-bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-
-int log2i(int x) {
-  int r = 0;
-  while ((1 << r) < x) ++r;
-  return r;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The new token's rows and where they go (KV append).
 struct AppendArgs {
@@ -437,8 +430,7 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
   p.scale_kind = scale_kind;
   p.k_scales = scale_kind == FD_SCALE_TENSOR ? nullptr : k_scales;
   p.v_scales = scale_kind == FD_SCALE_TENSOR ? nullptr : v_scales;
-  const long long wns = g_wait_ns.load();
-  p.wait_ns = wns > 0 ? (unsigned long long)wns : kDefaultWaitNs;
+  p.wait_ns = wait_limit_ns();
   p.starve = g_starve.load();
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -471,6 +471,28 @@ inline cudaError_t ensure_smem_limit(Kernel kern, int bytes,
   return e;
 }
 
+// ---------------------------------------------------------------------------
+// Host helpers shared by the entry points (fd_api.cu, fd_prompt_api.cu)
+// ---------------------------------------------------------------------------
+int current_sms();                     // SM count of the current device, 0 on failure
+unsigned long long wait_limit_ns();    // bound of a kernel's waits (fd_debug_set_wait_limit)
+
+inline bool dtypes_ok(int q_dtype, int kv_dtype) {
+  if (q_dtype != FD_F16 && q_dtype != FD_BF16) return false;
+  if (kv_dtype == FD_E4M3 || kv_dtype == FD_I8) return true;
+  return kv_dtype == q_dtype;
+}
+
+inline bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
+
+inline int log2i(int x) {
+  int r = 0;
+  while ((1 << r) < x) ++r;
+  return r;
+}
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
 // Host-side argument checks shared by the decode entry points (fd_api.cu).
 fd_status check_decode_args(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* kv_start_idx, const int32_t* block_table,

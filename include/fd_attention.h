@@ -331,6 +331,163 @@ fd_status fd_decode_attention_noalloc(const void *q, const void *k_cache, const 
                                       fd_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The prompt path: everything between a prompt and its first decode step.
+ *
+ * Packed tokens.  The new tokens of a batch lie behind one another without
+ * padding: q_start is a device int32 array [batch + 1], ascending, and
+ * sequence b owns tokens q_start[b] .. q_start[b + 1] - 1 of every packed
+ * array (none, one or many; a decode step's single tokens and a prompt's
+ * thousands may share one call).  Tokens outside [q_start[0],
+ * q_start[batch]) belong to no sequence: nothing is read for them and their
+ * rows of every output are left as they were.  A sequence whose entries
+ * descend or lie outside the packed arrays is skipped and recorded as
+ * FD_ERR_DEVICE_BOUNDS (info: the offending entry).
+ *
+ * Caches, block tables, scales, dtypes, workspaces, streams and errors are
+ * those of the decode entry points above, and so are the addressing rules:
+ * rows outside [0, kv_rows), negative page ids and pages past
+ * block_table_stride are never touched and are recorded as
+ * FD_ERR_DEVICE_BOUNDS.
+ * ---------------------------------------------------------------------------
+ */
+
+/* How rotary frequencies are scaled for contexts longer than the trained one. */
+typedef enum {
+  FD_ROTARY_PLAIN = 0,   /* f_i */
+  FD_ROTARY_LINEAR = 1,  /* f_i / factor (positions compressed by factor) */
+  FD_ROTARY_BY_PARTS = 2 /* by the turns r_i = original_positions * f_i / (2 pi) that a pair makes
+                            over the trained context: g f_i + (1 - g) f_i / factor,
+                            g = clamp((r_i - low_turns) / (high_turns - low_turns), 0, 1) */
+} fd_rotary_scaling;
+
+/*
+ * Table of rotary positions: row p (0 <= p < positions) of `table` holds
+ * amplitude * cos(p g_i) for i = 0 .. rot_dim / 2 - 1, then
+ * amplitude * sin(p g_i), with g_i the scaled frequency of
+ * f_i = theta^(-2 i / rot_dim).  Angles are exact to about 2^-53 of a turn per
+ * position (fixed-point turns), so far positions keep fp32 accuracy.
+ *
+ * table      device fp32 [positions, rot_dim], 16-byte aligned.
+ * positions  1 .. 2^31 - 1.
+ * rot_dim    multiple of 16, 16 .. 128.
+ * theta      finite, > 1.   factor  finite, >= 1 (ignored by FD_ROTARY_PLAIN).
+ * original_positions > 0 and 0 <= low_turns < high_turns, finite
+ *            (FD_ROTARY_BY_PARTS only).
+ * amplitude  finite.
+ */
+fd_status fd_rotary_table(float *table, int64_t positions, int rot_dim, double theta,
+                          fd_rotary_scaling scaling, double factor, double original_positions,
+                          double low_turns, double high_turns, float amplitude,
+                          fd_stream_t stream);
+
+/*
+ * Writes packed new tokens into the caches, any number per sequence, with
+ * optional rotary positions.  Token i of sequence b (packed index
+ * q_start[b] + i) stands at position t = positions[b] + i and goes to that
+ * token's cache row, as in fd_append_kv (16-bit caches: the elements rounded
+ * once to the cache's type; 8-bit caches: the codes and scales of
+ * fd_append_kv).  With a rotary table, pair (x1, x2) i of the first rot_dim
+ * dims of every query and key head becomes
+ *     y1 = x1 cos_i - x2 sin_i,   y2 = x2 cos_i + x1 sin_i
+ * (row t of the table) before that; values are not rotated.  A pair is dims
+ * (i, i + rot_dim / 2), or with `interleaved` non-zero dims (2 i, 2 i + 1).
+ * Each product, sum and quotient is one IEEE fp32 operation; keys enter the
+ * 8-bit quantisation unrounded.
+ *
+ * q          [num_tokens, num_q_heads, head_dim] of new_dtype, tokens
+ *            q_stride elements apart, or NULL (only k and v are written).
+ * q_out      dense [num_tokens, num_q_heads, head_dim]; may equal q when q is
+ *            dense.  Required with q.
+ * k_new, v_new  [num_tokens, num_kv_heads, head_dim] of new_dtype, tokens
+ *            kv_stride elements apart.
+ * q_stride, kv_stride  multiples of 8 elements, at least one token's heads
+ *            (so q, k and v may be slices of one projection's output).
+ * positions  int32 [batch]: position of each sequence's first new token;
+ *            < 0 leaves the sequence alone (its q_out rows too).
+ * num_tokens rows of the packed arrays (0: nothing to do); < 2^31.
+ * rotary     table of fd_rotary_table, [rotary_positions, rot_dim] fp32,
+ *            16-byte aligned, or NULL (no rotation).  A token at or past
+ *            rotary_positions is skipped and recorded as FD_ERR_DEVICE_BOUNDS.
+ * rot_dim    multiple of 16, 16 .. head_dim (ignored without a table).
+ * The other arguments are those of fd_append_kv.  Two tokens that share a
+ * cache row race; callers give distinct rows.
+ */
+fd_status fd_append_kv_packed(const void *q, int64_t q_stride, void *q_out, const void *k_new,
+                              const void *v_new, int64_t kv_stride, void *k_cache, void *v_cache,
+                              const int32_t *kv_start_idx, const int32_t *block_table,
+                              int block_table_stride, const int32_t *q_start,
+                              const int32_t *positions, int64_t num_tokens, int64_t kv_rows,
+                              int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                              int page_size, const float *rotary, int64_t rotary_positions,
+                              int rot_dim, int interleaved, float k_scale, float v_scale,
+                              fd_scale_kind scale_kind, float *k_scales, float *v_scales,
+                              fd_dtype new_dtype, fd_dtype kv_dtype, void *workspace,
+                              size_t workspace_bytes, fd_stream_t stream);
+
+/*
+ * Reads cached tokens back as packed 16-bit rows: packed row i of sequence b
+ * (out_start[b] <= i < out_start[b + 1]) receives token
+ * first[b] + i - out_start[b] of that sequence,
+ *     k = round(k_scale * ks * dec(code)),   v likewise,
+ * the decode entry points' values, rounded once to out_dtype (the products of
+ * scales and of scale and element are single fp32 operations).
+ *
+ * out_start  int32 [batch + 1], packed as q_start above.
+ * first      int32 [batch] first token of each sequence, or NULL for 0; < 0
+ *            leaves the sequence's rows as they were.
+ * num_rows   rows of k_out and v_out (0: nothing to do); < 2^31.
+ * k_out, v_out  dense [num_rows, num_kv_heads, head_dim] of out_dtype (FD_F16
+ *            or FD_BF16; that of a 16-bit cache), 16-byte aligned.
+ * Rows of tokens outside the cache receive zeros and are recorded.
+ */
+fd_status fd_read_kv(const void *k_cache, const void *v_cache, const int32_t *kv_start_idx,
+                     const int32_t *block_table, int block_table_stride,
+                     const int32_t *out_start, const int32_t *first, int64_t num_rows,
+                     int64_t kv_rows, int batch, int num_kv_heads, int head_dim, int page_size,
+                     float k_scale, float v_scale, fd_scale_kind scale_kind,
+                     const float *k_scales, const float *v_scales, fd_dtype kv_dtype,
+                     fd_dtype out_dtype, void *k_out, void *v_out, void *workspace,
+                     size_t workspace_bytes, fd_stream_t stream);
+
+/* Scratch bytes fd_prefill_attention needs on the current device (host
+ * function), for any batch, lengths and head counts; 0 for an invalid
+ * head_dim. */
+size_t fd_prefill_workspace_bytes(int head_dim);
+
+/*
+ * Attention of packed new tokens over the caches, which already hold them:
+ * the prompt (or a chunk of it, or single tokens) of every sequence.  The
+ * last n = q_start[b + 1] - q_start[b] tokens of sequence b's seq_len[b] are
+ * the new ones; new token j sits at position seq_len[b] - n + j and attends
+ * to its own and every earlier key, with the definition of
+ * fd_decode_attention.  A token with no key (seq_len[b] < n - j) gets out = 0
+ * and lse = -inf.  Cached rows past a token's position, rows of other
+ * sequences and unused pages have no effect, whatever bits they hold.
+ *
+ * q          [num_tokens, num_q_heads, head_dim] of q_dtype, tokens q_stride
+ *            elements apart (a multiple of 8, at least one token's heads).
+ * out        dense [num_tokens, num_q_heads, head_dim] of q_dtype.
+ * lse        fp32 [num_tokens, num_q_heads], or NULL.
+ * num_tokens rows of q, out and lse (0: nothing to do); < 2^31.
+ * workspace  >= fd_prefill_workspace_bytes(head_dim), 256-byte aligned.
+ * A 128-key tile that holds a row outside the cache is treated as absent and
+ * recorded.  kv_rows < 2^31.  Every other argument as for
+ * fd_decode_attention_scaled.
+ */
+fd_status fd_prefill_attention(const void *q, int64_t q_stride, const void *k_cache,
+                               const void *v_cache, const int32_t *kv_start_idx,
+                               const int32_t *block_table, int block_table_stride,
+                               const int32_t *q_start, const int32_t *seq_len,
+                               int64_t num_tokens, int64_t kv_rows, int batch, int num_q_heads,
+                               int num_kv_heads, int head_dim, int page_size,
+                               float softmax_scale, float k_scale, float v_scale,
+                               fd_scale_kind scale_kind, const float *k_scales,
+                               const float *v_scales, fd_dtype q_dtype, fd_dtype kv_dtype,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               fd_stream_t stream);
+
+/*
  * Synchronises `stream`, reads and clears the workspace's sticky device-error
  * word.  Returns FD_OK, FD_ERR_DEVICE_BOUNDS, FD_ERR_DEVICE_TIMEOUT or
  * FD_ERR_CUDA.  If info is not NULL it receives the first offending value
