@@ -70,6 +70,8 @@ unsigned long long wait_limit_ns() {
   return wns > 0 ? (unsigned long long)wns : kDefaultWaitNs;
 }
 
+int starve_switch() { return g_starve.load(); }
+
 namespace {
 
 struct Config {
@@ -431,7 +433,7 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
   p.k_scales = scale_kind == FD_SCALE_TENSOR ? nullptr : k_scales;
   p.v_scales = scale_kind == FD_SCALE_TENSOR ? nullptr : v_scales;
   p.wait_ns = wait_limit_ns();
-  p.starve = g_starve.load();
+  p.starve = starve_switch();
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   FD_RANGE("fd_decode_attention");

@@ -476,6 +476,7 @@ inline cudaError_t ensure_smem_limit(Kernel kern, int bytes,
 // ---------------------------------------------------------------------------
 int current_sms();                     // SM count of the current device, 0 on failure
 unsigned long long wait_limit_ns();    // bound of a kernel's waits (fd_debug_set_wait_limit)
+int starve_switch();                   // its test switch
 
 inline bool dtypes_ok(int q_dtype, int kv_dtype) {
   if (q_dtype != FD_F16 && q_dtype != FD_BF16) return false;

@@ -1,0 +1,1312 @@
+// fd_prefill.cuh -- attention of packed new tokens over the cache, on the
+// fifth-generation tensor cores; included by one translation unit per format
+// (fd_prefill_*.cu), which instantiate its variants, and by fd_prefill.cu
+// (tensor maps, dispatch, merge).
+//
+//   s_t = softmax_scale k_scale ks_t (q . k_t),  t <= position of the token,
+//   m = max_t s_t log2 e,  p_t = 2^(s_t log2 e - m),  l = sum_t p_t,
+//   out = v_scale sum_t p_t vs_t v_t / l,  lse = (m + log2 l) ln 2,
+// one pass over the keys in tiles of 128 with a running m and l.
+//
+// Rows.  A KV head's group of g query heads times the tokens of a sequence
+// are the rows of a product with that head's keys; a query tile is 128 / g
+// whole tokens (at most 128 rows), and a CTA works on two neighbouring query
+// tiles A and B at a time against the same stream of K and V tiles, so that
+// the softmax of one runs while the tensor cores work for the other.
+//
+// Split.  (sequence, KV head, pair of query tiles) are the streams.  Their
+// costs (keys to pass, once per active query tile, plus a start) are laid
+// end to end and cut into one equal range per CTA, whatever the lengths: a
+// long prompt's causal triangle, a chunk over a long context and single
+// tokens beside them all fill the GPU.  A stream cut between CTAs leaves
+// partial states (m, l, unnormalised out) that fd_prefill.cu merges in a
+// fixed order.
+//
+// Roles (one persistent CTA per SM):
+//   warps 0-3, 4-7  softmax of query tile A, B: one row per thread, the row's
+//                   128 scores in registers; P overwrites S in tensor memory
+//                   as 16-bit pairs;
+//   warp 8          TMA producer: Q tiles, K and V tiles through one ring;
+//   warp 9          issues S = Q K^T and O += P V for A and B as their inputs
+//                   become ready (O and S: 2 x 128 columns each, all 512);
+//   warps 10-11     repair V tiles that some row may not see (see below);
+//   warps 12-15     (8-bit caches, or pages of fewer than 8 rows) widen or
+//                   copy the cache rows into the ring; the producer then feeds
+//                   raw tiles to them.
+//
+// A tile in which some row sees fewer than all keys: scores of unseen keys
+// are excluded by selection, so K may hold any bits there, but in O += P V an
+// unseen non-finite V element would reach every row as 0 * NaN.  V elements
+// of such tiles are therefore zeroed when no row sees them, and when some
+// rows do, non-finite ones are zeroed and the segment is marked; its epilogue
+// then adds the non-finite elements of a row's own keys to that row.
+//
+// Roundings below 32 bits: P to the query's 16-bit type (the tensor cores
+// take 16-bit operands; an error of half a step of each probability, the
+// size of the output's own rounding), and the output.  With f16, P is scaled
+// by 2^6 so that small probabilities stay above f16's subnormals; the
+// running maximum is moved only when exceeded by 2^8 (O is then rescaled in
+// tensor memory), which keeps P below 2^14.
+#pragma once
+
+#include "fd_prompt.cuh"
+#include "fd_tcgen05.cuh"
+
+namespace fd {
+namespace pf {
+
+using mma::mbar_arrive;
+using mma::mbar_arrive_tx;
+using mma::mbar_init;
+using mma::mbar_try_wait;
+using mma::mbar_wait;
+using mma::smem_u32;
+using namespace tc;
+
+constexpr int kTile = 128;          // keys per tile
+constexpr int kRowsTile = 128;      // rows of a query tile
+constexpr int kRowsPair = 2 * kRowsTile;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
+constexpr int kPages = 32;          // block-table entries staged at a time
+constexpr int kMaxSlots = 8, kMaxRaw = 4;
+// Cost of a segment start (Q load, first product, epilogue), in keys of one
+// query tile.
+constexpr long long kStartCost = 640;
+
+// ---------------------------------------------------------------------------
+// Streams and their split
+// ---------------------------------------------------------------------------
+struct Seq {
+  int b, q0, n, T, ctx, pairs, span;   // span: tokens of a pair
+  long long head;                      // cost of one KV head
+};
+
+// Keys that the last token of pair m sees.
+__device__ __forceinline__ int pair_end(const Seq& s, int m) {
+  const long long t = (long long)(m + 1) * s.span;
+  const int e = s.ctx + (t < s.n ? (int)t : s.n);
+  return e > 0 ? e : 0;
+}
+
+__device__ __forceinline__ int pair_weight(const Seq& s, int m) {
+  return (long long)m * s.span + s.span / 2 < s.n ? 2 : 1;
+}
+
+__device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
+  return kStartCost + (long long)pair_weight(s, m) * pair_end(s, m);
+}
+
+// Cost of pairs 0 .. m - 1 (m < pairs: all of them have both query tiles).
+__device__ __forceinline__ long long pairs_before(const Seq& s, int m) {
+  long long c = (long long)m * kStartCost;
+  long long m0 = s.ctx >= 0 ? 0 : (-(long long)s.ctx) / s.span;   // pairs without keys
+  if (m > m0) {
+    const long long mm = m;
+    c += 2 * ((mm - m0) * s.ctx + (long long)s.span * ((mm * (mm + 1) - m0 * (m0 + 1)) / 2));
+  }
+  return c;
+}
+
+__device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
+  Seq s;
+  s.b = b;
+  const int lo = __ldg(p.q_start + b), hi = __ldg(p.q_start + b + 1);
+  s.T = max(0, __ldg(p.seq_len + b));
+  s.q0 = lo;
+  s.n = hi - lo;
+  if (lo < 0 || hi < lo || hi > p.tokens) {
+    if (report) raise_error(p.at.ws, kErrBounds, lo < 0 ? lo : hi);
+    s.n = 0;
+  }
+  s.ctx = s.T - s.n;
+  s.span = 2 * p.tile_tokens;
+  s.pairs = (int)(((long long)s.n + s.span - 1) / s.span);
+  s.head = s.n > 0 ? pairs_before(s, s.pairs - 1) + pair_cost(s, s.pairs - 1) : 0;
+  return s;
+}
+
+struct Plan {
+  long long total, per_cta;   // cost, and cost per CTA
+  long long first;            // cost before sequence b
+  int b;                      // sequence holding this CTA's first unit
+};
+
+// Every thread of the CTA gets the plan; `red` is 34 long longs of shared memory.
+__device__ inline Plan make_plan(const Prefill& p, long long* red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int B = p.at.batch;
+  long long mine = 0, v0 = 0;
+  for (int b = tid; b < B; b += blockDim.x) {
+    const long long v = load_seq(p, b, blockIdx.x == 0).head * p.num_kv_heads;
+    if (b == tid) v0 = v;
+    mine += v;
+  }
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) red[warp] = mine;
+  __syncthreads();
+  Plan r;
+  r.total = 0;
+  for (int w = 0; w < nw; ++w) r.total += red[w];
+  // every CTA but the last takes at least one tile of two query tiles, so a
+  // range inside a stream always holds a tile
+  r.per_cta = (r.total + p.grid - 1) / p.grid;
+  if (r.per_cta < 2 * kTile) r.per_cta = 2 * kTile;
+  const long long target = (long long)blockIdx.x * r.per_cta;
+  __syncthreads();
+  if (tid == 0) {
+    red[32] = B;
+    red[33] = r.total;
+  }
+  long long carry = 0;
+  for (int base = 0; base < B; base += blockDim.x) {
+    const int b = base + tid;
+    const long long v = b >= B ? 0 : base == 0 ? v0 : load_seq(p, b, false).head * p.num_kv_heads;
+    long long x = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    long long before = carry, all = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += red[w];
+      all += red[w];
+    }
+    const long long excl = before + x - v;
+    if (v > 0 && excl <= target && target < excl + v) {
+      red[32] = b;
+      red[33] = excl;
+    }
+    carry += all;
+    __syncthreads();
+  }
+  r.b = (int)red[32];
+  r.first = red[33];
+  fence_async_smem();   // `red` lies where the first Q tile lands
+  __syncthreads();
+  return r;
+}
+
+struct Seg {
+  int b, q0, n, ctx, h, m;   // sequence (first packed token, tokens, cached before), KV head, pair
+  int tb, te;                // tiles [tb, te) of the pair's stream
+  int end;                   // keys of the stream
+  int nt[2];                 // tiles of query tile A, B in the stream (0: no rows or no keys)
+  bool complete;             // the whole stream
+  int slot;                  // partial slot otherwise
+};
+
+// The segments of this CTA, in order; every role walks its own copy.
+struct Walk {
+  long long g, g_end, ps;
+  Seq s;
+  int h, m;
+
+  __device__ void init(const Prefill& p, const Plan& pl) {
+    g = (long long)blockIdx.x * pl.per_cta;
+    g_end = min(g + pl.per_cta, pl.total);
+    ps = g_end;
+    if (g >= pl.total || pl.b >= p.at.batch) return;
+    s = load_seq(p, pl.b, false);
+    const long long off = g - pl.first;
+    h = (int)(off / s.head);
+    const long long r = off - h * s.head;
+    int lo = 0, hi = s.pairs;   // the last pair that begins at or before r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pairs_before(s, mid) <= r) lo = mid;
+      else hi = mid;
+    }
+    m = lo;
+    ps = pl.first + h * s.head + pairs_before(s, m);
+  }
+
+  __device__ __forceinline__ bool next(const Prefill& p, Seg& o) {
+    while (ps < g_end) {
+      const int w = pair_weight(s, m), end = pair_end(s, m);
+      const long long cost = kStartCost + (long long)w * end;
+      const int n = (end + kTile - 1) / kTile;
+      const long long a = g > ps ? g : ps, e = ps + cost < g_end ? ps + cost : g_end;
+      // tile i stands at ps + kStartCost + i * unit and belongs to the range
+      // that holds this point
+      const long long unit = (long long)w * kTile;
+      const long long xa = a - ps - kStartCost, xe = e - ps - kStartCost;
+      const int tb = xa <= 0 ? 0 : (int)min((long long)n, (xa + unit - 1) / unit);
+      const int te = xe <= 0 ? 0 : (int)min((long long)n, (xe + unit - 1) / unit);
+      const bool yields = n > 0 ? te > tb : g <= ps;
+      if (yields) {
+        o.b = s.b;
+        o.q0 = s.q0;
+        o.n = s.n;
+        o.ctx = s.ctx;
+        o.h = h;
+        o.m = m;
+        o.tb = tb;
+        o.te = te;
+        o.end = end;
+        const int half = s.span >> 1;
+        const int ea = s.ctx + min((long long)s.n, (long long)m * s.span + half);
+        o.nt[0] = ea > 0 ? (ea + kTile - 1) / kTile : 0;
+        o.nt[1] = w == 2 ? n : 0;
+        o.complete = tb == 0 && te == n;
+        o.slot = 2 * (int)blockIdx.x + (tb > 0 ? 0 : 1);
+      }
+      ps += cost;
+      if (++m == s.pairs) {
+        m = 0;
+        if (++h == p.num_kv_heads) {
+          h = 0;
+          int b = s.b + 1;
+          for (; ps < g_end && b < p.at.batch; ++b) {
+            s = load_seq(p, b, false);
+            if (s.n > 0) break;
+          }
+        }
+      }
+      if (yields) return true;
+    }
+    return false;
+  }
+};
+
+// First key of the stream that some row of the pair does not see.
+__device__ __forceinline__ int first_unseen(const Seg& s, int span) {
+  const long long t = (long long)s.ctx + (long long)s.m * span + 1;
+  return t > 0 ? (int)t : 0;
+}
+
+// ---------------------------------------------------------------------------
+// Shape and shared memory
+// ---------------------------------------------------------------------------
+// KV: 0 16-bit cache in the query's type, 1 e4m3, 2 int8.  CONV: the
+// converter warps fill the ring.
+template <int D, int KV, bool CONV>
+struct Shape {
+  static constexpr int kThreads = CONV ? 512 : 384;
+  static constexpr uint32_t kQTile = kRowsTile * D * 2u;
+  static constexpr uint32_t kSlot = kTile * D * 2u;
+  static constexpr uint32_t kRaw = KV == 0 ? 0u : kTile * D * 1u;
+  static constexpr int kSlots = D == 128 ? (CONV ? 4 : 5) : (CONV ? 6 : 8);
+  static constexpr int kRawSlots = KV == 0 ? 0 : D == 128 ? 2 : 4;
+  static constexpr uint32_t kOffSlot = 2u * kQTile;
+  static constexpr uint32_t kOffRaw = kOffSlot + kSlots * kSlot;
+  static constexpr uint32_t kOffCtl = kOffRaw + kRawSlots * kRaw;
+};
+
+struct Control {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t fixed[4];   // V tiles repaired (no converters), or V scales written (converters)
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fin;
+  int tbad[8];      // tile j (slot j mod 8) holds a row outside the cache
+  int nf[8];        // segment i (slot i mod 8) + 1 when its V held masked non-finite elements
+  int abort_flag;
+  uint32_t tmem_base;
+  int pages[kPages];
+};
+
+constexpr uint32_t kCtlBytes = (sizeof(Control) + 15) / 16 * 16;
+
+// Per-token scales of a tile's 128 keys: rings of kKeyRing K arrays, then
+// kValRing V arrays.  Both are written when the converters fill the tile's
+// operand slot.  A K slot is free once S of both query tiles is done, but its
+// scales are read after S, by a softmax that is done once the next S of its
+// query tile is: one array more than the slots hold.
+template <int D, int KV>
+struct ScaleRing {
+  static constexpr int kKeyRing = Shape<D, KV, true>::kSlots / 2 + 1;
+  static constexpr int kValRing = Shape<D, KV, true>::kSlots / 2;
+  static constexpr uint32_t kBytes = (kKeyRing + kValRing) * kTile * 4u;
+  static __device__ __forceinline__ int key(int n) { return (n % kKeyRing) * kTile; }
+  static __device__ __forceinline__ int val(int n) { return (kKeyRing + n % kValRing) * kTile; }
+};
+
+template <int D, int KV, bool CONV, bool TOK>
+constexpr uint32_t smem_bytes() {
+  return Shape<D, KV, CONV>::kOffCtl + kCtlBytes + (TOK ? ScaleRing<D, KV>::kBytes : 0u);
+}
+static_assert(smem_bytes<128, 1, true, true>() <= 227u * 1024u, "shared memory");
+static_assert(smem_bytes<128, 0, false, false>() <= 227u * 1024u, "shared memory");
+
+__device__ __forceinline__ bool aborted(const Control& c) {
+  return *(volatile const int*)&c.abort_flag != 0;
+}
+
+__device__ __forceinline__ void record_abort(Control& c, const Prefill& p, int role) {
+  if (!aborted(c)) {
+    raise_error(p.at.ws, kErrTimeout, role);
+    *(volatile int*)&c.abort_flag = 1;
+  }
+}
+
+__device__ __forceinline__ bool wait_slow(Control& c, const Prefill& p, uint64_t* bar,
+                                       uint32_t parity, int role) {
+  if (aborted(c)) return false;
+  if (mbar_wait(bar, parity, p.wait_ns)) return true;
+  record_abort(c, p, role);
+  return false;
+}
+
+// A bounded wait; on expiry the timeout is recorded and the CTA aborts.
+__device__ __forceinline__ bool wait_for(Control& c, const Prefill& p, uint64_t* bar,
+                                         uint32_t parity, int role) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(c, p, bar, parity, role);
+}
+
+// The same by a whole warp, whose lanes all get one answer.
+__device__ __forceinline__ bool wait_warp(Control& c, const Prefill& p, uint64_t* bar,
+                                          uint32_t parity, int role) {
+  return __all_sync(0xffffffffu, wait_for(c, p, bar, parity, role));
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---------------------------------------------------------------------------
+// Packed fp32 pairs
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Non-finite 16-bit elements of a word zeroed; true if there was one.
+template <bool BF16>
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  const bool lo = (w & e) == e, hi = (w & (e << 16)) == (e << 16);
+  if (lo) w &= 0xFFFF0000u;
+  if (hi) w &= 0x0000FFFFu;
+  return lo || hi;
+}
+
+// NaN codes of an e4m3 word (S.1111.111) zeroed; true if there was one.
+__device__ __forceinline__ bool drop_nan_e4m3(uint32_t& w) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7Fu) == 0x7Fu) {
+      w &= ~(0xFFu << (8 * i));
+      any = true;
+    }
+  return any;
+}
+
+// ---------------------------------------------------------------------------
+// Producer warp
+// ---------------------------------------------------------------------------
+// One K or V tile by TMA into `dst` (16-bit: D / 64 blocks of 128-byte rows;
+// 8-bit: rows of D bytes): the boxes of the tile's rows below `end`.
+template <int D, int KV>
+struct TileCopy {
+  static constexpr int kRowBytes = KV == 0 || D == 128 ? 128 : 64;   // of a box
+  static constexpr int kBlocks = KV == 0 ? D / 64 : 1;
+  static constexpr int kBoxElems = KV == 0 ? 64 : D;
+};
+
+template <int D, int KV, bool CONV>
+__device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Control& c,
+                                         uint8_t* base, const CUtensorMap* tmq,
+                                         const CUtensorMap* tmk, const CUtensorMap* tmv) {
+  using SH = Shape<D, KV, CONV>;
+  using TC = TileCopy<D, KV>;
+  const int lane = threadIdx.x & 31;
+  // the ring that TMA fills: the operand ring, or the converters' raw ring
+  constexpr int NS = KV == 0 ? SH::kSlots : SH::kRawSlots;
+  uint64_t* full = KV == 0 ? c.full : c.raw_full;
+  uint64_t* empty = KV == 0 ? c.empty : c.raw_empty;
+  uint8_t* ring = base + (KV == 0 ? SH::kOffSlot : SH::kOffRaw);
+  constexpr uint32_t kSlot = KV == 0 ? SH::kSlot : SH::kRaw;
+  const bool tiles = !p.gather;   // gathered rows are the converters' business
+  uint64_t keep;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+  Walk walk;
+  walk.init(p, plan);
+  Seg seg;
+  int n = 0, qn[2] = {0, 0};
+  bool stop = p.starve != 0;
+  const int box_rows = p.at.block_table && p.at.page_size < kTile ? p.at.page_size : kTile;
+  while (!stop && walk.next(p, seg)) {
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (stop || seg.tb >= min(seg.te, seg.nt[x])) continue;
+        if (!wait_for(c, p, &c.q_empty[x], (uint32_t)((qn[x] & 1) ^ 1), 1)) {
+          stop = true;
+          continue;
+        }
+        const uint32_t rows = (uint32_t)(p.tile_tokens * p.group);
+        mbar_arrive_tx(&c.q_full[x], rows * D * 2u);
+        const int tok = seg.q0 + (2 * seg.m + x) * p.tile_tokens;
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+          mma::tma_load_3d_hint(base + x * SH::kQTile + d * (kRowsTile * 128), tmq, 64 * d,
+                                seg.h * p.group, tok, &c.q_full[x], keep);
+        ++qn[x];
+      }
+    }
+    stop = __shfl_sync(0xffffffffu, stop, 0);
+    if (!tiles || stop) continue;
+    const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
+    int win_lo = 0, win_hi = 0;
+    for (int j = seg.tb; j < seg.te; ++j, ++n) {
+      const int t0 = j * kTile;
+      const int valid = min(kTile, seg.end - t0);
+      const int nbox = (valid + box_rows - 1) / box_rows;
+      if (p.at.block_table) {
+        const int lo = t0 >> p.at.page_shift, hi = ((t0 + valid - 1) >> p.at.page_shift) + 1;
+        if (lo < win_lo || hi > win_hi) {
+          const int last = ((seg.end - 1) >> p.at.page_shift) + 1;
+          win_lo = lo;
+          win_hi = min(lo + kPages, last);
+          __syncwarp();
+          for (int k = lane; k < win_hi - win_lo; k += 32)
+            c.pages[k] = win_lo + k < p.at.bt_stride
+                             ? __ldg(p.at.block_table + (long long)seg.b * p.at.bt_stride + win_lo + k)
+                             : -1;
+          __syncwarp();
+        }
+      }
+      // one box per lane (at most 16): its row, and whether it lies in the cache
+      long long row = 0;
+      bool ok = true;
+      if (lane < nbox) {
+        const int t = t0 + lane * box_rows;
+        const int nval = min(box_rows, valid - lane * box_rows);
+        if (p.at.block_table) {
+          const int page = c.pages[(t >> p.at.page_shift) - win_lo];
+          row = ((long long)page << p.at.page_shift) + (t & (p.at.page_size - 1));
+          ok = page >= 0 && row + nval <= p.at.kv_rows;
+          if (!ok) raise_error(p.at.ws, kErrBounds, page);
+        } else {
+          row = start + t;
+          ok = row >= 0 && row + nval <= p.at.kv_rows;
+          if (!ok) raise_error(p.at.ws, kErrBounds, row < 0 ? row : row + nval - 1);
+        }
+      }
+      const bool bad = __any_sync(0xffffffffu, !ok);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = 2 * n + kv, slot = e % NS;
+        if (!wait_warp(c, p, &empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 2)) {
+          stop = true;
+          break;
+        }
+        uint8_t* dst = ring + (size_t)slot * kSlot;
+        if (bad) {
+          // a row outside the cache: the tile counts as absent (all scores
+          // excluded), its operands only have to be finite
+          for (uint32_t o = lane * 16; o < kSlot; o += 512)
+            *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          if (lane == 0 && kv == 0) c.tbad[n & 7] = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+          continue;
+        }
+        if (lane == 0) {
+          if (kv == 0) c.tbad[n & 7] = 0;
+          mbar_arrive_tx(&full[slot], (uint32_t)nbox * box_rows * TC::kRowBytes * TC::kBlocks);
+        }
+        __syncwarp();
+        if (lane < nbox) {
+#pragma unroll
+          for (int d = 0; d < TC::kBlocks; ++d)
+            mma::tma_load_3d_hint(dst + d * (kTile * TC::kRowBytes) +
+                                      (size_t)lane * box_rows * TC::kRowBytes,
+                                  kv ? tmv : tmk, d * TC::kBoxElems, seg.h, (int)row, &full[slot],
+                                  keep);
+        }
+      }
+      if (stop) break;
+    }
+    stop = __any_sync(0xffffffffu, stop);
+  }
+  if (stop && !p.starve) {
+    // copies in flight must land before the CTA ends
+    if (lane == 0) {
+      bool late = false;
+      if (tiles)
+        for (int e = max(0, 2 * n - NS); e < 2 * n; ++e)
+          late |= !mbar_wait(&full[e % NS], (uint32_t)((e / NS) & 1), mma::kDrainNs);
+      for (int x = 0; x < 2; ++x)
+        if (qn[x] > 0)
+          late |= !mbar_wait(&c.q_full[x], (uint32_t)((qn[x] - 1) & 1), mma::kDrainNs);
+      if (late) raise_error(p.at.ws, kErrDrain, 3);
+    }
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// MMA warp
+// ---------------------------------------------------------------------------
+// Progress of one query tile: its products alternate S, P V over its tiles.
+struct Issue {
+  Walk walk;
+  Seg seg;
+  bool have, pv;      // pv: the P V product of tile j is next
+  int j, n;           // tile of the stream, tile of the CTA
+  int done, segs;     // tiles and segments of this query tile so far
+  int fixes;          // repaired V tiles passed so far
+};
+
+template <int D, int KV, bool CONV, bool BF16>
+struct Mma {
+  using SH = Shape<D, KV, CONV>;
+  const Prefill& p;
+  Control& c;
+  uint32_t tbase;
+  uint64_t dq, dk, dv;   // operands at the start of Q and of the ring
+  static constexpr int NS = SH::kSlots;
+
+  __device__ __forceinline__ void advance(Issue& s) {
+    ++s.n;
+    if (++s.j >= s.seg.te) {
+      do {   // segments without tiles hold nothing for the tensor cores
+        s.have = s.walk.next(p, s.seg);
+      } while (s.have && s.seg.tb >= s.seg.te);
+      s.j = s.have ? s.seg.tb : 0;
+    }
+  }
+
+  // Issues the next product of query tile X if its inputs are there.
+  template <int X>
+  __device__ __forceinline__ bool step(Issue& s) {
+    constexpr uint32_t id_s = idesc_f16(kRowsTile, kTile, 0, BF16 ? 1 : 0);
+    constexpr uint32_t id_o = idesc_f16(kRowsTile, D, 1, BF16 ? 1 : 0);
+    const int ek = 2 * s.n, ev = ek + 1;
+    const int sk = ek % NS, sv = ev % NS;
+    const uint32_t pk = (uint32_t)((ek / NS) & 1), pv = (uint32_t)((ev / NS) & 1);
+    const int nt = min(s.seg.te, s.seg.nt[X]);
+    if (s.j >= nt) {   // no rows of this query tile see the tile
+      if (!mbar_test(&c.full[sk], pk) || !mbar_test(&c.full[sv], pv)) return false;
+      if (!CONV && needs_fix(s)) ++s.fixes;
+      mbar_arrive(&c.empty[sk]);
+      mbar_arrive(&c.empty[sv]);
+      advance(s);
+      return true;
+    }
+    const uint32_t tS = tbase + X * kTile, tO = tbase + 2 * kTile + X * kTile;
+    if (!s.pv) {
+      if (s.j == s.seg.tb && !mbar_test(&c.q_full[X], (uint32_t)(s.segs & 1))) return false;
+      if (!mbar_test(&c.full[sk], pk)) return false;
+      tc_fence_after();
+      const uint64_t a = dq + ((X * SH::kQTile) >> 4);
+      const uint64_t b = dk + (((uint32_t)sk * SH::kSlot) >> 4);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+        umma(tS, a + off, b + off, id_s, ks > 0);
+      }
+      umma_commit(&c.s_full[X]);
+      umma_commit(&c.empty[sk]);
+      if (s.j + 1 == nt) umma_commit(&c.q_empty[X]);
+      s.pv = true;
+      return true;
+    }
+    if (!mbar_test(&c.p_full[X], (uint32_t)(s.done & 1))) return false;
+    const bool fix = !CONV && needs_fix(s);
+    if (fix ? !mbar_test(&c.fixed[s.fixes & 3], (uint32_t)((s.fixes >> 2) & 1))
+            : !mbar_test(&c.full[sv], pv))
+      return false;
+    tc_fence_after();
+    const uint64_t b = dv + (((uint32_t)sv * SH::kSlot) >> 4);
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+      umma_ts(tO, tS + ks * 8, b + ((ks * 2048) >> 4), id_o, !(s.j == s.seg.tb && ks == 0));
+    umma_commit(&c.empty[sv]);
+    if (s.j + 1 == nt) {
+      umma_commit(&c.o_full[X]);
+      ++s.segs;
+    }
+    if (fix) ++s.fixes;
+    ++s.done;
+    s.pv = false;
+    advance(s);
+    return true;
+  }
+
+  __device__ __forceinline__ bool needs_fix(const Issue& s) const {
+    return (s.j + 1) * kTile > first_unseen(s.seg, 2 * p.tile_tokens);
+  }
+
+  __device__ __forceinline__ void run(const Plan& plan) {
+    Issue a;
+    a.walk.init(p, plan);
+    a.pv = false;
+    a.n = a.done = a.segs = a.fixes = 0;
+    do {
+      a.have = a.walk.next(p, a.seg);
+    } while (a.have && a.seg.tb >= a.seg.te);
+    a.j = a.have ? a.seg.tb : 0;
+    Issue b = a;
+    unsigned long long since = 0;
+    uint32_t spins = 0;
+    while (a.have || b.have) {
+      bool moved = false;
+      if (a.have) moved |= step<0>(a);
+      if (b.have) moved |= step<1>(b);
+      if (moved) {
+        spins = 0;
+      } else if ((++spins & 1023u) == 0) {
+        const unsigned long long now = mma::global_ns();
+        if (spins == 1024) since = now;
+        if (aborted(c)) break;
+        if (now - since > p.wait_ns) {
+          record_abort(c, p, 7);
+          break;
+        }
+      }
+    }
+    // every issued product is done before the tensor memory is freed
+    umma_commit(&c.fin);
+    if (!mbar_wait(&c.fin, 0, mma::kDrainNs)) raise_error(p.at.ws, kErrDrain, 10);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Repair of V tiles in the ring (16-bit caches by TMA)
+// ---------------------------------------------------------------------------
+template <int D, bool BF16>
+__device__ __forceinline__ void fixers(const Prefill& p, const Plan& plan, Control& c,
+                                       uint8_t* base) {
+  using SH = Shape<D, 0, false>;
+  constexpr int NS = SH::kSlots;
+  const int lane = threadIdx.x & 31, ft = threadIdx.x - kFixWarp0 * 32;
+  Walk walk;
+  walk.init(p, plan);
+  Seg seg;
+  int n = 0, fixes = 0, sn = 0;
+  for (; walk.next(p, seg); ++sn) {
+    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    for (int j = seg.tb; j < seg.te; ++j, ++n) {
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = 2 * n + kv, slot = e % NS;
+        if (!wait_warp(c, p, &c.full[slot], (uint32_t)((e / NS) & 1), 20)) return;
+        if (kv == 1 && (j + 1) * kTile > unseen) {
+          const int valid = min(kTile, seg.end - j * kTile);
+          const int from = max(0, unseen - j * kTile);   // rows before it are seen by all
+          uint8_t* v = base + SH::kOffSlot + (size_t)slot * SH::kSlot;
+          bool found = false;
+          const int items = (kTile - from) * 8;
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d) {
+#pragma unroll 4
+            for (int i = ft; i < items; i += 64) {
+              const int r = from + (i >> 3);
+              uint4* at = reinterpret_cast<uint4*>(v + d * (kTile * 128) + r * 128 + (i & 7) * 16);
+              if (r >= valid) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 w = *at;
+                bool hit = drop_nonfinite<BF16>(w.x);
+                hit |= drop_nonfinite<BF16>(w.y);
+                hit |= drop_nonfinite<BF16>(w.z);
+                hit |= drop_nonfinite<BF16>(w.w);
+                if (hit) {
+                  *at = w;
+                  found = true;
+                }
+              }
+            }
+          }
+          if (found) *(volatile int*)&c.nf[sn & 7] = sn + 1;
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.fixed[fixes & 3]);
+          ++fixes;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.empty[slot]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Converter warps: thread = key of the tile
+// ---------------------------------------------------------------------------
+template <int D, int KV, bool BF16, bool TOK>
+__device__ __forceinline__ void converters(const Prefill& p, const Plan& plan, Control& c,
+                                           uint8_t* base, float* scales) {
+  using SH = Shape<D, KV, true>;
+  constexpr int NS = SH::kSlots;
+  constexpr int NR = SH::kRawSlots > 0 ? SH::kRawSlots : 1;
+  constexpr int kChunks = KV == 0 ? D / 8 : D / 16;   // 16-byte chunks of a cache row
+  const int lane = threadIdx.x & 31, t = threadIdx.x - kConvWarp0 * 32;
+  const uint32_t ring = smem_u32(base) + SH::kOffSlot, raw = smem_u32(base) + SH::kOffRaw;
+  using SR = ScaleRing<D, KV>;
+  // key of tile j that this thread carries: its cache row (unchecked), or -1
+  // behind the stream's last key; in two steps so that loads can run ahead
+  auto page_of = [&](const Seg& g, int j) -> int {
+    const int k = j * kTile + t;
+    if (j >= g.te || k >= g.end) return -1;
+    if (!p.at.block_table) return 0;
+    const int col = k >> p.at.page_shift;
+    return col < p.at.bt_stride
+               ? __ldg(p.at.block_table + (long long)g.b * p.at.bt_stride + col)
+               : -1;
+  };
+  auto row_of = [&](const Seg& g, int j, int page, long long start) -> long long {
+    const int k = j * kTile + t;
+    if (page < 0) return -1;
+    const long long row = p.at.block_table ? ((long long)page << p.at.page_shift) +
+                                                 (k & (p.at.page_size - 1))
+                                           : start + k;
+    return row >= 0 && row < p.at.kv_rows ? row : -1;
+  };
+  Walk walk;
+  walk.init(p, plan);
+  Seg seg;
+  int n = 0, sn = 0;
+  for (; walk.next(p, seg); ++sn) {
+    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
+    // per-token scales run one tile ahead, their block-table entries two
+    float ks1 = 0.f, vs1 = 0.f;
+    int page2 = -1;
+    auto load_scales = [&](int j, int page) {
+      const long long row = row_of(seg, j, page, start);
+      ks1 = vs1 = 0.f;
+      if (row >= 0) {
+        ks1 = __ldg(p.k_scales + row * p.num_kv_heads + seg.h);
+        vs1 = __ldg(p.v_scales + row * p.num_kv_heads + seg.h);
+      }
+    };
+    if constexpr (TOK) {
+      load_scales(seg.tb, page_of(seg, seg.tb));
+      page2 = page_of(seg, seg.tb + 1);
+    }
+    for (int j = seg.tb; j < seg.te; ++j, ++n) {
+      const int valid = min(kTile, seg.end - j * kTile);
+      float ks = 0.f, vs = 0.f;
+      if constexpr (TOK) {
+        ks = ks1 * p.score_scale;
+        vs = vs1;
+        load_scales(j + 1, page2);
+        page2 = page_of(seg, j + 2);
+      }
+      long long row = -1;
+      int bad = 0;
+      if (p.gather) {
+        // a row outside the cache: the tile counts as absent; every warp looks
+        // at all 128 rows and so comes to the same answer
+        bool wrong = false;
+        for (int k = lane; k < valid; k += 32)
+          wrong |= placed_row(p.at, seg.b, j * kTile + k) < 0;
+        bad = __any_sync(0xffffffffu, wrong) ? 1 : 0;
+        if (t < valid) row = placed_row(p.at, seg.b, j * kTile + t);
+        if (t == 0) c.tbad[n & 7] = bad;
+      }
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = 2 * n + kv, slot = e % NS, rs = e % NR;
+        const uint32_t dst = ring + (uint32_t)slot * SH::kSlot;
+        uint4 w[kChunks];
+        if (p.gather) {
+          const uint8_t* src = static_cast<const uint8_t*>(kv ? p.v : p.k) +
+                               (row * p.num_kv_heads + seg.h) * (long long)(kChunks * 16);
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+            w[i] = row >= 0 && !bad ? __ldg(reinterpret_cast<const uint4*>(src) + i)
+                                    : make_uint4(0, 0, 0, 0);
+        } else if constexpr (KV != 0) {
+          if (!wait_warp(c, p, &c.raw_full[rs], (uint32_t)((e / NR) & 1), 21)) return;
+          const uint32_t src = raw + (uint32_t)rs * SH::kRaw + (uint32_t)t * D;
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int swz = D == 128 ? i ^ (t & 7) : i ^ ((t >> 1) & 3);
+            w[i] = lds128(src + (uint32_t)swz * 16);
+          }
+        }
+        // V rows that some query row does not see (see the file comment)
+        if (kv == 1 && (j + 1) * kTile > unseen && j * kTile + t >= unseen) {
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            if (t >= valid) {
+              w[i] = make_uint4(0, 0, 0, 0);
+            } else if constexpr (KV == 0) {
+              found |= drop_nonfinite<BF16>(w[i].x);
+              found |= drop_nonfinite<BF16>(w[i].y);
+              found |= drop_nonfinite<BF16>(w[i].z);
+              found |= drop_nonfinite<BF16>(w[i].w);
+            } else if constexpr (KV == 1) {
+              found |= drop_nan_e4m3(w[i].x);
+              found |= drop_nan_e4m3(w[i].y);
+              found |= drop_nan_e4m3(w[i].z);
+              found |= drop_nan_e4m3(w[i].w);
+            }
+          }
+          if (found) *(volatile int*)&c.nf[sn & 7] = sn + 1;
+        }
+        if (!wait_warp(c, p, &c.empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 22)) return;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          if constexpr (KV == 0) {
+            sts128(dst + kmajor_chunk(kTile, t, i), w[i]);
+          } else {
+            constexpr int KVT = KV == 1 ? FD_E4M3 : FD_I8;
+            const uint2 a = mma::widen8x4<KVT, BF16>(w[i].x), b = mma::widen8x4<KVT, BF16>(w[i].y);
+            const uint2 d = mma::widen8x4<KVT, BF16>(w[i].z), f = mma::widen8x4<KVT, BF16>(w[i].w);
+            sts128(dst + kmajor_chunk(kTile, t, 2 * i), make_uint4(a.x, a.y, b.x, b.y));
+            sts128(dst + kmajor_chunk(kTile, t, 2 * i + 1), make_uint4(d.x, d.y, f.x, f.y));
+          }
+        }
+        if constexpr (TOK) scales[(kv ? SR::val(n) : SR::key(n)) + t] = kv ? vs : ks;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (!p.gather && KV != 0) mbar_arrive(&c.raw_empty[rs]);
+          mbar_arrive(&c.full[slot]);
+          if (TOK && kv == 1) mbar_arrive(&c.fixed[n % SR::kValRing]);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax warps: thread = row of query tile X
+// ---------------------------------------------------------------------------
+// Elements of V that are not finite, in the keys [lo, hi) of a sequence: added
+// to this row's 32 dims from d0 (see the file comment; off every fast path).
+template <int D, int KV, bool BF16>
+__device__ __forceinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int lo, int hi,
+                                           int d0, float* o) {
+  for (int t = lo; t < hi; ++t) {
+    const long long row = placed_row(p.at, seg.b, t);
+    if (row < 0) continue;
+    const long long at = (row * p.num_kv_heads + seg.h) * D + d0;
+    for (int i = 0; i < 32; ++i) {
+      float x;
+      if constexpr (KV == 0) {
+        if constexpr (BF16) x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[at + i]);
+        else x = __half2float(static_cast<const __half*>(p.v)[at + i]);
+      } else {
+        x = (static_cast<const uint8_t*>(p.v)[at + i] & 0x7F) == 0x7F ? NAN : 0.f;
+      }
+      if (!isfinite(x)) o[i] += x;
+    }
+  }
+}
+
+template <int D, int KV, bool CONV, bool BF16, bool TOK>
+__device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Control& c, int X,
+                                        uint32_t tbase, const float* scales) {
+  // f16: P carries a factor 2^kLift (see the file comment)
+  constexpr float kLift = BF16 ? 0.f : 6.f;
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
+  const int r = 32 * w4 + lane;
+  const int rows = p.tile_tokens * p.group;
+  const int rtok = r / p.group, rhead = r - rtok * p.group;
+  const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);
+  const uint32_t tS = tl + X * kTile, tO = tl + 2 * kTile + X * kTile;
+  Walk walk;
+  walk.init(p, plan);
+  Seg seg;
+  int n = 0, done = 0, segs = 0, sn = 0;
+  using SR = ScaleRing<D, KV>;
+  // streams of the two partial slots, for the merge
+  int4 used0 = make_int4(-1, 0, 0, 0), used1 = used0;
+  bool dead = false;
+  for (; !dead && walk.next(p, seg); ++sn) {
+    const int tok0 = (2 * seg.m + X) * p.tile_tokens;   // first token of the query tile
+    const int live_rows = min(rows, max(0, (seg.n - tok0) * p.group));
+    const bool mine = r < live_rows;
+    const bool warp_live = 32 * w4 < live_rows;
+    // keys this row sees; a row of nobody never restricts its warp
+    const int lim = mine ? max(0, seg.ctx + tok0 + rtok + 1) : 0x7fffffff;
+    const int te = min(seg.te, X ? seg.nt[1] : seg.nt[0]);
+    float sc = p.score_scale, vsc = p.v_scale;
+    if (KV != 0 && p.scale_kind == FD_SCALE_HEAD) {
+      sc *= __ldg(p.k_scales + seg.h);
+      vsc *= __ldg(p.v_scales + seg.h);
+    }
+    float m_ref = -INFINITY, l = 0.f;
+    int vexp = -1000;   // TOK with f16: P carries 2^-vexp against the V scales
+    for (int j = seg.tb; j < te; ++j, ++done) {
+      const int jn = n + (j - seg.tb);   // tile of the CTA
+      if (!wait_warp(c, p, &c.s_full[X], (uint32_t)(done & 1), 11)) {
+        dead = true;
+        break;
+      }
+      tc_fence_after();
+      if (warp_live) {
+        float s[kTile];
+        {
+          float x[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            tmem_ld32<128>(tS + 32 * k, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * k + i] = x[i];
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) asm volatile("" : "+f"(s[i]));
+        }
+        const bool bad = *(volatile int*)&c.tbad[jn & 7] != 0;
+        const int left = bad ? 0 : max(0, min(kTile, lim - j * kTile));
+        const bool whole = __all_sync(0xffffffffu, left == kTile);
+        const float* vscl = scales + SR::val(jn);
+        if constexpr (TOK) {   // scores in log2 units, token by token
+          const float* ksc = scales + SR::key(jn);   // written before the tile's S was issued
+#pragma unroll
+          for (int i = 0; i < kTile; i += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ksc + i);
+            s[i] *= k4.x;
+            s[i + 1] *= k4.y;
+            s[i + 2] *= k4.z;
+            s[i + 3] *= k4.w;
+          }
+        } else if (sc < 0.f) {   // a negative scale: the maximum of -s is sought
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] = -s[i];
+        }
+        const float scl = TOK ? 1.f : fabsf(sc);
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] = i < left ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kTile; i += 4) {
+          mx[0] = fmaxf(mx[0], s[i]);
+          mx[1] = fmaxf(mx[1], s[i + 1]);
+          mx[2] = fmaxf(mx[2], s[i + 2]);
+          mx[3] = fmaxf(mx[3], s[i + 3]);
+        }
+        const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mt = smax == -INFINITY ? -INFINITY : smax * scl;
+        float fac = 1.f;
+        bool resc = false;
+        if (mt > m_ref + 8.f || m_ref == -INFINITY) {
+          if (m_ref != -INFINITY) {
+            fac = exp2f(m_ref - mt);
+            l *= fac;
+            resc = mine;
+          }
+          m_ref = mt;
+        }
+        float vmul = 1.f;
+        if constexpr (TOK) {
+          if (!wait_warp(c, p, &c.fixed[jn % SR::kValRing], (uint32_t)((jn / SR::kValRing) & 1),
+                         12)) {
+            dead = true;
+            break;
+          }
+          if constexpr (!BF16) {
+            // largest V scale of the tile -> its exponent; P stays below 2^15
+            float vm = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vscl[lane + 32 * i]));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+            int ev = (int)((__float_as_uint(vm) >> 23) & 255u) - 127;
+            ev = max(-120, min(120, ev));
+            if (ev > vexp) {
+              if (j > seg.tb) {
+                fac *= exp2f((float)max(vexp - ev, -200));
+                resc = true;
+              }
+              vexp = ev;
+            }
+            vmul = exp2f((float)-vexp);
+          }
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // the S commit that ended the wait above follows the last P V
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32<128>(tO + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= fac;
+            tmem_st32<128>(tO + c0, o);
+          }
+          tmem_wait_st();
+        }
+        // P = 2^(s - m_ref + kLift); excluded scores are -inf and give 0 (a
+        // row that has seen no key has m_ref = -inf: everything is excluded)
+        const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
+        const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm);
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+        const bool zero_scale = scl == 0.f && !whole;   // 0 * -inf
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int k = 32 * q4 + 2 * i;
+            const float2 x = unpack2(fma2(pack2(s[k], s[k + 1]), sc2, nm2));
+            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+            if (zero_scale) {
+              if (k >= left) p0 = 0.f;
+              if (k + 1 >= left) p1 = 0.f;
+            }
+            sum[i & 3] = add2(sum[i & 3], pack2(p0, p1));
+            if constexpr (TOK) {
+              const float2 v2 = *reinterpret_cast<const float2*>(vscl + k);
+              p0 *= BF16 ? v2.x : v2.x * vmul;
+              p1 *= BF16 ? v2.y : v2.y * vmul;
+            }
+            pk[i] = pack16<BF16>(p0, p1);
+          }
+          tmem_st16u(tS + 16 * q4, pk);
+        }
+        const float2 sa = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += sa.x + sa.y;
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.p_full[X]);
+    }
+    if (dead) break;
+    n += seg.te - seg.tb;
+    // ------------------------------------------------------------ segment end
+    const bool any = seg.tb < te;   // O of this query tile was accumulated
+    if (any) {
+      if (!wait_warp(c, p, &c.o_full[X], (uint32_t)(segs & 1), 15)) {
+        dead = true;
+        break;
+      }
+      ++segs;
+      tc_fence_after();
+    }
+    if (!seg.complete) {
+      if (seg.slot & 1) used1 = make_int4(seg.b, seg.h, seg.m, 0);
+      else used0 = make_int4(seg.b, seg.h, seg.m, 0);
+    }
+    const float m_out = m_ref == -INFINITY ? -INFINITY : m_ref - kLift;
+    float osc = 1.f;
+    if constexpr (TOK && !BF16) osc = vexp > -1000 ? exp2f((float)vexp) : 1.f;
+    if (seg.complete) osc *= l > 0.f ? vsc / l : 0.f;
+    const long long orow = (long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
+                           (long long)seg.h * p.group + rhead;
+    const long long prow = (long long)seg.slot * kRowsPair + X * kRowsTile + r;
+    const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
+    if (warp_live) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float o[32];
+        if (any) {
+          tmem_ld32<128>(tO + c0, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (KV != 2 && nonfinite && mine) {
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = o[i];
+          const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
+          add_nonfinite<D, KV, BF16>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = x[i];
+        }
+        if (!mine) continue;
+        if (seg.complete) {
+          uint16_t* op = static_cast<uint16_t*>(p.out) + orow * D + c0;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(op + i) =
+                make_uint4(pack16<BF16>(o[i] * osc, o[i + 1] * osc),
+                           pack16<BF16>(o[i + 2] * osc, o[i + 3] * osc),
+                           pack16<BF16>(o[i + 4] * osc, o[i + 5] * osc),
+                           pack16<BF16>(o[i + 6] * osc, o[i + 7] * osc));
+        } else {
+          float* pa = p.part_acc + prow * D + c0;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(pa + i) =
+                make_float4(o[i] * osc, o[i + 1] * osc, o[i + 2] * osc, o[i + 3] * osc);
+        }
+      }
+      if (mine) {
+        if (!seg.complete) p.part_ml[prow] = make_float2(m_out, l);
+        else if (p.lse) p.lse[orow] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+    tc_fence_before();
+  }
+  if (X == 0 && r == 0) {
+    // after a timeout nothing is merged: the outputs are undefined
+    if (dead) used0.x = used1.x = -1;
+    p.meta[2 * blockIdx.x] = used0;
+    p.meta[2 * blockIdx.x + 1] = used1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <int D, int KV, bool CONV, bool BF16, bool TOK>
+__global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
+    prefill_kernel(const __grid_constant__ Prefill p, const __grid_constant__ CUtensorMap tmq,
+                   const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv) {
+  using SH = Shape<D, KV, CONV>;
+  extern __shared__ __align__(1024) uint8_t base[];
+  Control& c = *reinterpret_cast<Control*>(base + SH::kOffCtl);
+  float* scales = reinterpret_cast<float*>(base + SH::kOffCtl + kCtlBytes);
+  const int warp = threadIdx.x >> 5;
+  if (smem_u32(base) & 1023u) {   // the swizzled operands need whole atoms
+    if (threadIdx.x == 0) raise_error(p.at.ws, kErrPlan, 0);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SH::kSlots; ++i) {
+      mbar_init(&c.full[i], CONV ? 4 : 1);        // converter warps, or the producer
+      mbar_init(&c.empty[i], CONV ? 2 : 4);       // A, B (and the two repair warps)
+    }
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(&c.raw_full[i], 1);
+      mbar_init(&c.raw_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&c.fixed[i], CONV ? 4 : 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.q_full[i], 1);
+      mbar_init(&c.q_empty[i], 1);
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_full[i], 4);
+      mbar_init(&c.o_full[i], 1);
+    }
+    mbar_init(&c.fin, 1);
+    for (int i = 0; i < 8; ++i) c.tbad[i] = c.nf[i] = 0;
+    c.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&c.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == kProducerWarp * 32) {
+    mma::prefetch_map(&tmq);
+    if (!p.gather) {
+      mma::prefetch_map(&tmk);
+      mma::prefetch_map(&tmv);
+    }
+  }
+  tc_fence_before();
+  const Plan plan = make_plan(p, reinterpret_cast<long long*>(base));   // (barriers)
+  tc_fence_after();
+  const uint32_t tbase = c.tmem_base;
+  allow_dependent_launch();
+
+  // Registers: the softmax threads hold 128 scores each.  The shares add up
+  // to the launch's registers (168 x 384; 128 x 512).
+  if (warp < 8) {
+    reg_inc<CONV ? 176 : 208>();
+    softmax<D, KV, CONV, BF16, TOK>(p, plan, c, warp >> 2, tbase, scales);
+  } else if (warp < kConvWarp0) {
+    reg_dec<CONV ? 64 : 88>();
+    if (warp == kProducerWarp) {
+      producer<D, KV, CONV>(p, plan, c, base, &tmq, &tmk, &tmv);
+    } else if (warp == kMmaWarp) {
+      if ((threadIdx.x & 31) == 0) {
+        const uint32_t ring = smem_u32(base) + SH::kOffSlot;
+        Mma<D, KV, CONV, BF16> mm{p, c, tbase, sdesc(smem_u32(base), 0, 1024),
+                                  sdesc(ring, 0, 1024), sdesc(ring, kTile * 128u, 1024)};
+        mm.run(plan);
+      }
+      __syncwarp();
+    } else if constexpr (!CONV) {
+      fixers<D, BF16>(p, plan, c, base);
+    }
+  } else if constexpr (CONV) {
+    reg_dec<96>();
+    converters<D, KV, BF16, TOK>(p, plan, c, base, scales);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512)
+                 : "memory");
+  }
+}
+
+template <int D, int KV, bool CONV, bool BF16, bool TOK>
+cudaError_t launch_one(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  constexpr uint32_t smem = smem_bytes<D, KV, CONV, TOK>();
+  static std::atomic<unsigned long long> limit_set{0};
+  const auto kern = prefill_kernel<D, KV, CONV, BF16, TOK>;
+  const cudaError_t e = ensure_smem_limit(kern, (int)smem, &limit_set);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)p.grid, Shape<D, KV, CONV>::kThreads, smem, stream>>>(p, maps[0], maps[1],
+                                                                        maps[2]);
+  return cudaGetLastError();
+}
+
+// 16-bit caches: by TMA, or gathered row by row.
+template <int D, bool BF16>
+cudaError_t launch_16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  return p.gather ? launch_one<D, 0, true, BF16, false>(p, maps, stream)
+                  : launch_one<D, 0, false, BF16, false>(p, maps, stream);
+}
+
+// 8-bit caches: with per-token scales or not.
+template <int D, int KV, bool BF16>
+cudaError_t launch_8(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  return p.scale_kind == FD_SCALE_TOKEN ? launch_one<D, KV, true, BF16, true>(p, maps, stream)
+                                        : launch_one<D, KV, true, BF16, false>(p, maps, stream);
+}
+
+// One per translation unit.
+cudaError_t launch_16bit(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+cudaError_t launch_e4m3_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+cudaError_t launch_e4m3_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+cudaError_t launch_i8_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+cudaError_t launch_i8_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+
+}  // namespace pf
+}  // namespace fd

@@ -107,14 +107,23 @@ struct Prefill {
   int q_dtype, kv_dtype;
   unsigned long long wait_ns;
   int starve;
-  int sms;
+  int grid;            // CTAs of the attention kernel
+  int tile_tokens;     // tokens of a 128-row query tile: 128 / group
+  int gather;          // pages too small for TMA boxes: rows copied by threads
+  // workspace: partial states of streams cut between CTAs
+  int4* meta;          // [grid][2]: stream {sequence, KV head, tile pair, rows} of a slot
+  float2* part_ml;     // [grid][2][256]
+  float* part_acc;     // [grid][2][256][head_dim]
 };
 
-size_t prefill_workspace(int head_dim, int sms);
+struct PrefillLayout {
+  size_t meta_off, ml_off, acc_off, total;
+};
+PrefillLayout prefill_layout(int head_dim, int sms);
 
 cudaError_t launch_append_packed(const AppendPacked& p, int sms, cudaStream_t stream);
 cudaError_t launch_read_kv(const ReadKv& p, int sms, cudaStream_t stream);
 cudaError_t launch_rotary_table(const RotaryTable& p, int sms, cudaStream_t stream);
-cudaError_t launch_prefill(const Prefill& p, cudaStream_t stream);
+cudaError_t launch_prefill(Prefill p, void* workspace, cudaStream_t stream);
 
 }  // namespace fd

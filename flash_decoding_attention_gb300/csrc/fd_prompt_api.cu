@@ -241,7 +241,7 @@ fd_status fd_read_kv(const void* k_cache, const void* v_cache, const int32_t* kv
 size_t fd_prefill_workspace_bytes(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const int sms = current_sms();
-  return sms > 0 ? prefill_workspace(head_dim, sms) : 0;
+  return sms > 0 ? prefill_layout(head_dim, sms).total : 0;
 }
 
 fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_cache,
@@ -271,7 +271,7 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
   if (kv_rows >= kMaxPacked) return FD_ERR_UNSUPPORTED;   // 32-bit TMA coordinates
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
-  if (workspace_bytes < prefill_workspace(head_dim, sms)) return FD_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < prefill_layout(head_dim, sms).total) return FD_ERR_WORKSPACE_TOO_SMALL;
   if (num_tokens == 0) return FD_OK;
 
   Prefill p;
@@ -299,9 +299,11 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
   p.q_dtype = q_dtype;
   p.kv_dtype = kv_dtype;
   p.wait_ns = wait_limit_ns();
-  p.sms = sms;
-  return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK
-                                                                                 : FD_ERR_CUDA;
+  p.starve = starve_switch();
+  p.grid = sms;
+  return launch_prefill(p, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FD_OK
+             : FD_ERR_CUDA;
 }
 
 }  // extern "C"
