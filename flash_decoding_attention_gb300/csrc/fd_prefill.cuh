@@ -294,12 +294,24 @@ struct Shape {
   static constexpr uint32_t kOffCtl = kOffRaw + kRawSlots * kRaw;
 };
 
+// A tile's info, written with its K tile: the query tiles that take part, the
+// ends of its segment, and what its rows are.  An entry behind the last tile
+// says stop.
+enum : int {
+  kInfoA = 1, kInfoB = 2,            // query tile A, B has rows that see the tile
+  kInfoLastA = 4, kInfoLastB = 8,    // its last tile of the segment
+  kInfoFirst = 16,                   // first tile of the segment
+  kInfoFix = 32,                     // V is repaired before use (no converters)
+  kInfoBad = 64,                     // a row lies outside the cache: the tile is absent
+  kInfoStop = 128
+};
+
 struct Control {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t fixed[4];   // V tiles repaired (no converters), or V scales written (converters)
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fin;
-  int tbad[8];      // tile j (slot j mod 8) holds a row outside the cache
+  int info[8];      // what the tensor cores do with tile j (slot j mod 8), kInfo bits
   int nf[8];        // segment i (slot i mod 8) + 1 when its V held masked non-finite elements
   int abort_flag;
   uint32_t tmem_base;
@@ -432,6 +444,15 @@ __device__ __forceinline__ bool drop_nan_e4m3(uint32_t& w) {
   return any;
 }
 
+__device__ __forceinline__ int tile_info(const Seg& s, int j, int unseen, bool bad) {
+  int w = bad ? kInfoBad : 0;
+  if (j < s.nt[0]) w |= kInfoA | (j + 1 == min(s.te, s.nt[0]) ? kInfoLastA : 0);
+  if (j < s.nt[1]) w |= kInfoB | (j + 1 == min(s.te, s.nt[1]) ? kInfoLastB : 0);
+  if (j == s.tb) w |= kInfoFirst;
+  if ((j + 1) * kTile > unseen) w |= kInfoFix;
+  return w;
+}
+
 // ---------------------------------------------------------------------------
 // Producer warp
 // ---------------------------------------------------------------------------
@@ -488,6 +509,7 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
     stop = __shfl_sync(0xffffffffu, stop, 0);
     if (!tiles || stop) continue;
     const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
+    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
     int win_lo = 0, win_hi = 0;
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
       const int t0 = j * kTile;
@@ -539,13 +561,13 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
           for (uint32_t o = lane * 16; o < kSlot; o += 512)
             *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
           fence_async_smem();
-          if (lane == 0 && kv == 0) c.tbad[n & 7] = 1;
+          if (lane == 0 && kv == 0) c.info[n & 7] = tile_info(seg, j, unseen, true);
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]);
           continue;
         }
         if (lane == 0) {
-          if (kv == 0) c.tbad[n & 7] = 0;
+          if (kv == 0) c.info[n & 7] = tile_info(seg, j, unseen, false);
           mbar_arrive_tx(&full[slot], (uint32_t)nbox * box_rows * TC::kRowBytes * TC::kBlocks);
         }
         __syncwarp();
@@ -561,6 +583,13 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
       if (stop) break;
     }
     stop = __any_sync(0xffffffffu, stop);
+  }
+  if (!stop && KV == 0 && !CONV) {   // (with converters they write the end)
+    const int e = 2 * n, slot = e % NS;
+    if (wait_warp(c, p, &empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 2) && lane == 0) {
+      c.info[n & 7] = kInfoStop;
+      mbar_arrive(&full[slot]);
+    }
   }
   if (stop && !p.starve) {
     // copies in flight must land before the CTA ends
@@ -581,127 +610,146 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
 // ---------------------------------------------------------------------------
 // MMA warp
 // ---------------------------------------------------------------------------
-// Progress of one query tile: its products alternate S, P V over its tiles.
-struct Issue {
-  Walk walk;
-  Seg seg;
-  bool have, pv;      // pv: the P V product of tile j is next
-  int j, n;           // tile of the stream, tile of the CTA
-  int done, segs;     // tiles and segments of this query tile so far
-  int fixes;          // repaired V tiles passed so far
-};
+// The whole warp walks the tiles, so that the operands' descriptors stay in
+// uniform registers; one elected lane issues.  For tile n, in this order:
+//   P V of A, S of A for tile n + 1, P V of B, S of B for tile n + 1,
+// so the softmax of one query tile has the other's two products to run in.
+// Products of one thread run in issue order, so S may overwrite the P that
+// the P V before it reads.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e;
+}
 
 template <int D, int KV, bool CONV, bool BF16>
 struct Mma {
   using SH = Shape<D, KV, CONV>;
+  static constexpr int NS = SH::kSlots;
   const Prefill& p;
   Control& c;
-  uint32_t tbase;
-  uint64_t dq, dk, dv;   // operands at the start of Q and of the ring
-  static constexpr int NS = SH::kSlots;
+  uint32_t tbase, base, elected;
 
-  __device__ __forceinline__ void advance(Issue& s) {
-    ++s.n;
-    if (++s.j >= s.seg.te) {
-      do {   // segments without tiles hold nothing for the tensor cores
-        s.have = s.walk.next(p, s.seg);
-      } while (s.have && s.seg.tb >= s.seg.te);
-      s.j = s.have ? s.seg.tb : 0;
-    }
-  }
-
-  // Issues the next product of query tile X if its inputs are there.
   template <int X>
-  __device__ __forceinline__ bool step(Issue& s) {
-    constexpr uint32_t id_s = idesc_f16(kRowsTile, kTile, 0, BF16 ? 1 : 0);
-    constexpr uint32_t id_o = idesc_f16(kRowsTile, D, 1, BF16 ? 1 : 0);
-    const int ek = 2 * s.n, ev = ek + 1;
-    const int sk = ek % NS, sv = ev % NS;
-    const uint32_t pk = (uint32_t)((ek / NS) & 1), pv = (uint32_t)((ev / NS) & 1);
-    const int nt = min(s.seg.te, s.seg.nt[X]);
-    if (s.j >= nt) {   // no rows of this query tile see the tile
-      if (!mbar_test(&c.full[sk], pk) || !mbar_test(&c.full[sv], pv)) return false;
-      if (!CONV && needs_fix(s)) ++s.fixes;
-      mbar_arrive(&c.empty[sk]);
-      mbar_arrive(&c.empty[sv]);
-      advance(s);
-      return true;
-    }
-    const uint32_t tS = tbase + X * kTile, tO = tbase + 2 * kTile + X * kTile;
-    if (!s.pv) {
-      if (s.j == s.seg.tb && !mbar_test(&c.q_full[X], (uint32_t)(s.segs & 1))) return false;
-      if (!mbar_test(&c.full[sk], pk)) return false;
-      tc_fence_after();
-      const uint64_t a = dq + ((X * SH::kQTile) >> 4);
-      const uint64_t b = dk + (((uint32_t)sk * SH::kSlot) >> 4);
+  __device__ __forceinline__ void scores(int slot) const {
+    constexpr uint32_t id = idesc_f16(kRowsTile, kTile, 0, BF16 ? 1 : 0);
+    const uint64_t a = sdesc(base + X * SH::kQTile, 0, 1024);
+    const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, 0, 1024);
+    if (elected) {
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-        umma(tS, a + off, b + off, id_s, ks > 0);
+        umma(tbase + X * kTile, a + off, b + off, id, ks > 0);
       }
       umma_commit(&c.s_full[X]);
-      umma_commit(&c.empty[sk]);
-      if (s.j + 1 == nt) umma_commit(&c.q_empty[X]);
-      s.pv = true;
-      return true;
     }
-    if (!mbar_test(&c.p_full[X], (uint32_t)(s.done & 1))) return false;
-    const bool fix = !CONV && needs_fix(s);
-    if (fix ? !mbar_test(&c.fixed[s.fixes & 3], (uint32_t)((s.fixes >> 2) & 1))
-            : !mbar_test(&c.full[sv], pv))
-      return false;
-    tc_fence_after();
-    const uint64_t b = dv + (((uint32_t)sv * SH::kSlot) >> 4);
+  }
+
+  template <int X>
+  __device__ __forceinline__ void values(int slot, int accumulate) const {
+    constexpr uint32_t id = idesc_f16(kRowsTile, D, 1, BF16 ? 1 : 0);
+    const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, kTile * 128u, 1024);
+    if (elected) {
 #pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks)
-      umma_ts(tO, tS + ks * 8, b + ((ks * 2048) >> 4), id_o, !(s.j == s.seg.tb && ks == 0));
-    umma_commit(&c.empty[sv]);
-    if (s.j + 1 == nt) {
-      umma_commit(&c.o_full[X]);
-      ++s.segs;
+      for (int ks = 0; ks < kTile / 16; ++ks)
+        umma_ts(tbase + (2 + X) * kTile, tbase + X * kTile + ks * 8, b + ((ks * 2048) >> 4), id,
+                ks > 0 ? 1 : accumulate);
     }
-    if (fix) ++s.fixes;
-    ++s.done;
-    s.pv = false;
-    advance(s);
-    return true;
   }
 
-  __device__ __forceinline__ bool needs_fix(const Issue& s) const {
-    return (s.j + 1) * kTile > first_unseen(s.seg, 2 * p.tile_tokens);
+  __device__ __forceinline__ void commit(uint64_t* bar) const {
+    if (elected) umma_commit(bar);
   }
 
-  __device__ __forceinline__ void run(const Plan& plan) {
-    Issue a;
-    a.walk.init(p, plan);
-    a.pv = false;
-    a.n = a.done = a.segs = a.fixes = 0;
-    do {
-      a.have = a.walk.next(p, a.seg);
-    } while (a.have && a.seg.tb >= a.seg.te);
-    a.j = a.have ? a.seg.tb : 0;
-    Issue b = a;
-    unsigned long long since = 0;
-    uint32_t spins = 0;
-    while (a.have || b.have) {
-      bool moved = false;
-      if (a.have) moved |= step<0>(a);
-      if (b.have) moved |= step<1>(b);
-      if (moved) {
-        spins = 0;
-      } else if ((++spins & 1023u) == 0) {
-        const unsigned long long now = mma::global_ns();
-        if (spins == 1024) since = now;
-        if (aborted(c)) break;
-        if (now - since > p.wait_ns) {
-          record_abort(c, p, 7);
-          break;
-        }
+  __device__ __forceinline__ void run() {
+    int n = 0, ks = 0, vs = 1, fixes = 0;      // tile, its slots
+    uint32_t kph = 0, vph = 0;                 // their phases
+    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+    bool ok = wait_warp(c, p, &c.full[0], 0, 7);
+    // a value every lane read from shared memory, in a uniform register
+    auto info_of = [&](int i) {
+      return (int)__reduce_or_sync(0xffffffffu, (unsigned)*(volatile int*)&c.info[i & 7]);
+    };
+    int cur = ok ? info_of(0) : kInfoStop;
+    auto first_scores = [&](int info, int slot) {
+      if (info & kInfoA) {
+        ok = ok && wait_warp(c, p, &c.q_full[0], qph[0], 7);
+        qph[0] ^= 1;
+        tc_fence_after();
+        scores<0>(slot);
+        if (info & kInfoLastA) commit(&c.q_empty[0]);
       }
+      if (info & kInfoB) {
+        ok = ok && wait_warp(c, p, &c.q_full[1], qph[1], 7);
+        qph[1] ^= 1;
+        tc_fence_after();
+        scores<1>(slot);
+        if (info & kInfoLastB) commit(&c.q_empty[1]);
+      }
+      commit(&c.empty[slot]);
+    };
+    if (!(cur & kInfoStop)) first_scores(cur, 0);
+    while (ok && !(cur & kInfoStop)) {
+      const int acc = cur & kInfoFirst ? 0 : 1;
+      // V of the tile
+      if (!CONV && (cur & kInfoFix)) {
+        ok = wait_warp(c, p, &c.fixed[fixes & 3], (uint32_t)((fixes >> 2) & 1), 7);
+        ++fixes;
+      } else {
+        ok = wait_warp(c, p, &c.full[vs], vph, 7);
+      }
+      int nks = ks + 2, nvs = vs + 2;
+      uint32_t nkph = kph, nvph = vph;
+      if (nks >= NS) { nks -= NS; nkph ^= 1; }
+      if (nvs >= NS) { nvs -= NS; nvph ^= 1; }
+      if (cur & kInfoA) {
+        ok = ok && wait_warp(c, p, &c.p_full[0], pph[0], 7);
+        if (!ok) break;
+        pph[0] ^= 1;
+        tc_fence_after();
+        values<0>(vs, acc);
+        if (cur & kInfoLastA) commit(&c.o_full[0]);
+      }
+      // the next tile, or the end
+      ok = ok && wait_warp(c, p, &c.full[nks], nkph, 7);
+      if (!ok) break;
+      const int next = info_of(n + 1);
+      const bool follows = !(next & (kInfoFirst | kInfoStop));
+      if (follows && (next & kInfoA)) {
+        tc_fence_after();
+        scores<0>(nks);
+        if (next & kInfoLastA) commit(&c.q_empty[0]);
+      }
+      if (cur & kInfoB) {
+        ok = wait_warp(c, p, &c.p_full[1], pph[1], 7);
+        if (!ok) break;
+        pph[1] ^= 1;
+        tc_fence_after();
+        values<1>(vs, acc);
+        if (cur & kInfoLastB) commit(&c.o_full[1]);
+      }
+      commit(&c.empty[vs]);
+      if (follows) {
+        if (next & kInfoB) {
+          scores<1>(nks);
+          if (next & kInfoLastB) commit(&c.q_empty[1]);
+        }
+        commit(&c.empty[nks]);
+      } else if (!(next & kInfoStop)) {
+        first_scores(next, nks);
+      }
+      cur = next;
+      ++n;
+      ks = nks; vs = nvs; kph = nkph; vph = nvph;
     }
     // every issued product is done before the tensor memory is freed
-    umma_commit(&c.fin);
-    if (!mbar_wait(&c.fin, 0, mma::kDrainNs)) raise_error(p.at.ws, kErrDrain, 10);
+    commit(&c.fin);
+    if (!wait_drain(&c.fin) && elected) raise_error(p.at.ws, kErrDrain, 10);
+  }
+
+  static __device__ __forceinline__ bool wait_drain(uint64_t* bar) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, 0, mma::kDrainNs));
   }
 };
 
@@ -838,7 +886,7 @@ __device__ __forceinline__ void converters(const Prefill& p, const Plan& plan, C
           wrong |= placed_row(p.at, seg.b, j * kTile + k) < 0;
         bad = __any_sync(0xffffffffu, wrong) ? 1 : 0;
         if (t < valid) row = placed_row(p.at, seg.b, j * kTile + t);
-        if (t == 0) c.tbad[n & 7] = bad;
+        if (t == 0) c.info[n & 7] = tile_info(seg, j, unseen, bad != 0);
       }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
@@ -906,6 +954,11 @@ __device__ __forceinline__ void converters(const Prefill& p, const Plan& plan, C
       }
     }
   }
+  const int e = 2 * n, slot = e % NS;   // the end
+  if (!wait_warp(c, p, &c.empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 22)) return;
+  if (t == 0) c.info[n & 7] = kInfoStop;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&c.full[slot]);
 }
 
 // ---------------------------------------------------------------------------
@@ -988,7 +1041,7 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
 #pragma unroll
           for (int i = 0; i < kTile; ++i) asm volatile("" : "+f"(s[i]));
         }
-        const bool bad = *(volatile int*)&c.tbad[jn & 7] != 0;
+        const bool bad = (*(volatile int*)&c.info[jn & 7] & kInfoBad) != 0;
         const int left = bad ? 0 : max(0, min(kTile, lim - j * kTile));
         const bool whole = __all_sync(0xffffffffu, left == kTile);
         const float* vscl = scales + SR::val(jn);
@@ -1006,7 +1059,12 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
 #pragma unroll
           for (int i = 0; i < kTile; ++i) s[i] = -s[i];
         }
-        const float scl = TOK ? 1.f : fabsf(sc);
+        float scl = TOK ? 1.f : fabsf(sc);
+        if (!TOK && scl == 0.f) {   // all scores alike (0 * -inf would not be)
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] = 0.f;
+          scl = 1.f;
+        }
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < kTile; ++i) s[i] = i < left ? s[i] : -INFINITY;
@@ -1075,7 +1133,6 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
         const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
         const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm);
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-        const bool zero_scale = scl == 0.f && !whole;   // 0 * -inf
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
           uint32_t pk[16];
@@ -1084,10 +1141,6 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
             const int k = 32 * q4 + 2 * i;
             const float2 x = unpack2(fma2(pack2(s[k], s[k + 1]), sc2, nm2));
             float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-            if (zero_scale) {
-              if (k >= left) p0 = 0.f;
-              if (k + 1 >= left) p1 = 0.f;
-            }
             sum[i & 3] = add2(sum[i & 3], pack2(p0, p1));
             if constexpr (TOK) {
               const float2 v2 = *reinterpret_cast<const float2*>(vscl + k);
@@ -1203,7 +1256,7 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < SH::kSlots; ++i) {
       mbar_init(&c.full[i], CONV ? 4 : 1);        // converter warps, or the producer
-      mbar_init(&c.empty[i], CONV ? 2 : 4);       // A, B (and the two repair warps)
+      mbar_init(&c.empty[i], CONV ? 1 : 3);       // the last product (and the two repair warps)
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&c.raw_full[i], 1);
@@ -1218,7 +1271,7 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
       mbar_init(&c.o_full[i], 1);
     }
     mbar_init(&c.fin, 1);
-    for (int i = 0; i < 8; ++i) c.tbad[i] = c.nf[i] = 0;
+    for (int i = 0; i < 8; ++i) c.info[i] = c.nf[i] = 0;
     c.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1252,13 +1305,8 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
     if (warp == kProducerWarp) {
       producer<D, KV, CONV>(p, plan, c, base, &tmq, &tmk, &tmv);
     } else if (warp == kMmaWarp) {
-      if ((threadIdx.x & 31) == 0) {
-        const uint32_t ring = smem_u32(base) + SH::kOffSlot;
-        Mma<D, KV, CONV, BF16> mm{p, c, tbase, sdesc(smem_u32(base), 0, 1024),
-                                  sdesc(ring, 0, 1024), sdesc(ring, kTile * 128u, 1024)};
-        mm.run(plan);
-      }
-      __syncwarp();
+      Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one()};
+      mm.run();
     } else if constexpr (!CONV) {
       fixers<D, BF16>(p, plan, c, base);
     }
