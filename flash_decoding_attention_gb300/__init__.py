@@ -12,6 +12,7 @@ loading fails loudly when it is missing, and there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -83,6 +84,8 @@ _lock = threading.Lock()
 def load_library(path: Optional[str] = None):
     """Loads libfdattn.so and declares the C signatures."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -161,8 +164,15 @@ def load_library(path: Optional[str] = None):
         return lib
 
 
+# The current stream's handle without a Stream object around it (a few
+# microseconds a call); the public way where this torch does not have it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return stream
@@ -623,11 +633,14 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 # convenience API of the prompt path
 # ---------------------------------------------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Context in which ``device``, and ``stream`` if one is given, are current:
     what a call allocates for itself then belongs to the stream that uses it."""
     if stream is None:
-        return torch.cuda.device(device)
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
             torch.cuda.default_stream(device)
@@ -637,11 +650,15 @@ def _on(device, stream):
 def _heads_rows(name: str, t: torch.Tensor, heads: int, dim: int) -> int:
     """Checks a packed [tokens, heads, dim] tensor whose tokens may lie apart
     (a slice of a wider projection) and returns its token stride."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
+    if t.is_contiguous() or shape[0] == 0:
+        return heads * dim
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name}: the heads of a token must be dense (strides {stride})")
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def _cache_sizes(k_cache, v_cache, kv_start_idx, block_table):
@@ -649,57 +666,63 @@ def _cache_sizes(k_cache, v_cache, kv_start_idx, block_table):
     if (kv_start_idx is None) == (block_table is None):
         raise ValueError("give kv_start_idx (contiguous cache) or block_table (paged cache)")
     want = 4 if block_table is not None else 3
-    if k_cache.dim() != want or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    if len(shape) != want or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError(f"k_cache and v_cache must be alike and {want}-d, got "
-                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+                         f"{tuple(shape)} and {tuple(v_cache.shape)}")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k_cache and v_cache must be contiguous")
+    if not k_cache.is_cuda:
+        raise ValueError(f"the caches must be on a GPU, got {k_cache.device}")
     if block_table is not None:
-        pages, P, KVH, D = k_cache.shape
-        return pages * P, KVH, D, P
-    rows, KVH, D = k_cache.shape
-    return rows, KVH, D, 0
+        return shape[0] * shape[1], shape[2], shape[3], shape[1]
+    return shape[0], shape[1], shape[2], 0
 
 
-def _scale_kind(k_scales, v_scales, kv_rows: int, KVH: int) -> int:
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("give k_scales and v_scales, or neither")
-    if k_scales is None:
+def _scale_kind(k_scales, v_scales, kv_rows: int, KVH: int, at: int) -> int:
+    if k_scales is None and v_scales is None:
         return FD_SCALE_TENSOR
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t.dtype != torch.float32 or not t.is_contiguous() or \
-                tuple(t.shape) not in ((KVH,), (kv_rows, KVH)) or t.shape != k_scales.shape:
-            raise ValueError(f"{name} must be dense fp32 [{KVH}] or [{kv_rows}, {KVH}], got "
-                             f"{t.dtype} {tuple(t.shape)}")
-    return FD_SCALE_HEAD if k_scales.dim() == 1 else FD_SCALE_TOKEN
+    if k_scales is None or v_scales is None:
+        raise ValueError("give k_scales and v_scales, or neither")
+    shape = k_scales.shape
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or \
+            shape not in ((KVH,), (kv_rows, KVH)) or v_scales.shape != shape or \
+            not (k_scales.is_contiguous() and v_scales.is_contiguous()):
+        raise ValueError(f"k_scales and v_scales must be dense fp32 [{KVH}] or [{kv_rows}, {KVH}], "
+                         f"got {k_scales.dtype} {tuple(shape)} and {v_scales.dtype} "
+                         f"{tuple(v_scales.shape)}")
+    _same_device(at, k_scales=k_scales, v_scales=v_scales)
+    return FD_SCALE_HEAD if len(shape) == 1 else FD_SCALE_TOKEN
 
 
-def _check_index(device, batch: int, **arrays) -> None:
-    """int32 index arrays on the caches' device: ``q_start`` / ``out_start``
-    have batch + 1 entries, the others batch."""
-    for name, t in arrays.items():
-        if t is None:
-            continue
-        n = batch + 1 if name in ("q_start", "out_start") else batch
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != n or \
-                t.dim() != (2 if name == "block_table" else 1):
-            raise ValueError(f"{name} must be dense int32 with {n} entries, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
-
-
-def _check_device(device, **tensors) -> None:
+def _same_device(at: int, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"{name} is on {t.device}, the caches on cuda:{at}")
+
+
+def _index(name: str, t: torch.Tensor, n: int, at: int, dims: int = 1) -> None:
+    """A dense int32 index array of ``n`` entries (rows) on the caches' device."""
+    shape = t.shape
+    if t.dtype != torch.int32 or len(shape) != dims or shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be dense int32 with {n} entries, got {t.dtype} "
+                         f"{tuple(shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on {t.device}, the caches on cuda:{at}")
+
+
+def _layout_index(kv_start_idx, block_table, batch: int, at: int) -> None:
+    if block_table is not None:
+        _index("block_table", block_table, batch, at, 2)
+    else:
+        _index("kv_start_idx", kv_start_idx, batch, at)
 
 
 def alloc_prefill_workspace(head_dim: int, device=None) -> torch.Tensor:
     """Workspace of prefill_attention (and enough for append_kv and read_kv)
     on ``device``; keep it from call to call."""
     device = torch.device(device or "cuda")
-    with torch.cuda.device(device):
+    with torch.cuda.device(device):   # (an index-less device is the current one)
         n = fd_prefill_workspace_bytes(head_dim)
         if n == 0:
             raise FdError(FD_ERR_INVALID_ARG, "fd_prefill_workspace_bytes")
@@ -722,7 +745,12 @@ def rotary_table(positions: int, rot_dim: int, *, theta: float = 10000.0, scalin
     if out is not None and (out.dtype != torch.float32 or not out.is_contiguous() or
                             tuple(out.shape) != (positions, rot_dim)):
         raise ValueError(f"out must be dense fp32 [{positions}, {rot_dim}]")
-    device = torch.device(device or "cuda") if out is None else out.device
+    if out is not None:
+        device = out.device
+    elif device is None or torch.device(device).index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    else:
+        device = torch.device(device)
     with _on(device, stream):
         if out is None:
             out = torch.empty((int(positions), int(rot_dim)), dtype=torch.float32, device=device)
@@ -751,18 +779,20 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
     is allowed), or None without ``q``.  k_new, v_new and q may be slices of
     one wider projection."""
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
-    dev = k_cache.device
+    dev, at = k_cache.device, k_cache.get_device()
     n = k_new.shape[0]
     ks, vs = _heads_rows("k_new", k_new, KVH, D), _heads_rows("v_new", v_new, KVH, D)
     if v_new.shape[0] != n or v_new.dtype != k_new.dtype:
         raise ValueError("k_new and v_new must be alike")
     if ks != vs:
         raise ValueError(f"k_new and v_new must have one token stride, got {ks} and {vs}")
-    _check_index(dev, positions.shape[0], q_start=q_start, positions=positions,
-                 kv_start_idx=kv_start_idx, block_table=block_table)
-    _check_device(dev, k_new=k_new, v_new=v_new, v_cache=v_cache, q=q, q_out=q_out, rotary=rotary,
-                  k_scales=k_scales, v_scales=v_scales, workspace=workspace)
-    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    batch = positions.shape[0]
+    _index("q_start", q_start, batch + 1, at)
+    _index("positions", positions, batch, at)
+    _layout_index(kv_start_idx, block_table, batch, at)
+    _same_device(at, k_new=k_new, v_new=v_new, v_cache=v_cache, q=q, q_out=q_out, rotary=rotary,
+                 workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     QH = qs = 0
     if q is not None:
         if q.dim() != 3 or q.shape[0] != n or q.dtype != k_new.dtype:
@@ -804,13 +834,14 @@ def read_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, out_start: torch.Tenso
     are sequence b's tokens from ``first[b]`` (0 without ``first``) on, decoded
     and scaled.  ``dtype`` defaults to the cache's 16-bit type, or f16."""
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
-    dev = k_cache.device
+    dev, at = k_cache.device, k_cache.get_device()
     batch = out_start.shape[0] - 1
-    _check_index(dev, batch, out_start=out_start, first=first, kv_start_idx=kv_start_idx,
-                 block_table=block_table)
-    _check_device(dev, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
-                  v_out=v_out, workspace=workspace)
-    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    _index("out_start", out_start, batch + 1, at)
+    if first is not None:
+        _index("first", first, batch, at)
+    _layout_index(kv_start_idx, block_table, batch, at)
+    _same_device(at, v_cache=v_cache, k_out=k_out, v_out=v_out, workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else k_cache.dtype if \
             k_cache.dtype in (torch.float16, torch.bfloat16) else torch.float16
@@ -852,16 +883,18 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     by ``rotary`` if given); ``seq_len`` counts them.  Without ``k_new`` the
     caches hold them already and ``q`` is taken as it is."""
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
-    dev = k_cache.device
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, heads, {D}], got {tuple(q.shape)}")
-    n, QH = q.shape[0], q.shape[1]
+    dev, at = k_cache.device, k_cache.get_device()
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, {D}], got {tuple(shape)}")
+    n, QH = shape[0], shape[1]
     qs = _heads_rows("q", q, QH, D)
-    _check_index(dev, seq_len.shape[0], q_start=q_start, seq_len=seq_len,
-                 kv_start_idx=kv_start_idx, block_table=block_table)
-    _check_device(dev, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, out=out,
-                  lse=lse, workspace=workspace)
-    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH)
+    batch = seq_len.shape[0]
+    _index("q_start", q_start, batch + 1, at)
+    _index("seq_len", seq_len, batch, at)
+    _layout_index(kv_start_idx, block_table, batch, at)
+    _same_device(at, q=q, v_cache=v_cache, out=out, lse=lse, workspace=workspace)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     if (k_new is None) != (v_new is None) or (k_new is None) != (positions is None):
         raise ValueError("give k_new, v_new and positions, or none of them")
     if rotary is not None and k_new is None:
@@ -876,7 +909,7 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         raise ValueError(f"lse must be dense fp32 [{n}, {QH}]")
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
         if lse is None:
             lse = torch.empty((n, QH), dtype=torch.float32, device=dev)
         if workspace is None:
