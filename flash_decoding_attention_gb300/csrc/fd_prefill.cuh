@@ -411,6 +411,18 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Four floats of shared memory, all lanes at one address (in program order:
+// gathered ahead they would not fit beside a row's scores).
+__device__ __forceinline__ void lds_pairs(const float* a, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(smem_u32(a)));
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
   if constexpr (BF16) {
@@ -629,37 +641,33 @@ struct Mma {
   static constexpr int NS = SH::kSlots;
   const Prefill& p;
   Control& c;
-  uint32_t tbase, base, elected;
+  uint32_t tbase, base, lead;   // lead: this lane issues
 
   template <int X>
   __device__ __forceinline__ void scores(int slot) const {
     constexpr uint32_t id = idesc_f16(kRowsTile, kTile, 0, BF16 ? 1 : 0);
     const uint64_t a = sdesc(base + X * SH::kQTile, 0, 1024);
     const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, 0, 1024);
-    if (elected) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-        umma(tbase + X * kTile, a + off, b + off, id, ks > 0);
-      }
-      umma_commit(&c.s_full[X]);
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+      umma_lead(lead, tbase + X * kTile, a + off, b + off, id, ks > 0);
     }
+    commit(&c.s_full[X]);
   }
 
   template <int X>
   __device__ __forceinline__ void values(int slot, int accumulate) const {
     constexpr uint32_t id = idesc_f16(kRowsTile, D, 1, BF16 ? 1 : 0);
     const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, kTile * 128u, 1024);
-    if (elected) {
 #pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
-        umma_ts(tbase + (2 + X) * kTile, tbase + X * kTile + ks * 8, b + ((ks * 2048) >> 4), id,
-                ks > 0 ? 1 : accumulate);
-    }
+    for (int ks = 0; ks < kTile / 16; ++ks)
+      umma_ts_lead(lead, tbase + (2 + X) * kTile, tbase + X * kTile + ks * 8,
+                   b + ((ks * 2048) >> 4), id, ks > 0 ? 1 : accumulate);
   }
 
   __device__ __forceinline__ void commit(uint64_t* bar) const {
-    if (elected) umma_commit(bar);
+    umma_commit_lead(lead, bar);
   }
 
   __device__ __forceinline__ void run() {
@@ -703,6 +711,9 @@ struct Mma {
       uint32_t nkph = kph, nvph = vph;
       if (nks >= NS) { nks -= NS; nkph ^= 1; }
       if (nvs >= NS) { nvs -= NS; nvph ^= 1; }
+      // the next tile, if it is there already (else after P V of A)
+      bool known = __all_sync(0xffffffffu, mbar_test(&c.full[nks], nkph));
+      int next = known ? info_of(n + 1) : 0;
       if (cur & kInfoA) {
         ok = ok && wait_warp(c, p, &c.p_full[0], pph[0], 7);
         if (!ok) break;
@@ -711,10 +722,11 @@ struct Mma {
         values<0>(vs, acc);
         if (cur & kInfoLastA) commit(&c.o_full[0]);
       }
-      // the next tile, or the end
-      ok = ok && wait_warp(c, p, &c.full[nks], nkph, 7);
-      if (!ok) break;
-      const int next = info_of(n + 1);
+      if (!known) {
+        ok = ok && wait_warp(c, p, &c.full[nks], nkph, 7);
+        if (!ok) break;
+        next = info_of(n + 1);
+      }
       const bool follows = !(next & (kInfoFirst | kInfoStop));
       if (follows && (next & kInfoA)) {
         tc_fence_after();
@@ -745,7 +757,7 @@ struct Mma {
     }
     // every issued product is done before the tensor memory is freed
     commit(&c.fin);
-    if (!wait_drain(&c.fin) && elected) raise_error(p.at.ws, kErrDrain, 10);
+    if (!wait_drain(&c.fin) && lead) raise_error(p.at.ws, kErrDrain, 10);
   }
 
   static __device__ __forceinline__ bool wait_drain(uint64_t* bar) {
@@ -1049,11 +1061,14 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
           const float* ksc = scales + SR::key(jn);   // written before the tile's S was issued
 #pragma unroll
           for (int i = 0; i < kTile; i += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(ksc + i);
-            s[i] *= k4.x;
-            s[i + 1] *= k4.y;
-            s[i + 2] *= k4.z;
-            s[i + 3] *= k4.w;
+            uint64_t k01, k23;
+            lds_pairs(ksc + i, k01, k23);
+            const float2 a = unpack2(mul2(pack2(s[i], s[i + 1]), k01));
+            const float2 b = unpack2(mul2(pack2(s[i + 2], s[i + 3]), k23));
+            s[i] = a.x;
+            s[i + 1] = a.y;
+            s[i + 2] = b.x;
+            s[i + 3] = b.y;
           }
         } else if (sc < 0.f) {   // a negative scale: the maximum of -s is sought
 #pragma unroll
@@ -1071,12 +1086,12 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kTile; i += 4) {
-          mx[0] = fmaxf(mx[0], s[i]);
-          mx[1] = fmaxf(mx[1], s[i + 1]);
-          mx[2] = fmaxf(mx[2], s[i + 2]);
-          mx[3] = fmaxf(mx[3], s[i + 3]);
+        for (int i = 4; i + 7 < kTile; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kTile - 4 + k]);
         const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float mt = smax == -INFINITY ? -INFINITY : smax * scl;
         float fac = 1.f;
@@ -1131,23 +1146,29 @@ __device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Cont
         // P = 2^(s - m_ref + kLift); excluded scores are -inf and give 0 (a
         // row that has seen no key has m_ref = -inf: everything is excluded)
         const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
-        const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm);
+        const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm), vm2 = pack2(vmul, vmul);
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
           uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 16; i += 2) {
             const int k = 32 * q4 + 2 * i;
             const float2 x = unpack2(fma2(pack2(s[k], s[k + 1]), sc2, nm2));
-            float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-            sum[i & 3] = add2(sum[i & 3], pack2(p0, p1));
+            const float2 y = unpack2(fma2(pack2(s[k + 2], s[k + 3]), sc2, nm2));
+            uint64_t pa = pack2(fast_exp2(x.x), fast_exp2(x.y));
+            uint64_t pb = pack2(fast_exp2(y.x), fast_exp2(y.y));
+            sum[i & 2] = add2(sum[i & 2], pa);
+            sum[(i & 2) + 1] = add2(sum[(i & 2) + 1], pb);
             if constexpr (TOK) {
-              const float2 v2 = *reinterpret_cast<const float2*>(vscl + k);
-              p0 *= BF16 ? v2.x : v2.x * vmul;
-              p1 *= BF16 ? v2.y : v2.y * vmul;
+              uint64_t va, vb;
+              lds_pairs(vscl + k, va, vb);
+              pa = mul2(pa, BF16 ? va : mul2(va, vm2));
+              pb = mul2(pb, BF16 ? vb : mul2(vb, vm2));
             }
-            pk[i] = pack16<BF16>(p0, p1);
+            const float2 qa = unpack2(pa), qb = unpack2(pb);
+            pk[i] = pack16<BF16>(qa.x, qa.y);
+            pk[i + 1] = pack16<BF16>(qb.x, qb.y);
           }
           tmem_st16u(tS + 16 * q4, pk);
         }
