@@ -46,150 +46,210 @@ bool make_map(CUtensorMap* m, const void* base, int elem, int head_dim, int head
 // 2 (c - 1) + 1 and its continuations in slots 2 c, 2 (c + 1), ...:
 //   M = max_k m_k, L = sum_k l_k 2^(m_k - M), A = sum_k acc_k 2^(m_k - M),
 //   out = v_scale A / L, lse = (M + log2 L) ln 2,
-// in the order of k.  Every CTA finds all cut streams from the slots' notes
-// (one per boundary between CTAs at most), lays their rows end to end and
-// takes its share.
+// in a fixed order.  Every CTA finds all cut streams from the slots' notes (one
+// per boundary between CTAs at most) and lays their work end to end: items of
+// 32 rows (a row per lane, as the states are laid out) times 16 dims.  A warp
+// takes an item of a stream cut into few parts; the warps of a CTA share the
+// states of an item of a stream cut into many.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxGrid = 512;   // boundaries (SMs)
+constexpr int kFew = 6;         // parts one warp passes alone
 
-template <int D, bool BF16, int WPI>
+struct Part {
+  int c, X, row0, dim0, parts;   // boundary, query tile, first row, first dim, parts
+  int4 id;
+};
+
+// Running state of one row and 16 dims.
+struct State {
+  float m, l, a[16];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(float mk, float lk, const float (&x)[16]) {
+    const float M = fmaxf(m, mk);
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - M);
+    const float g = mk == -INFINITY ? 0.f : fast_exp2(mk - M);
+    m = M;
+    l = l * f + lk * g;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = fmaf(x[i], g, a[i] * f);
+  }
+};
+
+template <int D, bool BF16>
+struct Merge {
+  const Prefill& p;
+  int lane;
+
+  __device__ __forceinline__ int live_rows(const Seq& s, int m, int X) const {
+    const long long left = (long long)s.n - (long long)m * s.span - (long long)X * p.tile_tokens;
+    return (int)(left < p.tile_tokens ? (left > 0 ? left : 0) : p.tile_tokens) * p.group;
+  }
+
+  // Adds parts first, first + step, ... of `it` to `st`.
+  __device__ __forceinline__ void gather(const Part& it, int first, int step, bool live,
+                                         State& st) const {
+    constexpr int kAhead = 2;
+    for (int k0 = first; k0 < it.parts; k0 += kAhead * step) {
+      float2 ml[kAhead];
+      float4 x[kAhead][4];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * step;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (live && k < it.parts) {
+          // (written as a sum: with a choice between two addresses the
+          // compiled loop read the wrong slot from its second state on)
+          const int slot = 2 * (it.c - 1 + k) + (k == 0 ? 1 : 0);
+          const long long tile = 2ll * slot + it.X;
+          ml[u] = p.part_ml[tile * kRowsTile + it.row0 + lane];
+          const float4* src = reinterpret_cast<const float4*>(p.part_acc) +
+                              (tile * (D / 4) + it.dim0 / 4) * kRowsTile + it.row0 + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][i] = src[i * kRowsTile];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (!live || k0 + u * step >= it.parts) continue;
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[4 * i] = x[u][i].x;
+          y[4 * i + 1] = x[u][i].y;
+          y[4 * i + 2] = x[u][i].z;
+          y[4 * i + 3] = x[u][i].w;
+        }
+        st.add(ml[u].x, ml[u].y, y);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void write(const Part& it, const Seq& s, const State& st) const {
+    const int r = it.row0 + lane;
+    const long long tok = (long long)s.q0 + (long long)(2 * it.id.z + it.X) * p.tile_tokens +
+                          r / p.group;
+    const long long orow = tok * p.num_q_heads + (long long)it.id.y * p.group + r % p.group;
+    float vsc = p.v_scale;
+    if (p.scale_kind == FD_SCALE_HEAD) vsc *= __ldg(p.v_scales + it.id.y);
+    const float q = st.l > 0.f ? vsc / st.l : 0.f;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack16<BF16>(st.a[2 * i] * q, st.a[2 * i + 1] * q);
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * D + it.dim0);
+    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (p.lse && it.dim0 == 0)
+      p.lse[orow] = st.l > 0.f ? (st.m + log2f(st.l)) * kLn2 : -INFINITY;
+  }
+};
+
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Prefill p) {
-  constexpr int DPL = D / 32, kWarps = kMergeThreads / 32;
-  __shared__ int4 first[kMaxGrid];     // slot 2 c
-  __shared__ int rows_before[kMaxGrid + 1];
-  __shared__ int wsum[kWarps];
-  __shared__ float red_m[kWarps], red_l[kWarps], red_a[kWarps][D];
+  __shared__ int4 first[kMaxGrid];                  // stream of slot 2 c
+  __shared__ short parts_of[kMaxGrid];
+  __shared__ int before[2][kMaxGrid + 1];           // items before c: few parts, many parts
+  __shared__ int wsum[2][kMergeWarps];
+  __shared__ float red[kMergeWarps][18][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Merge<D, BF16> mg{p, lane};
   for (int c = tid; c < p.grid; c += kMergeThreads) first[c] = p.meta[2 * c];
-  int carry = 0;
+  __syncthreads();
+  auto same = [](const int4& a, const int4& b) { return a.x == b.x && a.y == b.y && a.z == b.z; };
+  int carry[2] = {0, 0};
   for (int base = 0; base < p.grid; base += kMergeThreads) {
     const int c = base + tid;
-    int rows = 0;
+    int items[2] = {0, 0};
     if (c > 0 && c < p.grid) {
-      const int4 a = p.meta[2 * c - 1], b = p.meta[2 * c];
-      if (b.x >= 0 && b.x < p.at.batch && a.x == b.x && a.y == b.y && a.z == b.z) {
-        // whole tokens of both query tiles, as the attention kernel lays them
-        const Seq s = load_seq(p, b.x, false);
-        const long long left = (long long)s.n - (long long)b.z * s.span;
-        rows = (int)(left < s.span ? (left > 0 ? left : 0) : s.span) * p.group;
+      const int4 id = first[c], begun = p.meta[2 * c - 1];
+      if (id.x >= 0 && id.x < p.at.batch && same(id, begun)) {
+        int parts = 2;   // the beginning and this continuation
+        while (c + parts - 1 < p.grid && same(first[c + parts - 1], id)) ++parts;
+        parts_of[c] = (short)parts;
+        const Seq s = load_seq(p, id.x, false);
+        const int blocks = (mg.live_rows(s, id.z, 0) + 31) / 32 + (mg.live_rows(s, id.z, 1) + 31) / 32;
+        items[parts <= kFew ? 0 : 1] = blocks * (D / 16);
       }
     }
-    int x = rows;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    for (int k = 0; k < 2; ++k) {
+      int x = items[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) wsum[k][warp] = x;
+      __syncthreads();
+      int b = carry[k];
+      for (int w = 0; w < kMergeWarps; ++w) {
+        if (w < warp) b += wsum[k][w];
+        carry[k] += wsum[k][w];
+      }
+      if (c < p.grid) before[k][c] = b + x - items[k];
     }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
-    }
-    if (c < p.grid) rows_before[c] = before + x - rows;
-    carry += all;
     __syncthreads();
   }
-  if (tid == 0) rows_before[p.grid] = carry;
-  __syncthreads();
-  const int total = carry;
-  constexpr int kItems = kWarps / WPI;   // rows a CTA merges at a time
-  const int part = warp % WPI, slot_in_cta = warp / WPI;
-  for (int it0 = blockIdx.x * kItems; it0 < total; it0 += gridDim.x * kItems) {
-    const int item = it0 + slot_in_cta;
-    const bool live = item < total;
-    int c = 0, nseg = 0, row = 0;
-    int4 id = make_int4(0, 0, 0, 0);
-    if (live) {
-      int lo = 0, hi = p.grid;   // the last boundary with rows_before <= item
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (rows_before[mid] <= item) lo = mid;
-        else hi = mid;
+  auto part_at = [&](int k, int item) {
+    int lo = 0, hi = p.grid;   // the last boundary with before <= item
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[k][mid] <= item) lo = mid;
+      else hi = mid;
+    }
+    Part it;
+    it.c = lo;
+    it.id = first[lo];
+    it.parts = parts_of[lo];
+    const int w = item - before[k][lo];
+    it.dim0 = (w % (D / 16)) * 16;
+    it.row0 = w / (D / 16) * 32;   // over both query tiles for now
+    return it;
+  };
+  for (int item = blockIdx.x * kMergeWarps + warp; item < carry[0];
+       item += gridDim.x * kMergeWarps) {
+    Part it = part_at(0, item);
+    const Seq s = load_seq(p, it.id.x, false);
+    const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
+    it.X = it.row0 >= rows_a ? 1 : 0;
+    if (it.X) it.row0 -= rows_a;
+    const bool live = it.row0 + lane < mg.live_rows(s, it.id.z, it.X);
+    State st;
+    st.clear();
+    mg.gather(it, 0, 1, live, st);
+    if (live) mg.write(it, s, st);
+  }
+  for (int item = blockIdx.x; item < carry[1]; item += gridDim.x) {
+    Part it = part_at(1, item);
+    const Seq s = load_seq(p, it.id.x, false);
+    const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
+    it.X = it.row0 >= rows_a ? 1 : 0;
+    if (it.X) it.row0 -= rows_a;
+    const bool live = it.row0 + lane < mg.live_rows(s, it.id.z, it.X);
+    State st;
+    st.clear();
+    mg.gather(it, warp, kMergeWarps, live, st);
+    red[warp][16][lane] = st.m;
+    red[warp][17][lane] = st.l;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) red[warp][i][lane] = st.a[i];
+    __syncthreads();
+    if (warp == 0 && live) {
+      for (int w = 1; w < kMergeWarps; ++w) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = red[w][i][lane];
+        st.add(red[w][16][lane], red[w][17][lane], x);
       }
-      c = lo;
-      id = first[c];
-      nseg = 2;   // the beginning and this continuation
-      while (c + nseg - 1 < p.grid && first[c + nseg - 1].x == id.x &&
-             first[c + nseg - 1].y == id.y && first[c + nseg - 1].z == id.z)
-        ++nseg;
-      row = item - rows_before[c];
+      mg.write(it, s, st);
     }
-    // row of the pair: query tile, token of the tile, head of the group
-    const int per_tile = p.tile_tokens * p.group;
-    const int X = row >= per_tile ? 1 : 0;
-    const int r = row - X * per_tile;
-    auto at = [&](int k) -> long long {
-      // (written as a sum: with a choice between two addresses the compiled
-      // loop read the wrong slot from its second state on)
-      const int slot = 2 * (c - 1 + k) + (k == 0 ? 1 : 0);
-      return (long long)slot * kRowsPair + X * kRowsTile + r;
-    };
-    // this warp's states: part, part + WPI, ...; the lanes share a state's dims
-    const int nu = nseg > part ? (nseg - part + WPI - 1) / WPI : 0;
-    float M = -INFINITY;
-    for (int u = lane; u < nu; u += 32) M = fmaxf(M, p.part_ml[at(part + WPI * u)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if constexpr (WPI > 1) {
-      if (lane == 0) red_m[warp] = M;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < WPI; ++w) M = fmaxf(M, red_m[slot_in_cta * WPI + w]);
-    }
-    float L = 0.f, a[DPL];
-#pragma unroll
-    for (int k = 0; k < DPL; ++k) a[k] = 0.f;
-#pragma unroll 4
-    for (int u = 0; u < nu; ++u) {
-      const long long i = at(part + WPI * u);
-      const float2 ml = p.part_ml[i];
-      const float* src = p.part_acc + i * D + lane * DPL;
-      float x[DPL];
-      if constexpr (DPL == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        x[0] = y.x; x[1] = y.y;
-      }
-      const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-      L = fmaf(ml.y, w, L);
-#pragma unroll
-      for (int k = 0; k < DPL; ++k) a[k] = fmaf(x[k], w, a[k]);
-    }
-    if constexpr (WPI > 1) {
-      if (lane == 0) red_l[warp] = L;
-#pragma unroll
-      for (int k = 0; k < DPL; ++k) red_a[warp][lane * DPL + k] = a[k];
-      __syncthreads();
-      L = 0.f;
-#pragma unroll
-      for (int k = 0; k < DPL; ++k) a[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < WPI; ++w) {
-        L += red_l[slot_in_cta * WPI + w];
-#pragma unroll
-        for (int k = 0; k < DPL; ++k) a[k] += red_a[slot_in_cta * WPI + w][lane * DPL + k];
-      }
-      __syncthreads();
-    }
-    if (!live || part != 0) continue;
-    const Seq s = load_seq(p, id.x, false);
-    const long long tok = (long long)s.q0 + (long long)(2 * id.z + X) * p.tile_tokens + r / p.group;
-    const long long orow = tok * p.num_q_heads + (long long)id.y * p.group + r % p.group;
-    float vsc = p.v_scale;
-    if (p.scale_kind == FD_SCALE_HEAD) vsc *= __ldg(p.v_scales + id.y);
-    const float q = L > 0.f ? vsc / L : 0.f;
-    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + lane * DPL);
-    if constexpr (DPL == 4)
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(pack16<BF16>(a[0] * q, a[1] * q), pack16<BF16>(a[2] * q, a[3] * q));
-    else
-      *o = pack16<BF16>(a[0] * q, a[1] * q);
-    if (p.lse && lane == 0) p.lse[orow] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    __syncthreads();
   }
 }
 
@@ -205,7 +265,7 @@ cudaError_t launch_merge(const Prefill& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D, BF16, 2>, p);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D, BF16>, p);
 }
 
 }  // namespace

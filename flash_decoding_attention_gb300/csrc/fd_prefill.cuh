@@ -67,11 +67,10 @@ constexpr int kTile = 128;          // keys per tile
 constexpr int kRowsTile = 128;      // rows of a query tile
 constexpr int kRowsPair = 2 * kRowsTile;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
-constexpr int kPages = 32;          // block-table entries staged at a time
+constexpr int kPages = 20;          // block-table entries staged at a time (a tile has 16)
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
-// Cost of a segment start (Q load, first product, epilogue), in keys of one
-// query tile.
-constexpr long long kStartCost = 640;
+// Cost of a segment start (Q load, first product, epilogue), in keys.
+constexpr long long kStartCost = 256;
 
 // ---------------------------------------------------------------------------
 // Streams and their split
@@ -88,21 +87,17 @@ __device__ __forceinline__ int pair_end(const Seq& s, int m) {
   return e > 0 ? e : 0;
 }
 
-__device__ __forceinline__ int pair_weight(const Seq& s, int m) {
-  return (long long)m * s.span + s.span / 2 < s.n ? 2 : 1;
-}
-
 __device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
-  return kStartCost + (long long)pair_weight(s, m) * pair_end(s, m);
+  return kStartCost + (long long)pair_end(s, m);
 }
 
-// Cost of pairs 0 .. m - 1 (m < pairs: all of them have both query tiles).
+// Cost of pairs 0 .. m - 1 (m < pairs: all of them are full).
 __device__ __forceinline__ long long pairs_before(const Seq& s, int m) {
   long long c = (long long)m * kStartCost;
-  long long m0 = s.ctx >= 0 ? 0 : (-(long long)s.ctx) / s.span;   // pairs without keys
+  const int m0 = s.ctx >= 0 ? 0 : -s.ctx / s.span;   // pairs without keys
   if (m > m0) {
-    const long long mm = m;
-    c += 2 * ((mm - m0) * s.ctx + (long long)s.span * ((mm * (mm + 1) - m0 * (m0 + 1)) / 2));
+    const long long a = m, b = m0;
+    c += (a - b) * s.ctx + (long long)s.span * ((a * (a + 1) - b * (b + 1)) / 2);
   }
   return c;
 }
@@ -120,7 +115,7 @@ __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   }
   s.ctx = s.T - s.n;
   s.span = 2 * p.tile_tokens;
-  s.pairs = (int)(((long long)s.n + s.span - 1) / s.span);
+  s.pairs = (int)(((unsigned)s.n + (unsigned)s.span - 1u) / (unsigned)s.span);
   s.head = s.n > 0 ? pairs_before(s, s.pairs - 1) + pair_cost(s, s.pairs - 1) : 0;
   return s;
 }
@@ -147,10 +142,10 @@ __device__ inline Plan make_plan(const Prefill& p, long long* red) {
   Plan r;
   r.total = 0;
   for (int w = 0; w < nw; ++w) r.total += red[w];
-  // every CTA but the last takes at least one tile of two query tiles, so a
-  // range inside a stream always holds a tile
+  // every CTA but the last takes at least one tile, so a range inside a
+  // stream always holds one
   r.per_cta = (r.total + p.grid - 1) / p.grid;
-  if (r.per_cta < 2 * kTile) r.per_cta = 2 * kTile;
+  if (r.per_cta < kTile) r.per_cta = kTile;
   const long long target = (long long)blockIdx.x * r.per_cta;
   __syncthreads();
   if (tid == 0) {
@@ -193,6 +188,7 @@ struct Seg {
   int tb, te;                // tiles [tb, te) of the pair's stream
   int end;                   // keys of the stream
   int nt[2];                 // tiles of query tile A, B in the stream (0: no rows or no keys)
+  bool solo;                 // no rows in B: its softmax takes A's odd tiles (see below)
   bool complete;             // the whole stream
   int slot;                  // partial slot otherwise
 };
@@ -224,16 +220,15 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const Prefill& p, Seg& o) {
     while (ps < g_end) {
-      const int w = pair_weight(s, m), end = pair_end(s, m);
-      const long long cost = kStartCost + (long long)w * end;
+      const int end = pair_end(s, m);
+      const long long cost = kStartCost + end;
       const int n = (end + kTile - 1) / kTile;
       const long long a = g > ps ? g : ps, e = ps + cost < g_end ? ps + cost : g_end;
-      // tile i stands at ps + kStartCost + i * unit and belongs to the range
-      // that holds this point
-      const long long unit = (long long)w * kTile;
+      // tile i stands at ps + kStartCost + 128 i and belongs to the range that
+      // holds this point
       const long long xa = a - ps - kStartCost, xe = e - ps - kStartCost;
-      const int tb = xa <= 0 ? 0 : (int)min((long long)n, (xa + unit - 1) / unit);
-      const int te = xe <= 0 ? 0 : (int)min((long long)n, (xe + unit - 1) / unit);
+      const int tb = xa <= 0 ? 0 : min(n, (int)((xa + kTile - 1) >> 7));
+      const int te = xe <= 0 ? 0 : min(n, (int)((xe + kTile - 1) >> 7));
       const bool yields = n > 0 ? te > tb : g <= ps;
       if (yields) {
         o.b = s.b;
@@ -246,9 +241,10 @@ struct Walk {
         o.te = te;
         o.end = end;
         const int half = s.span >> 1;
-        const int ea = s.ctx + min((long long)s.n, (long long)m * s.span + half);
+        const int ea = s.ctx + (int)min((long long)s.n, (long long)m * s.span + half);
         o.nt[0] = ea > 0 ? (ea + kTile - 1) / kTile : 0;
-        o.nt[1] = w == 2 ? n : 0;
+        o.solo = (long long)m * s.span + half >= s.n;
+        o.nt[1] = o.solo ? 0 : n;
         o.complete = tb == 0 && te == n;
         o.slot = 2 * (int)blockIdx.x + (tb > 0 ? 0 : 1);
       }
@@ -298,22 +294,26 @@ struct Shape {
 // ends of its segment, and what its rows are.  An entry behind the last tile
 // says stop.
 enum : int {
-  kInfoA = 1, kInfoB = 2,            // query tile A, B has rows that see the tile
-  kInfoLastA = 4, kInfoLastB = 8,    // its last tile of the segment
-  kInfoFirst = 16,                   // first tile of the segment
+  kInfoA = 1, kInfoB = 2,            // products for query tile A, B
+  kInfoLastA = 4, kInfoLastB = 8,    // their last of the segment
+  kInfoStart = 16,                   // first tile of the segment
   kInfoFix = 32,                     // V is repaired before use (no converters)
   kInfoBad = 64,                     // a row lies outside the cache: the tile is absent
-  kInfoStop = 128
+  kInfoSolo = 128,                   // A and B take turns on query tile A
+  kInfoEnd = 256,                    // last tile of the segment
+  kInfoStop = 512
 };
 
 struct Control {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t fixed[4];   // V tiles repaired (no converters), or V scales written (converters)
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fin;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], fin;
+  uint64_t x_full, x_empty;   // exchange between the softmax halves of a solo segment
   int info[8];      // what the tensor cores do with tile j (slot j mod 8), kInfo bits
   int nf[8];        // segment i (slot i mod 8) + 1 when its V held masked non-finite elements
   int abort_flag;
+  int swaps;        // exchanges of solo segments that are over
   uint32_t tmem_base;
   int pages[kPages];
 };
@@ -456,11 +456,36 @@ __device__ __forceinline__ bool drop_nan_e4m3(uint32_t& w) {
   return any;
 }
 
+// Solo segments of two tiles or more: the two softmax halves exchange their
+// states through query tile B's place in shared memory.
+__device__ __forceinline__ bool swaps_in(const Seg& s) { return s.solo && s.te - s.tb > 1; }
+
+// Waits until `want` exchanges are over; bounded like every wait.
+__device__ __forceinline__ bool wait_swaps(Control& c, const Prefill& p, int want) {
+  if (*(volatile int*)&c.swaps >= want) return true;
+  const unsigned long long t0 = mma::global_ns();
+  while (*(volatile int*)&c.swaps < want) {
+    if (aborted(c)) return false;
+    if (mma::global_ns() - t0 > p.wait_ns) {
+      record_abort(c, p, 4);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ int tile_info(const Seg& s, int j, int unseen, bool bad) {
   int w = bad ? kInfoBad : 0;
-  if (j < s.nt[0]) w |= kInfoA | (j + 1 == min(s.te, s.nt[0]) ? kInfoLastA : 0);
-  if (j < s.nt[1]) w |= kInfoB | (j + 1 == min(s.te, s.nt[1]) ? kInfoLastB : 0);
-  if (j == s.tb) w |= kInfoFirst;
+  if (s.solo) {
+    const int x = (j - s.tb) & 1;
+    w |= kInfoSolo | (x ? kInfoB : kInfoA);
+    if (j + 2 >= s.te) w |= x ? kInfoLastB : kInfoLastA;
+  } else {
+    if (j < s.nt[0]) w |= kInfoA | (j + 1 == min(s.te, s.nt[0]) ? kInfoLastA : 0);
+    if (j < s.nt[1]) w |= kInfoB | (j + 1 == min(s.te, s.nt[1]) ? kInfoLastB : 0);
+  }
+  if (j == s.tb) w |= kInfoStart;
+  if (j + 1 == s.te) w |= kInfoEnd;
   if ((j + 1) * kTile > unseen) w |= kInfoFix;
   return w;
 }
@@ -496,7 +521,7 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
   Walk walk;
   walk.init(p, plan);
   Seg seg;
-  int n = 0, qn[2] = {0, 0};
+  int n = 0, qn[2] = {0, 0}, swaps = 0;
   bool stop = p.starve != 0;
   const int box_rows = p.at.block_table && p.at.page_size < kTile ? p.at.page_size : kTile;
   while (!stop && walk.next(p, seg)) {
@@ -504,10 +529,16 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (stop || seg.tb >= min(seg.te, seg.nt[x])) continue;
+        // tile B's place may still serve an exchange of an earlier segment
+        if (x == 1 && !wait_swaps(c, p, swaps)) {
+          stop = true;
+          continue;
+        }
         if (!wait_for(c, p, &c.q_empty[x], (uint32_t)((qn[x] & 1) ^ 1), 1)) {
           stop = true;
           continue;
         }
+        ++qn[x];
         const uint32_t rows = (uint32_t)(p.tile_tokens * p.group);
         mbar_arrive_tx(&c.q_full[x], rows * D * 2u);
         const int tok = seg.q0 + (2 * seg.m + x) * p.tile_tokens;
@@ -515,10 +546,10 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
         for (int d = 0; d < D / 64; ++d)
           mma::tma_load_3d_hint(base + x * SH::kQTile + d * (kRowsTile * 128), tmq, 64 * d,
                                 seg.h * p.group, tok, &c.q_full[x], keep);
-        ++qn[x];
       }
     }
     stop = __shfl_sync(0xffffffffu, stop, 0);
+    if (swaps_in(seg)) ++swaps;
     if (!tiles || stop) continue;
     const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
     const int unseen = first_unseen(seg, 2 * p.tile_tokens);
@@ -626,6 +657,8 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
 // uniform registers; one elected lane issues.  For tile n, in this order:
 //   P V of A, S of A for tile n + 1, P V of B, S of B for tile n + 1,
 // so the softmax of one query tile has the other's two products to run in.
+// In a solo segment (rows in A only) A and B take the tiles in turns:
+//   P V of A for tile n, S of A for n + 2, P V of B for n + 1, S of B for n + 3.
 // Products of one thread run in issue order, so S may overwrite the P that
 // the P V before it reads.
 __device__ __forceinline__ uint32_t elect_one() {
@@ -642,11 +675,14 @@ struct Mma {
   const Prefill& p;
   Control& c;
   uint32_t tbase, base, lead;   // lead: this lane issues
+  uint32_t qph[2], pph[2];      // phases of Q and of P
+  int fixes;                    // repaired V tiles so far
 
+  // S of X with Q tile `qt` and the K tile in `slot`.
   template <int X>
-  __device__ __forceinline__ void scores(int slot) const {
+  __device__ __forceinline__ void scores(int slot, int qt) const {
     constexpr uint32_t id = idesc_f16(kRowsTile, kTile, 0, BF16 ? 1 : 0);
-    const uint64_t a = sdesc(base + X * SH::kQTile, 0, 1024);
+    const uint64_t a = sdesc(base + (uint32_t)qt * SH::kQTile, 0, 1024);
     const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, 0, 1024);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -656,105 +692,187 @@ struct Mma {
     commit(&c.s_full[X]);
   }
 
+  // P V of X with the V tile in `slot`: the first half of the keys as soon as
+  // their P is there, then the others.
   template <int X>
-  __device__ __forceinline__ void values(int slot, int accumulate) const {
+  __device__ __forceinline__ bool values(int slot, int accumulate) {
     constexpr uint32_t id = idesc_f16(kRowsTile, D, 1, BF16 ? 1 : 0);
     const uint64_t b = sdesc(base + SH::kOffSlot + (uint32_t)slot * SH::kSlot, kTile * 128u, 1024);
+    constexpr int kHalf = kTile / 32;
+    if (!wait_warp(c, p, &c.p_half[X], pph[X], 7)) return false;
+    tc_fence_after();
 #pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks)
+    for (int ks = 0; ks < kHalf; ++ks)
       umma_ts_lead(lead, tbase + (2 + X) * kTile, tbase + X * kTile + ks * 8,
                    b + ((ks * 2048) >> 4), id, ks > 0 ? 1 : accumulate);
+    if (!wait_warp(c, p, &c.p_full[X], pph[X], 7)) return false;
+    pph[X] ^= 1;
+    tc_fence_after();
+#pragma unroll
+    for (int ks = kHalf; ks < 2 * kHalf; ++ks)
+      umma_ts_lead(lead, tbase + (2 + X) * kTile, tbase + X * kTile + ks * 8,
+                   b + ((ks * 2048) >> 4), id, 1);
+    return true;
   }
 
   __device__ __forceinline__ void commit(uint64_t* bar) const {
     umma_commit_lead(lead, bar);
   }
 
-  __device__ __forceinline__ void run() {
-    int n = 0, ks = 0, vs = 1, fixes = 0;      // tile, its slots
-    uint32_t kph = 0, vph = 0;                 // their phases
-    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
-    bool ok = wait_warp(c, p, &c.full[0], 0, 7);
-    // a value every lane read from shared memory, in a uniform register
-    auto info_of = [&](int i) {
-      return (int)__reduce_or_sync(0xffffffffu, (unsigned)*(volatile int*)&c.info[i & 7]);
-    };
-    int cur = ok ? info_of(0) : kInfoStop;
-    auto first_scores = [&](int info, int slot) {
-      if (info & kInfoA) {
-        ok = ok && wait_warp(c, p, &c.q_full[0], qph[0], 7);
-        qph[0] ^= 1;
-        tc_fence_after();
-        scores<0>(slot);
-        if (info & kInfoLastA) commit(&c.q_empty[0]);
-      }
-      if (info & kInfoB) {
-        ok = ok && wait_warp(c, p, &c.q_full[1], qph[1], 7);
-        qph[1] ^= 1;
-        tc_fence_after();
-        scores<1>(slot);
-        if (info & kInfoLastB) commit(&c.q_empty[1]);
-      }
-      commit(&c.empty[slot]);
-    };
-    if (!(cur & kInfoStop)) first_scores(cur, 0);
-    while (ok && !(cur & kInfoStop)) {
-      const int acc = cur & kInfoFirst ? 0 : 1;
-      // V of the tile
-      if (!CONV && (cur & kInfoFix)) {
-        ok = wait_warp(c, p, &c.fixed[fixes & 3], (uint32_t)((fixes >> 2) & 1), 7);
-        ++fixes;
-      } else {
-        ok = wait_warp(c, p, &c.full[vs], vph, 7);
-      }
-      int nks = ks + 2, nvs = vs + 2;
-      uint32_t nkph = kph, nvph = vph;
-      if (nks >= NS) { nks -= NS; nkph ^= 1; }
-      if (nvs >= NS) { nvs -= NS; nvph ^= 1; }
+  static __device__ __forceinline__ int slot_of(int e) { return e % NS; }
+
+  __device__ __forceinline__ bool key_there(int n) {   // without waiting
+    return __all_sync(0xffffffffu, mbar_test(&c.full[slot_of(2 * n)], (uint32_t)((2 * n / NS) & 1)));
+  }
+  __device__ __forceinline__ bool wait_key(int n) {
+    return wait_warp(c, p, &c.full[slot_of(2 * n)], (uint32_t)((2 * n / NS) & 1), 7);
+  }
+  // V of tile n with info w
+  __device__ __forceinline__ bool wait_value(int n, int w) {
+    if (!CONV && (w & kInfoFix)) {
+      const int f = fixes++;
+      return wait_warp(c, p, &c.fixed[f & 3], (uint32_t)((f >> 2) & 1), 7);
+    }
+    const int e = 2 * n + 1;
+    return wait_warp(c, p, &c.full[slot_of(e)], (uint32_t)((e / NS) & 1), 7);
+  }
+  // A tile's info, which every lane reads from shared memory, in a uniform
+  // register; valid once its K tile is there.
+  __device__ __forceinline__ int info_of(int n) const {
+    return (int)__reduce_or_sync(0xffffffffu, (unsigned)*(volatile int*)&c.info[n & 7]);
+  }
+  __device__ __forceinline__ bool wait_q(int x) {
+    const bool ok = wait_warp(c, p, &c.q_full[x], qph[x], 7);
+    qph[x] ^= 1;
+    tc_fence_after();
+    return ok;
+  }
+
+  // A segment whose first tile n has info w; n and w become those of the next
+  // segment's first tile (or the end's).  False after a timeout.
+  __device__ __forceinline__ bool dual(int& n, int& w) {
+    int slot = slot_of(2 * n);
+    if (w & kInfoA) {
+      if (!wait_q(0)) return false;
+      scores<0>(slot, 0);
+      if (w & kInfoLastA) commit(&c.q_empty[0]);
+    }
+    if (w & kInfoB) {
+      if (!wait_q(1)) return false;
+      scores<1>(slot, 1);
+      if (w & kInfoLastB) commit(&c.q_empty[1]);
+    }
+    commit(&c.empty[slot]);
+    int acc = 0;
+    for (;;) {
+      const int vs = slot_of(2 * n + 1);
+      if (!wait_value(n, w)) return false;
       // the next tile, if it is there already (else after P V of A)
-      bool known = __all_sync(0xffffffffu, mbar_test(&c.full[nks], nkph));
+      const bool known = key_there(n + 1);
       int next = known ? info_of(n + 1) : 0;
-      if (cur & kInfoA) {
-        ok = ok && wait_warp(c, p, &c.p_full[0], pph[0], 7);
-        if (!ok) break;
-        pph[0] ^= 1;
-        tc_fence_after();
-        values<0>(vs, acc);
-        if (cur & kInfoLastA) commit(&c.o_full[0]);
+      if (w & kInfoA) {
+        if (!values<0>(vs, acc)) return false;
+        if (w & kInfoLastA) commit(&c.o_full[0]);
       }
       if (!known) {
-        ok = ok && wait_warp(c, p, &c.full[nks], nkph, 7);
-        if (!ok) break;
+        if (!wait_key(n + 1)) return false;
         next = info_of(n + 1);
       }
-      const bool follows = !(next & (kInfoFirst | kInfoStop));
+      const bool follows = !(next & (kInfoStart | kInfoStop));
+      slot = slot_of(2 * n + 2);
       if (follows && (next & kInfoA)) {
         tc_fence_after();
-        scores<0>(nks);
+        scores<0>(slot, 0);
         if (next & kInfoLastA) commit(&c.q_empty[0]);
       }
-      if (cur & kInfoB) {
-        ok = wait_warp(c, p, &c.p_full[1], pph[1], 7);
-        if (!ok) break;
-        pph[1] ^= 1;
-        tc_fence_after();
-        values<1>(vs, acc);
-        if (cur & kInfoLastB) commit(&c.o_full[1]);
+      if (w & kInfoB) {
+        if (!values<1>(vs, acc)) return false;
+        if (w & kInfoLastB) commit(&c.o_full[1]);
       }
       commit(&c.empty[vs]);
-      if (follows) {
-        if (next & kInfoB) {
-          scores<1>(nks);
-          if (next & kInfoLastB) commit(&c.q_empty[1]);
-        }
-        commit(&c.empty[nks]);
-      } else if (!(next & kInfoStop)) {
-        first_scores(next, nks);
-      }
-      cur = next;
       ++n;
-      ks = nks; vs = nvs; kph = nkph; vph = nvph;
+      w = next;
+      if (!follows) return true;
+      if (next & kInfoB) {
+        tc_fence_after();
+        scores<1>(slot, 1);
+        if (next & kInfoLastB) commit(&c.q_empty[1]);
+      }
+      commit(&c.empty[slot]);
+      acc = 1;
     }
+  }
+
+  // S of X for tile n (info w) of a solo segment.
+  template <int X>
+  __device__ __forceinline__ void solo_scores(int n, int w) {
+    tc_fence_after();
+    scores<X>(slot_of(2 * n), 0);
+    commit(&c.empty[slot_of(2 * n)]);
+    if (w & kInfoEnd) commit(&c.q_empty[0]);
+  }
+
+  // P V of X for tile n (info w) of a solo segment.
+  template <int X>
+  __device__ __forceinline__ bool solo_values(int n, int w, int acc) {
+    const int vs = slot_of(2 * n + 1);
+    if (!wait_value(n, w) || !values<X>(vs, acc)) return false;
+    commit(&c.empty[vs]);
+    if (w & (X ? kInfoLastB : kInfoLastA)) commit(&c.o_full[X]);
+    return true;
+  }
+
+  // The same for a solo segment.
+  __device__ __forceinline__ bool solo(int& n, int& w) {
+    if (!wait_q(0)) return false;
+    solo_scores<0>(n, w);
+    int na = n++, wa = w, nb = 0, wb = 0;   // tiles whose P V is due
+    bool a_due = true, b_due = false, more = !(w & kInfoEnd);
+    int acc = 0;
+    if (more) {
+      if (!wait_key(n)) return false;
+      w = info_of(n);
+      solo_scores<1>(n, w);
+      nb = n++;
+      wb = w;
+      b_due = true;
+      more = !(w & kInfoEnd);
+    }
+    while (a_due || b_due) {
+      if (a_due) {
+        if (!solo_values<0>(na, wa, acc)) return false;
+        a_due = more;
+        if (more) {
+          if (!wait_key(n)) return false;
+          wa = info_of(n);
+          solo_scores<0>(n, wa);
+          na = n++;
+          more = !(wa & kInfoEnd);
+        }
+      }
+      if (b_due) {
+        if (!solo_values<1>(nb, wb, acc)) return false;
+        b_due = more;
+        if (more) {
+          if (!wait_key(n)) return false;
+          wb = info_of(n);
+          solo_scores<1>(n, wb);
+          nb = n++;
+          more = !(wb & kInfoEnd);
+        }
+      }
+      acc = 1;
+    }
+    if (!wait_key(n)) return false;
+    w = info_of(n);
+    return true;
+  }
+
+  __device__ __forceinline__ void run() {
+    int n = 0;
+    bool ok = wait_key(0);
+    int w = ok ? info_of(0) : kInfoStop;
+    while (ok && !(w & kInfoStop)) ok = w & kInfoSolo ? solo(n, w) : dual(n, w);
     // every issued product is done before the tensor memory is freed
     commit(&c.fin);
     if (!wait_drain(&c.fin) && lead) raise_error(p.at.ws, kErrDrain, 10);
@@ -998,264 +1116,484 @@ __device__ __forceinline__ void add_nonfinite(const Prefill& p, const Seg& seg, 
   }
 }
 
+// Turns 16-byte chunks among four neighbouring lanes: v[t] of lane 4 i + q
+// becomes v[q] of lane 4 i + t (two rounds of exchanges).
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4& keep0, uint4& keep1, int bit) {   // lanes without `bit` give keep1
+    uint4& give = lane & bit ? keep0 : keep1;
+    give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+    give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+    give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+    give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+  };
+  swap(v[0], v[1], 1);
+  swap(v[2], v[3], 1);
+  swap(v[0], v[2], 2);
+  swap(v[1], v[3], 2);
+}
+
 template <int D, int KV, bool CONV, bool BF16, bool TOK>
-__device__ __forceinline__ void softmax(const Prefill& p, const Plan& plan, Control& c, int X,
-                                        uint32_t tbase, const float* scales) {
-  // f16: P carries a factor 2^kLift (see the file comment)
-  constexpr float kLift = BF16 ? 0.f : 6.f;
-  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
-  const int r = 32 * w4 + lane;
-  const int rows = p.tile_tokens * p.group;
-  const int rtok = r / p.group, rhead = r - rtok * p.group;
-  const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);
-  const uint32_t tS = tl + X * kTile, tO = tl + 2 * kTile + X * kTile;
-  Walk walk;
-  walk.init(p, plan);
-  Seg seg;
-  int n = 0, done = 0, segs = 0, sn = 0;
+struct Softmax {
+  using SH = Shape<D, KV, CONV>;
   using SR = ScaleRing<D, KV>;
-  // streams of the two partial slots, for the merge
-  int4 used0 = make_int4(-1, 0, 0, 0), used1 = used0;
-  bool dead = false;
-  for (; !dead && walk.next(p, seg); ++sn) {
-    const int tok0 = (2 * seg.m + X) * p.tile_tokens;   // first token of the query tile
-    const int live_rows = min(rows, max(0, (seg.n - tok0) * p.group));
-    const bool mine = r < live_rows;
-    const bool warp_live = 32 * w4 < live_rows;
-    // keys this row sees; a row of nobody never restricts its warp
-    const int lim = mine ? max(0, seg.ctx + tok0 + rtok + 1) : 0x7fffffff;
-    const int te = min(seg.te, X ? seg.nt[1] : seg.nt[0]);
-    float sc = p.score_scale, vsc = p.v_scale;
-    if (KV != 0 && p.scale_kind == FD_SCALE_HEAD) {
-      sc *= __ldg(p.k_scales + seg.h);
-      vsc *= __ldg(p.v_scales + seg.h);
+  // f16: P carries a factor 2^kLift (see the file comment)
+  static constexpr float kLift = BF16 ? 0.f : 6.f;
+  // exchange of a solo segment: dims per round, and where the states' (m, l) go
+  static constexpr int kRound = D / 4;
+  static constexpr uint32_t kOffMl = SH::kQTile / 2;
+
+  const Prefill& p;
+  Control& c;
+  uint8_t* base;
+  const float* scales;
+  int X, lane, w4, r;
+  uint32_t tS, tO;
+  // the row's state in the segment
+  float m_ref, l, sc;
+  int vexp;   // TOK with f16: P carries 2^-vexp against the V scales
+
+  __device__ __forceinline__ static void fetch(uint32_t tS, float (&x)[32], int k) {
+    tmem_ld32<128>(tS + 32 * k, x);
+  }
+  // the loads before this have arrived: nothing may read x earlier
+  __device__ __forceinline__ static void arrived(float (&x)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(x[i]));
+  }
+  // scores 32 k .. 32 k + 31 into log2 units by their keys' scales
+  __device__ __forceinline__ static void key_scales(float (&x)[32], const float* ks) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      uint64_t k01, k23;
+      lds_pairs(ks + i, k01, k23);
+      const float2 u = unpack2(mul2(pack2(x[i], x[i + 1]), k01));
+      const float2 v = unpack2(mul2(pack2(x[i + 2], x[i + 3]), k23));
+      x[i] = u.x;
+      x[i + 1] = u.y;
+      x[i + 2] = v.x;
+      x[i + 3] = v.y;
     }
-    float m_ref = -INFINITY, l = 0.f;
-    int vexp = -1000;   // TOK with f16: P carries 2^-vexp against the V scales
-    for (int j = seg.tb; j < te; ++j, ++done) {
-      const int jn = n + (j - seg.tb);   // tile of the CTA
-      if (!wait_warp(c, p, &c.s_full[X], (uint32_t)(done & 1), 11)) {
-        dead = true;
-        break;
+  }
+  // off the straight path: the sign of the scale, and -inf for keys that the
+  // row does not see (`left` of the 32)
+  __device__ __forceinline__ void exclude(float (&x)[32], int left) const {
+    if (!TOK && sc <= 0.f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = sc == 0.f ? 0.f : -x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i < left ? x[i] : -INFINITY;
+  }
+  __device__ __forceinline__ static void row_max(const float (&x)[32], float (&mx)[4]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], x[i + 2 * k], x[i + 2 * k + 1]);
+    }
+  }
+  // P of scores 32 k .. into 16 columns of tensor memory, over scores that
+  // were read before; their sum into `sum`.
+  __device__ __forceinline__ void exponents(const float (&x)[32], int k, uint64_t sc2, uint64_t nm2,
+                                            uint64_t vm2, const float* vs, int left, bool all,
+                                            uint64_t (&sum)[4]) const {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float2 u = unpack2(fma2(pack2(x[i], x[i + 1]), sc2, nm2));
+      const float2 v = unpack2(fma2(pack2(x[i + 2], x[i + 3]), sc2, nm2));
+      uint64_t pa = pack2(fast_exp2(u.x), fast_exp2(u.y));
+      uint64_t pb = pack2(fast_exp2(v.x), fast_exp2(v.y));
+      sum[(i >> 1) & 2] = add2(sum[(i >> 1) & 2], pa);
+      sum[((i >> 1) & 2) + 1] = add2(sum[((i >> 1) & 2) + 1], pb);
+      if constexpr (TOK) {
+        uint64_t va, vb;
+        lds_pairs(vs + 32 * k + i, va, vb);
+        pa = mul2(pa, BF16 ? va : mul2(va, vm2));
+        pb = mul2(pb, BF16 ? vb : mul2(vb, vm2));
       }
-      tc_fence_after();
-      if (warp_live) {
-        float s[kTile];
-        {
-          float x[32];
+      float2 qa = unpack2(pa), qb = unpack2(pb);
+      if (TOK && !all) {   // 0 times an excluded key's scale, whatever that is
+        const int t = 32 * k + i;
+        qa.x = t < left ? qa.x : 0.f;
+        qa.y = t + 1 < left ? qa.y : 0.f;
+        qb.x = t + 2 < left ? qb.x : 0.f;
+        qb.y = t + 3 < left ? qb.y : 0.f;
+      }
+      pk[i / 2] = pack16<BF16>(qa.x, qa.y);
+      pk[i / 2 + 1] = pack16<BF16>(qb.x, qb.y);
+    }
+    tmem_st16u(tS + 16 * k, pk);
+  }
+
+  // P is in tensor memory up to here: one of this warp's two arrivals a tile.
+  __device__ __forceinline__ void publish(uint64_t* bar) const {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+
+  // One tile (tile jn of the CTA), of whose 128 keys the row sees the first
+  // `left`.  False after a timeout.  The scores are read from tensor memory
+  // twice, 32 at a time: a thread that kept all 128 would spill.
+  __device__ __forceinline__ bool tile(int jn, int left, bool fresh, bool mine) {
+    const bool whole = __all_sync(0xffffffffu, left == kTile);
+    const float* ks = scales + SR::key(jn);   // written before the tile's S was issued
+    const float* vs = scales + SR::val(jn);
+    // |sc| is factored out of the scores (a negative scale: the maximum of -s
+    // is sought; zero: all scores alike, as 0 * -inf would not be)
+    const float scl = TOK || sc == 0.f ? 1.f : fabsf(sc);
+    // tiles whose keys every row of the warp sees take a straight path
+    const bool fast = whole && (TOK || sc > 0.f);
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (fast) {
+      float x[2][32];
+      fetch(tS, x[0], 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            tmem_ld32<128>(tS + 32 * k, x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[32 * k + i] = x[i];
-          }
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) asm volatile("" : "+f"(s[i]));
-        }
-        const bool bad = (*(volatile int*)&c.info[jn & 7] & kInfoBad) != 0;
-        const int left = bad ? 0 : max(0, min(kTile, lim - j * kTile));
-        const bool whole = __all_sync(0xffffffffu, left == kTile);
-        const float* vscl = scales + SR::val(jn);
-        if constexpr (TOK) {   // scores in log2 units, token by token
-          const float* ksc = scales + SR::key(jn);   // written before the tile's S was issued
-#pragma unroll
-          for (int i = 0; i < kTile; i += 4) {
-            uint64_t k01, k23;
-            lds_pairs(ksc + i, k01, k23);
-            const float2 a = unpack2(mul2(pack2(s[i], s[i + 1]), k01));
-            const float2 b = unpack2(mul2(pack2(s[i + 2], s[i + 3]), k23));
-            s[i] = a.x;
-            s[i + 1] = a.y;
-            s[i + 2] = b.x;
-            s[i + 3] = b.y;
-          }
-        } else if (sc < 0.f) {   // a negative scale: the maximum of -s is sought
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = -s[i];
-        }
-        float scl = TOK ? 1.f : fabsf(sc);
-        if (!TOK && scl == 0.f) {   // all scores alike (0 * -inf would not be)
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = 0.f;
-          scl = 1.f;
-        }
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = i < left ? s[i] : -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i + 7 < kTile; i += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[kTile - 4 + k]);
-        const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float mt = smax == -INFINITY ? -INFINITY : smax * scl;
-        float fac = 1.f;
-        bool resc = false;
-        if (mt > m_ref + 8.f || m_ref == -INFINITY) {
-          if (m_ref != -INFINITY) {
-            fac = exp2f(m_ref - mt);
-            l *= fac;
-            resc = mine;
-          }
-          m_ref = mt;
-        }
-        float vmul = 1.f;
-        if constexpr (TOK) {
-          if (!wait_warp(c, p, &c.fixed[jn % SR::kValRing], (uint32_t)((jn / SR::kValRing) & 1),
-                         12)) {
-            dead = true;
-            break;
-          }
-          if constexpr (!BF16) {
-            // largest V scale of the tile -> its exponent; P stays below 2^15
-            float vm = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vscl[lane + 32 * i]));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-            int ev = (int)((__float_as_uint(vm) >> 23) & 255u) - 127;
-            ev = max(-120, min(120, ev));
-            if (ev > vexp) {
-              if (j > seg.tb) {
-                fac *= exp2f((float)max(vexp - ev, -200));
-                resc = true;
-              }
-              vexp = ev;
-            }
-            vmul = exp2f((float)-vexp);
-          }
-        }
-        if (__any_sync(0xffffffffu, resc)) {
-          // the S commit that ended the wait above follows the last P V
+      for (int k = 0; k < 4; ++k) {
+        tmem_wait_ld();
+        arrived(x[k & 1]);
+        if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
+        if constexpr (TOK) key_scales(x[k & 1], ks + 32 * k);
+        row_max(x[k & 1], mx);
+      }
+    } else {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld32<128>(tO + c0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= fac;
-            tmem_st32<128>(tO + c0, o);
-          }
-          tmem_wait_st();
-        }
-        // P = 2^(s - m_ref + kLift); excluded scores are -inf and give 0 (a
-        // row that has seen no key has m_ref = -inf: everything is excluded)
-        const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
-        const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm), vm2 = pack2(vmul, vmul);
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const int k = 32 * q4 + 2 * i;
-            const float2 x = unpack2(fma2(pack2(s[k], s[k + 1]), sc2, nm2));
-            const float2 y = unpack2(fma2(pack2(s[k + 2], s[k + 3]), sc2, nm2));
-            uint64_t pa = pack2(fast_exp2(x.x), fast_exp2(x.y));
-            uint64_t pb = pack2(fast_exp2(y.x), fast_exp2(y.y));
-            sum[i & 2] = add2(sum[i & 2], pa);
-            sum[(i & 2) + 1] = add2(sum[(i & 2) + 1], pb);
-            if constexpr (TOK) {
-              uint64_t va, vb;
-              lds_pairs(vscl + k, va, vb);
-              pa = mul2(pa, BF16 ? va : mul2(va, vm2));
-              pb = mul2(pb, BF16 ? vb : mul2(vb, vm2));
-            }
-            const float2 qa = unpack2(pa), qb = unpack2(pb);
-            pk[i] = pack16<BF16>(qa.x, qa.y);
-            pk[i + 1] = pack16<BF16>(qb.x, qb.y);
-          }
-          tmem_st16u(tS + 16 * q4, pk);
-        }
-        const float2 sa = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-        l += sa.x + sa.y;
-        tmem_wait_st();
+      for (int k = 0; k < 4; ++k) {
+        float x[32];
+        fetch(tS, x, k);
+        tmem_wait_ld();
+        arrived(x);
+        if constexpr (TOK) key_scales(x, ks + 32 * k);
+        exclude(x, left - 32 * k);
+        row_max(x, mx);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.p_full[X]);
     }
-    if (dead) break;
-    n += seg.te - seg.tb;
-    // ------------------------------------------------------------ segment end
-    const bool any = seg.tb < te;   // O of this query tile was accumulated
-    if (any) {
-      if (!wait_warp(c, p, &c.o_full[X], (uint32_t)(segs & 1), 15)) {
-        dead = true;
-        break;
+    const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    const float mt = smax == -INFINITY ? -INFINITY : smax * scl;
+    float fac = 1.f;
+    bool resc = false;
+    if (mt > m_ref + 8.f || m_ref == -INFINITY) {
+      if (m_ref != -INFINITY) {
+        fac = exp2f(m_ref - mt);
+        l *= fac;
+        resc = mine;
       }
-      ++segs;
-      tc_fence_after();
+      m_ref = mt;
     }
-    if (!seg.complete) {
-      if (seg.slot & 1) used1 = make_int4(seg.b, seg.h, seg.m, 0);
-      else used0 = make_int4(seg.b, seg.h, seg.m, 0);
+    float vmul = 1.f;
+    if constexpr (TOK) {
+      if (!wait_warp(c, p, &c.fixed[jn % SR::kValRing], (uint32_t)((jn / SR::kValRing) & 1), 12))
+        return false;
+      if constexpr (!BF16) {
+        // largest V scale of the tile -> its exponent; P stays below 2^15
+        float vm = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vs[lane + 32 * i]));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        int ev = (int)((__float_as_uint(vm) >> 23) & 255u) - 127;
+        ev = max(-120, min(120, ev));
+        if (ev > vexp) {
+          if (!fresh) {
+            fac *= exp2f((float)max(vexp - ev, -200));
+            resc = true;
+          }
+          vexp = ev;
+        }
+        vmul = exp2f((float)-vexp);
+      }
     }
-    const float m_out = m_ref == -INFINITY ? -INFINITY : m_ref - kLift;
-    float osc = 1.f;
-    if constexpr (TOK && !BF16) osc = vexp > -1000 ? exp2f((float)vexp) : 1.f;
-    if (seg.complete) osc *= l > 0.f ? vsc / l : 0.f;
-    const long long orow = (long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
-                           (long long)seg.h * p.group + rhead;
-    const long long prow = (long long)seg.slot * kRowsPair + X * kRowsTile + r;
-    const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
-    if (warp_live) {
+    if (__any_sync(0xffffffffu, resc)) {
+      // the S commit that the caller waited for follows the last P V
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
-        if (any) {
-          tmem_ld32<128>(tO + c0, o);
-          tmem_wait_ld();
-        } else {
+        tmem_ld32<128>(tO + c0, o);
+        tmem_wait_ld();
+        arrived(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (KV != 2 && nonfinite && mine) {
-          float x[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = o[i];
-          const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
-          add_nonfinite<D, KV, BF16>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = x[i];
-        }
-        if (!mine) continue;
-        if (seg.complete) {
-          uint16_t* op = static_cast<uint16_t*>(p.out) + orow * D + c0;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(op + i) =
-                make_uint4(pack16<BF16>(o[i] * osc, o[i + 1] * osc),
-                           pack16<BF16>(o[i + 2] * osc, o[i + 3] * osc),
-                           pack16<BF16>(o[i + 4] * osc, o[i + 5] * osc),
-                           pack16<BF16>(o[i + 6] * osc, o[i + 7] * osc));
-        } else {
-          float* pa = p.part_acc + prow * D + c0;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(pa + i) =
-                make_float4(o[i] * osc, o[i + 1] * osc, o[i + 2] * osc, o[i + 3] * osc);
-        }
+        for (int i = 0; i < 32; ++i) o[i] *= fac;
+        tmem_st32<128>(tO + c0, o);
       }
-      if (mine) {
-        if (!seg.complete) p.part_ml[prow] = make_float2(m_out, l);
-        else if (p.lse) p.lse[orow] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
+      tmem_wait_st();
+    }
+    // P = 2^(s - m_ref + kLift); excluded scores are -inf and give 0 (a row
+    // that has seen no key has m_ref = -inf: everything is excluded)
+    const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
+    const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm), vm2 = pack2(vmul, vmul);
+    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    if (fast) {
+      float x[2][32];
+      fetch(tS, x[0], 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        tmem_wait_ld();
+        arrived(x[k & 1]);
+        if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
+        if constexpr (TOK) key_scales(x[k & 1], ks + 32 * k);
+        exponents(x[k & 1], k, sc2, nm2, vm2, vs, left, true, sum);
+        if (k == 1) publish(&c.p_half[X]);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        float x[32];
+        fetch(tS, x, k);
+        tmem_wait_ld();
+        arrived(x);
+        if constexpr (TOK) key_scales(x, ks + 32 * k);
+        exclude(x, left - 32 * k);
+        exponents(x, k, sc2, nm2, vm2, vs, left, false, sum);
+        if (k == 1) publish(&c.p_half[X]);
       }
     }
-    tc_fence_before();
+    publish(&c.p_full[X]);
+    const float2 sa = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+    l += sa.x + sa.y;
+    return true;
   }
-  if (X == 0 && r == 0) {
-    // after a timeout nothing is merged: the outputs are undefined
-    if (dead) used0.x = used1.x = -1;
-    p.meta[2 * blockIdx.x] = used0;
-    p.meta[2 * blockIdx.x + 1] = used1;
+
+  // Solo segments: A merges B's state (m, l, O) into its own, in rounds of
+  // kRound dims through query tile B's place.  `o` takes A's dims as they are
+  // read from tensor memory.
+  __device__ __forceinline__ float4* swap_at(int d4) const {
+    return reinterpret_cast<float4*>(base + SH::kQTile) + d4 * kRowsTile + r;
   }
-}
+
+  __device__ void run(const Plan& plan) {
+    const int rows = p.tile_tokens * p.group;
+    const int rtok = r / p.group, rhead = r - rtok * p.group;
+    Walk walk;
+    walk.init(p, plan);
+    Seg seg;
+    int n = 0, done = 0, segs = 0, sn = 0;
+    uint32_t xph = 0;   // phase of the exchange barriers
+    // streams of the two partial slots, for the merge
+    int4 used0 = make_int4(-1, 0, 0, 0), used1 = used0;
+    bool dead = false;
+    for (; !dead && walk.next(p, seg); ++sn) {
+      const int qt = seg.solo ? 0 : X;                     // query tile of this half
+      const int tok0 = (2 * seg.m + qt) * p.tile_tokens;   // its first token
+      const int live_rows = min(rows, max(0, (seg.n - tok0) * p.group));
+      const bool mine = r < live_rows;
+      const bool warp_live = 32 * w4 < live_rows;
+      // keys this row sees; a row of nobody never restricts its warp
+      const int lim = mine ? max(0, seg.ctx + tok0 + rtok + 1) : 0x7fffffff;
+      const int te = min(seg.te, qt ? seg.nt[1] : seg.nt[0]);
+      const int first = seg.tb + (seg.solo ? X : 0), step = seg.solo ? 2 : 1;
+      float vsc = p.v_scale;
+      sc = p.score_scale;
+      if (KV != 0 && p.scale_kind == FD_SCALE_HEAD) {
+        sc *= __ldg(p.k_scales + seg.h);
+        vsc *= __ldg(p.v_scales + seg.h);
+      }
+      m_ref = -INFINITY;
+      l = 0.f;
+      vexp = -1000;
+      for (int j = first; j < te; j += step, ++done) {
+        const int jn = n + (j - seg.tb);   // tile of the CTA
+        if (!wait_warp(c, p, &c.s_full[X], (uint32_t)(done & 1), 11)) {
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          const bool bad = (*(volatile int*)&c.info[jn & 7] & kInfoBad) != 0;
+          if (!tile(jn, bad ? 0 : max(0, min(kTile, lim - j * kTile)), j == first, mine)) {
+            dead = true;
+            break;
+          }
+        } else {   // no row of this warp: P may be anything
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&c.p_half[X]);
+            mbar_arrive(&c.p_full[X]);
+          }
+        }
+      }
+      if (dead) break;
+      n += seg.te - seg.tb;
+      // ---------------------------------------------------------- segment end
+      const bool any = first < te;   // O of this half was accumulated
+      if (any) {
+        if (!wait_warp(c, p, &c.o_full[X], (uint32_t)(segs & 1), 15)) {
+          dead = true;
+          break;
+        }
+        ++segs;
+        tc_fence_after();
+      }
+      if (!seg.complete) {
+        if (seg.slot & 1) used1 = make_int4(seg.b, seg.h, seg.m, 0);
+        else used0 = make_int4(seg.b, seg.h, seg.m, 0);
+      }
+      float m_out = m_ref == -INFINITY ? -INFINITY : m_ref - kLift;
+      float osc = 1.f;   // of this half's O
+      if constexpr (TOK && !BF16) osc = vexp > -1000 ? exp2f((float)vexp) : 1.f;
+      const bool swap = swaps_in(seg);
+      float bsc = 0.f;   // of the other half's O (A of a solo segment)
+      if (swap) {
+        float2* ml = reinterpret_cast<float2*>(base + SH::kQTile + kOffMl) + r;
+        if (X == 1) {
+          *ml = make_float2(m_out, l);
+          for (int q = 0; q < 4 && !dead; ++q) {   // rounds of kRound dims
+            if (warp_live) {
+#pragma unroll
+              for (int d0 = 0; d0 < kRound; d0 += 16) {
+                float o[16];
+                load16(tO + q * kRound + d0, o);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  *swap_at((d0 + i) / 4) =
+                      make_float4(o[i] * osc, o[i + 1] * osc, o[i + 2] * osc, o[i + 3] * osc);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.x_full);
+            dead = !wait_warp(c, p, &c.x_empty, xph, 16);
+            xph ^= 1;
+          }
+          if (dead) break;
+          fence_async_smem();   // a later query tile B lands here
+          if (w4 == 0 && lane == 0) *(volatile int*)&c.swaps = c.swaps + 1;
+        } else {
+          if (!wait_warp(c, p, &c.x_full, xph, 17)) {
+            dead = true;
+            break;
+          }
+          const float2 b = *ml;
+          const float M = fmaxf(m_out, b.x);
+          const float fa = m_out == -INFINITY ? 0.f : fast_exp2(m_out - M);
+          bsc = b.x == -INFINITY ? 0.f : fast_exp2(b.x - M);
+          l = l * fa + b.y * bsc;
+          osc *= fa;
+          m_out = M;
+        }
+      }
+      const bool writes = !(seg.solo && X == 1);
+      if (seg.complete) {
+        const float q = l > 0.f ? vsc / l : 0.f;
+        osc *= q;
+        bsc *= q;
+      }
+      const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
+      if (writes && (warp_live || swap)) {
+        const int lane4 = lane & 3, row4 = r & ~3;
+        // output rows of this lane's four neighbours (their chunks are turned)
+        long long orow[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int rt = (row4 + t) / p.group;
+          orow[t] = (long long)(seg.q0 + tok0 + rt) * p.num_q_heads + (long long)seg.h * p.group +
+                    (row4 + t - rt * p.group);
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          if (any && warp_live) {
+            tmem_ld32<128>(tO + c0, o);
+            tmem_wait_ld();
+            arrived(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= osc;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (swap) {   // 32 dims are one round, or two of 16
+#pragma unroll
+            for (int q = 0; q < 32 / kRound; ++q) {
+              const int round = c0 / kRound + q;
+              if (round > 0) dead = dead || !wait_warp(c, p, &c.x_full, xph, 17);
+              xph ^= 1;
+              if (warp_live && bsc != 0.f) {
+#pragma unroll
+                for (int i = 0; i < kRound; i += 4) {
+                  const float4 y = *swap_at(i / 4);
+                  const int k = q * kRound + i;
+                  o[k] = fmaf(y.x, bsc, o[k]);
+                  o[k + 1] = fmaf(y.y, bsc, o[k + 1]);
+                  o[k + 2] = fmaf(y.z, bsc, o[k + 2]);
+                  o[k + 3] = fmaf(y.w, bsc, o[k + 3]);
+                }
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&c.x_empty);
+            }
+          }
+          if (!warp_live) continue;
+          if (KV != 2 && nonfinite && mine) {
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = o[i];
+            const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
+            add_nonfinite<D, KV, BF16>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = x[i];
+          }
+          if (seg.complete) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = make_uint4(pack16<BF16>(o[8 * i], o[8 * i + 1]),
+                                pack16<BF16>(o[8 * i + 2], o[8 * i + 3]),
+                                pack16<BF16>(o[8 * i + 4], o[8 * i + 5]),
+                                pack16<BF16>(o[8 * i + 6], o[8 * i + 7]));
+            transpose4(v, lane);   // four lanes write 64 bytes of one row
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              if (row4 + t < live_rows)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow[t] * D + c0 +
+                                          8 * lane4) = v[t];
+          } else if (mine) {
+            // partial states: [slot][query tile][dim / 4][row][4]
+            float4* pa = reinterpret_cast<float4*>(p.part_acc) +
+                         ((long long)(2 * seg.slot + qt) * (D / 4) + c0 / 4) * kRowsTile + r;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              pa[(i / 4) * kRowsTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (mine) {
+          if (!seg.complete) {
+            p.part_ml[(long long)(2 * seg.slot + qt) * kRowsTile + r] = make_float2(m_out, l);
+          } else if (p.lse) {
+            const long long at = (long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
+                                 (long long)seg.h * p.group + rhead;
+            p.lse[at] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    if (X == 0 && r == 0) {
+      // after a timeout nothing is merged: the outputs are undefined
+      if (dead) used0.x = used1.x = -1;
+      p.meta[2 * blockIdx.x] = used0;
+      p.meta[2 * blockIdx.x + 1] = used1;
+    }
+  }
+
+  __device__ __forceinline__ static void load16(uint32_t taddr, float (&v)[16]) {
+    uint32_t w[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7]), "=r"(w[8]), "=r"(w[9]), "=r"(w[10]), "=r"(w[11]), "=r"(w[12]), "=r"(w[13]),
+          "=r"(w[14]), "=r"(w[15])
+        : "r"(taddr));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = __uint_as_float(w[i]);
+      asm volatile("" : "+f"(v[i]));
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // The kernel
@@ -1288,12 +1626,16 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
       mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_half[i], 4);
       mbar_init(&c.p_full[i], 4);
       mbar_init(&c.o_full[i], 1);
     }
     mbar_init(&c.fin, 1);
+    mbar_init(&c.x_full, 4);
+    mbar_init(&c.x_empty, 4);
     for (int i = 0; i < 8; ++i) c.info[i] = c.nf[i] = 0;
     c.abort_flag = 0;
+    c.swaps = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -1316,23 +1658,25 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   const uint32_t tbase = c.tmem_base;
   allow_dependent_launch();
 
-  // Registers: the softmax threads hold 128 scores each.  The shares add up
-  // to the launch's registers (168 x 384; 128 x 512).
+  // The register shares add up to the launch's registers (168 x 384; 128 x 512).
   if (warp < 8) {
-    reg_inc<CONV ? 176 : 208>();
-    softmax<D, KV, CONV, BF16, TOK>(p, plan, c, warp >> 2, tbase, scales);
+    reg_inc<CONV ? 144 : 208>();
+    const int X = warp >> 2, w4 = warp & 3, lane = threadIdx.x & 31;
+    const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);
+    Softmax<D, KV, CONV, BF16, TOK> sm{p, c, base, scales, X, lane, w4, 32 * w4 + lane,
+                                       tl + X * kTile, tl + (2 + X) * kTile};
+    sm.run(plan);
   } else if (warp < kConvWarp0) {
-    reg_dec<CONV ? 64 : 88>();
+    reg_dec<CONV ? 96 : 88>();
     if (warp == kProducerWarp) {
       producer<D, KV, CONV>(p, plan, c, base, &tmq, &tmk, &tmv);
     } else if (warp == kMmaWarp) {
-      Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one()};
+      Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one(), {0, 0}, {0, 0}, 0};
       mm.run();
     } else if constexpr (!CONV) {
       fixers<D, BF16>(p, plan, c, base);
     }
   } else if constexpr (CONV) {
-    reg_dec<96>();
     converters<D, KV, BF16, TOK>(p, plan, c, base, scales);
   }
   tc_fence_before();

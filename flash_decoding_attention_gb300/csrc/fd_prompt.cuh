@@ -111,9 +111,9 @@ struct Prefill {
   int tile_tokens;     // tokens of a 128-row query tile: 128 / group
   int gather;          // pages too small for TMA boxes: rows copied by threads
   // workspace: partial states of streams cut between CTAs
-  int4* meta;          // [grid][2]: stream {sequence, KV head, tile pair, rows} of a slot
-  float2* part_ml;     // [grid][2][256]
-  float* part_acc;     // [grid][2][256][head_dim]
+  int4* meta;          // [grid][2]: stream {sequence, KV head, tile pair} of a slot
+  float2* part_ml;     // [grid][2][query tile][128 rows]: m (log2 units), l
+  float* part_acc;     // [grid][2][query tile][head_dim / 4][128 rows][4]
 };
 
 struct PrefillLayout {
