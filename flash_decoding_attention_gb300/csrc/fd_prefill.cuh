@@ -70,7 +70,7 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
 constexpr int kPages = 20;          // block-table entries staged at a time (a tile has 16)
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
 // Cost of a segment start (Q load, first product, epilogue), in keys.
-constexpr long long kStartCost = 256;
+constexpr long long kStartCost = 640;
 
 // ---------------------------------------------------------------------------
 // Streams and their split
@@ -352,7 +352,7 @@ __device__ __forceinline__ void record_abort(Control& c, const Prefill& p, int r
   }
 }
 
-__device__ __forceinline__ bool wait_slow(Control& c, const Prefill& p, uint64_t* bar,
+static __device__ __noinline__ bool wait_slow(Control& c, const Prefill& p, uint64_t* bar,
                                        uint32_t parity, int role) {
   if (aborted(c)) return false;
   if (mbar_wait(bar, parity, p.wait_ns)) return true;
@@ -503,7 +503,7 @@ struct TileCopy {
 };
 
 template <int D, int KV, bool CONV>
-__device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Control& c,
+__device__ __forceinline__ void producer(const Prefill& p, Walk walk, Control& c,
                                          uint8_t* base, const CUtensorMap* tmq,
                                          const CUtensorMap* tmk, const CUtensorMap* tmv) {
   using SH = Shape<D, KV, CONV>;
@@ -518,8 +518,6 @@ __device__ __forceinline__ void producer(const Prefill& p, const Plan& plan, Con
   const bool tiles = !p.gather;   // gathered rows are the converters' business
   uint64_t keep;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-  Walk walk;
-  walk.init(p, plan);
   Seg seg;
   int n = 0, qn[2] = {0, 0}, swaps = 0;
   bool stop = p.starve != 0;
@@ -887,13 +885,11 @@ struct Mma {
 // Repair of V tiles in the ring (16-bit caches by TMA)
 // ---------------------------------------------------------------------------
 template <int D, bool BF16>
-__device__ __forceinline__ void fixers(const Prefill& p, const Plan& plan, Control& c,
+__device__ __forceinline__ void fixers(const Prefill& p, Walk walk, Control& c,
                                        uint8_t* base) {
   using SH = Shape<D, 0, false>;
   constexpr int NS = SH::kSlots;
   const int lane = threadIdx.x & 31, ft = threadIdx.x - kFixWarp0 * 32;
-  Walk walk;
-  walk.init(p, plan);
   Seg seg;
   int n = 0, fixes = 0, sn = 0;
   for (; walk.next(p, seg); ++sn) {
@@ -911,7 +907,7 @@ __device__ __forceinline__ void fixers(const Prefill& p, const Plan& plan, Contr
           const int items = (kTile - from) * 8;
 #pragma unroll
           for (int d = 0; d < D / 64; ++d) {
-#pragma unroll 4
+#pragma unroll 2
             for (int i = ft; i < items; i += 64) {
               const int r = from + (i >> 3);
               uint4* at = reinterpret_cast<uint4*>(v + d * (kTile * 128) + r * 128 + (i & 7) * 16);
@@ -947,7 +943,7 @@ __device__ __forceinline__ void fixers(const Prefill& p, const Plan& plan, Contr
 // Converter warps: thread = key of the tile
 // ---------------------------------------------------------------------------
 template <int D, int KV, bool BF16, bool TOK>
-__device__ __forceinline__ void converters(const Prefill& p, const Plan& plan, Control& c,
+__device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control& c,
                                            uint8_t* base, float* scales) {
   using SH = Shape<D, KV, true>;
   constexpr int NS = SH::kSlots;
@@ -975,8 +971,6 @@ __device__ __forceinline__ void converters(const Prefill& p, const Plan& plan, C
                                            : start + k;
     return row >= 0 && row < p.at.kv_rows ? row : -1;
   };
-  Walk walk;
-  walk.init(p, plan);
   Seg seg;
   int n = 0, sn = 0;
   for (; walk.next(p, seg); ++sn) {
@@ -1243,10 +1237,28 @@ struct Softmax {
     // |sc| is factored out of the scores (a negative scale: the maximum of -s
     // is sought; zero: all scores alike, as 0 * -inf would not be)
     const float scl = TOK || sc == 0.f ? 1.f : fabsf(sc);
-    // tiles whose keys every row of the warp sees take a straight path
+    // Other tiles than those whose keys every row of the warp sees (or with
+    // the scale's sign turned) are put right in tensor memory first, so that
+    // one stretch of code, kept in the instruction cache, serves all.  (With
+    // per-token scales, which may be anything for unseen keys, they have a
+    // path of their own.)
     const bool fast = whole && (TOK || sc > 0.f);
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (fast) {
+    if (!fast) {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        float x[32];
+        fetch(tS, x, k);
+        tmem_wait_ld();
+        arrived(x);
+        if constexpr (TOK) key_scales(x, ks + 32 * k);
+        exclude(x, left - 32 * k);
+        if constexpr (TOK) row_max(x, mx);
+        else tmem_st32<128>(tS + 32 * k, x);
+      }
+      if constexpr (!TOK) tmem_wait_st();
+    }
+    if (!TOK || fast) {
       float x[2][32];
       fetch(tS, x[0], 0);
 #pragma unroll
@@ -1256,17 +1268,6 @@ struct Softmax {
         if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
         if constexpr (TOK) key_scales(x[k & 1], ks + 32 * k);
         row_max(x[k & 1], mx);
-      }
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        float x[32];
-        fetch(tS, x, k);
-        tmem_wait_ld();
-        arrived(x);
-        if constexpr (TOK) key_scales(x, ks + 32 * k);
-        exclude(x, left - 32 * k);
-        row_max(x, mx);
       }
     }
     const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -1323,7 +1324,7 @@ struct Softmax {
     const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
     const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm), vm2 = pack2(vmul, vmul);
     uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-    if (fast) {
+    if (!TOK || fast) {
       float x[2][32];
       fetch(tS, x[0], 0);
 #pragma unroll
@@ -1361,11 +1362,9 @@ struct Softmax {
     return reinterpret_cast<float4*>(base + SH::kQTile) + d4 * kRowsTile + r;
   }
 
-  __device__ void run(const Plan& plan) {
+  __device__ void run(Walk walk) {
     const int rows = p.tile_tokens * p.group;
     const int rtok = r / p.group, rhead = r - rtok * p.group;
-    Walk walk;
-    walk.init(p, plan);
     Seg seg;
     int n = 0, done = 0, segs = 0, sn = 0;
     uint32_t xph = 0;   // phase of the exchange barriers
@@ -1655,29 +1654,29 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   tc_fence_before();
   const Plan plan = make_plan(p, reinterpret_cast<long long*>(base));   // (barriers)
   tc_fence_after();
+  Walk walk;   // every role walks its own copy
+  walk.init(p, plan);
   const uint32_t tbase = c.tmem_base;
   allow_dependent_launch();
 
   // The register shares add up to the launch's registers (168 x 384; 128 x 512).
   if (warp < 8) {
-    reg_inc<CONV ? 144 : 208>();
     const int X = warp >> 2, w4 = warp & 3, lane = threadIdx.x & 31;
     const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);
     Softmax<D, KV, CONV, BF16, TOK> sm{p, c, base, scales, X, lane, w4, 32 * w4 + lane,
                                        tl + X * kTile, tl + (2 + X) * kTile};
-    sm.run(plan);
+    sm.run(walk);
   } else if (warp < kConvWarp0) {
-    reg_dec<CONV ? 96 : 88>();
     if (warp == kProducerWarp) {
-      producer<D, KV, CONV>(p, plan, c, base, &tmq, &tmk, &tmv);
+      producer<D, KV, CONV>(p, walk, c, base, &tmq, &tmk, &tmv);
     } else if (warp == kMmaWarp) {
       Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one(), {0, 0}, {0, 0}, 0};
       mm.run();
     } else if constexpr (!CONV) {
-      fixers<D, BF16>(p, plan, c, base);
+      fixers<D, BF16>(p, walk, c, base);
     }
   } else if constexpr (CONV) {
-    converters<D, KV, BF16, TOK>(p, plan, c, base, scales);
+    converters<D, KV, BF16, TOK>(p, walk, c, base, scales);
   }
   tc_fence_before();
   __syncthreads();
