@@ -1479,15 +1479,11 @@ struct Softmax {
       }
       const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
       if (writes && (warp_live || swap)) {
+        // this row's place in the output; its lane's four neighbours write each
+        // other's rows, their chunks turned
         const int lane4 = lane & 3, row4 = r & ~3;
-        // output rows of this lane's four neighbours (their chunks are turned)
-        long long orow[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int rt = (row4 + t) / p.group;
-          orow[t] = (long long)(seg.q0 + tok0 + rt) * p.num_q_heads + (long long)seg.h * p.group +
-                    (row4 + t - rt * p.group);
-        }
+        const long long mine_at = ((long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
+                                   (long long)seg.h * p.group + rhead) * D;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
@@ -1543,10 +1539,12 @@ struct Softmax {
                                 pack16<BF16>(o[8 * i + 6], o[8 * i + 7]));
             transpose4(v, lane);   // four lanes write 64 bytes of one row
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t) {
+              const long long at = __shfl_sync(0xffffffffu, mine_at, t, 4);
               if (row4 + t < live_rows)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow[t] * D + c0 +
-                                          8 * lane4) = v[t];
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + c0 + 8 * lane4) =
+                    v[t];
+            }
           } else if (mine) {
             // partial states: [slot][query tile][dim / 4][row][4]
             float4* pa = reinterpret_cast<float4*>(p.part_acc) +
@@ -1560,9 +1558,7 @@ struct Softmax {
           if (!seg.complete) {
             p.part_ml[(long long)(2 * seg.slot + qt) * kRowsTile + r] = make_float2(m_out, l);
           } else if (p.lse) {
-            const long long at = (long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
-                                 (long long)seg.h * p.group + rhead;
-            p.lse[at] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
+            p.lse[mine_at / D] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
           }
         }
       }
