@@ -939,6 +939,29 @@ __device__ __forceinline__ void fixers(const Prefill& p, Walk walk, Control& c,
   }
 }
 
+// Four 8-bit codes (low byte first) as two registers of 16-bit pairs, exact.
+// int8 as bf16: with m the low seven bits, 128 + m is 0x43 above m, and code =
+// (128 + m) - (128 or, with the sign bit set, 256), which is 0x43 above 0x00
+// or 0x80: the sign bit itself.
+template <int KVT, bool BF16>
+__device__ __forceinline__ uint2 widen(uint32_t w) {
+  if constexpr (KVT == FD_I8 && BF16) {
+    const uint32_t m = w & 0x7F7F7F7Fu, s = w & 0x80808080u;
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __byte_perm(m, 0x43u, i ? 0x4342 : 0x4140);
+      const uint32_t b = __byte_perm(s, 0x43u, i ? 0x4342 : 0x4140);
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&b));
+      r[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    return make_uint2(r[0], r[1]);
+  } else {
+    return mma::widen8x4<KVT, BF16>(w);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Converter warps: thread = key of the tile
 // ---------------------------------------------------------------------------
@@ -1061,8 +1084,8 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
             sts128(dst + kmajor_chunk(kTile, t, i), w[i]);
           } else {
             constexpr int KVT = KV == 1 ? FD_E4M3 : FD_I8;
-            const uint2 a = mma::widen8x4<KVT, BF16>(w[i].x), b = mma::widen8x4<KVT, BF16>(w[i].y);
-            const uint2 d = mma::widen8x4<KVT, BF16>(w[i].z), f = mma::widen8x4<KVT, BF16>(w[i].w);
+            const uint2 a = widen<KVT, BF16>(w[i].x), b = widen<KVT, BF16>(w[i].y);
+            const uint2 d = widen<KVT, BF16>(w[i].z), f = widen<KVT, BF16>(w[i].w);
             sts128(dst + kmajor_chunk(kTile, t, 2 * i), make_uint4(a.x, a.y, b.x, b.y));
             sts128(dst + kmajor_chunk(kTile, t, 2 * i + 1), make_uint4(d.x, d.y, f.x, f.y));
           }
@@ -1130,7 +1153,7 @@ template <int D, int KV, bool CONV, bool BF16, bool TOK>
 struct Softmax {
   using SH = Shape<D, KV, CONV>;
   using SR = ScaleRing<D, KV>;
-  // f16: P carries a factor 2^kLift (see the file comment)
+  // f16: a factor of P (see the file comment)
   static constexpr float kLift = BF16 ? 0.f : 6.f;
   // exchange of a solo segment: dims per round, and where the states' (m, l) go
   static constexpr int kRound = D / 4;
@@ -1144,7 +1167,10 @@ struct Softmax {
   uint32_t tS, tO;
   // the row's state in the segment
   float m_ref, l, sc;
-  int vexp;   // TOK with f16: P carries 2^-vexp against the V scales
+  int vexp;   // TOK with f16: P's factor carries 2^-vexp against the V scales
+
+  // P and l carry a factor 2^lift()
+  __device__ __forceinline__ float lift() const { return TOK && !BF16 ? kLift - vexp : kLift; }
 
   __device__ __forceinline__ static void fetch(uint32_t tS, float (&x)[32], int k) {
     tmem_ld32<128>(tS + 32 * k, x);
@@ -1188,7 +1214,7 @@ struct Softmax {
   // P of scores 32 k .. into 16 columns of tensor memory, over scores that
   // were read before; their sum into `sum`.
   __device__ __forceinline__ void exponents(const float (&x)[32], int k, uint64_t sc2, uint64_t nm2,
-                                            uint64_t vm2, const float* vs, int left, bool all,
+                                            const float* vs, int left, bool all,
                                             uint64_t (&sum)[4]) const {
     uint32_t pk[16];
 #pragma unroll
@@ -1202,8 +1228,8 @@ struct Softmax {
       if constexpr (TOK) {
         uint64_t va, vb;
         lds_pairs(vs + 32 * k + i, va, vb);
-        pa = mul2(pa, BF16 ? va : mul2(va, vm2));
-        pb = mul2(pb, BF16 ? vb : mul2(vb, vm2));
+        pa = mul2(pa, va);
+        pb = mul2(pb, vb);
       }
       float2 qa = unpack2(pa), qb = unpack2(pb);
       if (TOK && !all) {   // 0 times an excluded key's scale, whatever that is
@@ -1239,12 +1265,11 @@ struct Softmax {
     const float scl = TOK || sc == 0.f ? 1.f : fabsf(sc);
     // Other tiles than those whose keys every row of the warp sees (or with
     // the scale's sign turned) are put right in tensor memory first, so that
-    // one stretch of code, kept in the instruction cache, serves all.  (With
-    // per-token scales, which may be anything for unseen keys, they have a
-    // path of their own.)
+    // one stretch of code, kept in the instruction cache, serves all.  Scores
+    // with per-token scales always go back scaled, and are read once more.
     const bool fast = whole && (TOK || sc > 0.f);
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (!fast) {
+    if (TOK || !fast) {
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         float x[32];
@@ -1252,13 +1277,13 @@ struct Softmax {
         tmem_wait_ld();
         arrived(x);
         if constexpr (TOK) key_scales(x, ks + 32 * k);
-        exclude(x, left - 32 * k);
+        if (!TOK || !whole) exclude(x, left - 32 * k);
+        tmem_st32<128>(tS + 32 * k, x);
         if constexpr (TOK) row_max(x, mx);
-        else tmem_st32<128>(tS + 32 * k, x);
       }
-      if constexpr (!TOK) tmem_wait_st();
+      tmem_wait_st();
     }
-    if (!TOK || fast) {
+    if constexpr (!TOK) {
       float x[2][32];
       fetch(tS, x[0], 0);
 #pragma unroll
@@ -1266,7 +1291,6 @@ struct Softmax {
         tmem_wait_ld();
         arrived(x[k & 1]);
         if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
-        if constexpr (TOK) key_scales(x[k & 1], ks + 32 * k);
         row_max(x[k & 1], mx);
       }
     }
@@ -1282,27 +1306,28 @@ struct Softmax {
       }
       m_ref = mt;
     }
-    float vmul = 1.f;
     if constexpr (TOK) {
       if (!wait_warp(c, p, &c.fixed[jn % SR::kValRing], (uint32_t)((jn / SR::kValRing) & 1), 12))
         return false;
       if constexpr (!BF16) {
-        // largest V scale of the tile -> its exponent; P stays below 2^15
+        // largest V scale of the tile -> its exponent, which P's factor takes
+        // back, so that P times a V scale stays below 2^15
         float vm = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vs[lane + 32 * i]));
 #pragma unroll
         for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
         int ev = (int)((__float_as_uint(vm) >> 23) & 255u) - 127;
-        ev = max(-120, min(120, ev));
-        if (ev > vexp) {
-          if (!fresh) {
-            fac *= exp2f((float)max(vexp - ev, -200));
-            resc = true;
-          }
+        ev = max(-60, min(60, ev));
+        if (fresh) {
+          vexp = ev;
+        } else if (ev > vexp) {
+          const float f = exp2f((float)(vexp - ev));
+          fac *= f;
+          l *= f;
+          resc = true;
           vexp = ev;
         }
-        vmul = exp2f((float)-vexp);
       }
     }
     if (__any_sync(0xffffffffu, resc)) {
@@ -1321,33 +1346,18 @@ struct Softmax {
     }
     // P = 2^(s - m_ref + kLift); excluded scores are -inf and give 0 (a row
     // that has seen no key has m_ref = -inf: everything is excluded)
-    const float nm = m_ref == -INFINITY ? 0.f : kLift - m_ref;
-    const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm), vm2 = pack2(vmul, vmul);
+    const float nm = m_ref == -INFINITY ? 0.f : lift() - m_ref;
+    const uint64_t sc2 = pack2(scl, scl), nm2 = pack2(nm, nm);
     uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-    if (!TOK || fast) {
-      float x[2][32];
-      fetch(tS, x[0], 0);
+    float x[2][32];
+    fetch(tS, x[0], 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        tmem_wait_ld();
-        arrived(x[k & 1]);
-        if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
-        if constexpr (TOK) key_scales(x[k & 1], ks + 32 * k);
-        exponents(x[k & 1], k, sc2, nm2, vm2, vs, left, true, sum);
-        if (k == 1) publish(&c.p_half[X]);
-      }
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        float x[32];
-        fetch(tS, x, k);
-        tmem_wait_ld();
-        arrived(x);
-        if constexpr (TOK) key_scales(x, ks + 32 * k);
-        exclude(x, left - 32 * k);
-        exponents(x, k, sc2, nm2, vm2, vs, left, false, sum);
-        if (k == 1) publish(&c.p_half[X]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      tmem_wait_ld();
+      arrived(x[k & 1]);
+      if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
+      exponents(x[k & 1], k, sc2, nm2, vs, left, whole, sum);
+      if (k == 1) publish(&c.p_half[X]);
     }
     publish(&c.p_full[X]);
     const float2 sa = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
@@ -1389,7 +1399,7 @@ struct Softmax {
       }
       m_ref = -INFINITY;
       l = 0.f;
-      vexp = -1000;
+      vexp = 0;
       for (int j = first; j < te; j += step, ++done) {
         const int jn = n + (j - seg.tb);   // tile of the CTA
         if (!wait_warp(c, p, &c.s_full[X], (uint32_t)(done & 1), 11)) {
@@ -1428,9 +1438,8 @@ struct Softmax {
         if (seg.slot & 1) used1 = make_int4(seg.b, seg.h, seg.m, 0);
         else used0 = make_int4(seg.b, seg.h, seg.m, 0);
       }
-      float m_out = m_ref == -INFINITY ? -INFINITY : m_ref - kLift;
+      float m_out = m_ref == -INFINITY ? -INFINITY : m_ref - lift();
       float osc = 1.f;   // of this half's O
-      if constexpr (TOK && !BF16) osc = vexp > -1000 ? exp2f((float)vexp) : 1.f;
       const bool swap = swaps_in(seg);
       float bsc = 0.f;   // of the other half's O (A of a solo segment)
       if (swap) {
