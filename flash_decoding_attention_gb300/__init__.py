@@ -396,18 +396,17 @@ def fd_append_kv_packed(q, q_stride: int, q_out, k_new, v_new, kv_stride: int, k
     """Rotates (``rotary``: a table of fd_rotary_table, or None) and writes
     packed new tokens into the caches; ``q`` (or None) is rotated into
     ``q_out``."""
-    lib = load_library()
-    stride = int(block_table.shape[1]) if block_table is not None else 0
-    st = lib.fd_append_kv_packed(
-        _ptr(q), int(q_stride), _ptr(q_out), _ptr(k_new), _ptr(v_new), int(kv_stride),
-        _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx), _ptr(block_table), stride,
-        _ptr(q_start), _ptr(positions), int(num_tokens), int(kv_rows), int(positions.shape[0]),
-        int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size), _ptr(rotary),
-        int(rotary.shape[0]) if rotary is not None else 0, int(rot_dim), int(bool(interleaved)),
-        float(k_scale), float(v_scale), int(scale_kind), _ptr(k_scales), _ptr(v_scales),
-        _q_dtype(k_new) if new_dtype is None else int(new_dtype),
-        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    st = (_lib or load_library()).fd_append_kv_packed(
+        None if q is None else q.data_ptr(), q_stride, None if q is None else q_out.data_ptr(),
+        k_new.data_ptr(), v_new.data_ptr(), kv_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(kv_start_idx), _ptr(block_table), 0 if block_table is None else block_table.shape[1],
+        q_start.data_ptr(), positions.data_ptr(), num_tokens, kv_rows, positions.shape[0],
+        num_q_heads, num_kv_heads, head_dim, page_size, _ptr(rotary),
+        0 if rotary is None else rotary.shape[0], rot_dim, 1 if interleaved else 0, k_scale,
+        v_scale, scale_kind, _ptr(k_scales), _ptr(v_scales),
+        _q_dtype(k_new) if new_dtype is None else new_dtype,
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype,
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_append_kv_packed")
     return st
@@ -420,16 +419,14 @@ def fd_read_kv(k_cache, v_cache, kv_start_idx, block_table, out_start, first, nu
                check: bool = True) -> int:
     """Reads cached tokens (from ``first`` on, or from each sequence's start)
     back into packed 16-bit rows."""
-    lib = load_library()
-    stride = int(block_table.shape[1]) if block_table is not None else 0
-    st = lib.fd_read_kv(
-        _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx), _ptr(block_table), stride,
-        _ptr(out_start), _ptr(first), int(num_rows), int(kv_rows), int(out_start.shape[0]) - 1,
-        int(num_kv_heads), int(head_dim), int(page_size), float(k_scale), float(v_scale),
-        int(scale_kind), _ptr(k_scales), _ptr(v_scales),
-        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype),
-        _q_dtype(k_out) if out_dtype is None else int(out_dtype), _ptr(k_out), _ptr(v_out),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    st = (_lib or load_library()).fd_read_kv(
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_start_idx), _ptr(block_table),
+        0 if block_table is None else block_table.shape[1], out_start.data_ptr(), _ptr(first),
+        num_rows, kv_rows, out_start.shape[0] - 1, num_kv_heads, head_dim, page_size, k_scale,
+        v_scale, scale_kind, _ptr(k_scales), _ptr(v_scales),
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype,
+        _q_dtype(k_out) if out_dtype is None else out_dtype, k_out.data_ptr(), v_out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_read_kv")
     return st
@@ -447,16 +444,14 @@ def fd_prefill_attention(q, q_stride: int, k_cache, v_cache, kv_start_idx, block
                          kv_dtype: Optional[int] = None, check: bool = True) -> int:
     """Attention of packed new tokens (the last of each sequence's ``seq_len``
     cached ones) over the caches."""
-    lib = load_library()
-    stride = int(block_table.shape[1]) if block_table is not None else 0
-    st = lib.fd_prefill_attention(
-        _ptr(q), int(q_stride), _ptr(k_cache), _ptr(v_cache), _ptr(kv_start_idx),
-        _ptr(block_table), stride, _ptr(q_start), _ptr(seq_len), int(num_tokens), int(kv_rows),
-        int(seq_len.shape[0]), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
-        float(softmax_scale), float(k_scale), float(v_scale), int(scale_kind), _ptr(k_scales),
-        _ptr(v_scales), _q_dtype(q) if q_dtype is None else int(q_dtype),
-        _kv_dtype(k_cache) if kv_dtype is None else int(kv_dtype), _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    st = (_lib or load_library()).fd_prefill_attention(
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_start_idx),
+        _ptr(block_table), 0 if block_table is None else block_table.shape[1], q_start.data_ptr(),
+        seq_len.data_ptr(), num_tokens, kv_rows, seq_len.shape[0], num_q_heads, num_kv_heads,
+        head_dim, page_size, softmax_scale, k_scale, v_scale, scale_kind, _ptr(k_scales),
+        _ptr(v_scales), _q_dtype(q) if q_dtype is None else q_dtype,
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype, out.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_prefill_attention")
     return st
@@ -691,14 +686,15 @@ def _scale_kind(k_scales, v_scales, kv_rows: int, KVH: int, at: int) -> int:
         raise ValueError(f"k_scales and v_scales must be dense fp32 [{KVH}] or [{kv_rows}, {KVH}], "
                          f"got {k_scales.dtype} {tuple(shape)} and {v_scales.dtype} "
                          f"{tuple(v_scales.shape)}")
-    _same_device(at, k_scales=k_scales, v_scales=v_scales)
+    _same_device(at, k_scales, v_scales)
     return FD_SCALE_HEAD if len(shape) == 1 else FD_SCALE_TOKEN
 
 
-def _same_device(at: int, **tensors) -> None:
-    for name, t in tensors.items():
+def _same_device(at: int, *tensors) -> None:
+    for t in tensors:
         if t is not None and t.get_device() != at:
-            raise ValueError(f"{name} is on {t.device}, the caches on cuda:{at}")
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the caches on "
+                             f"cuda:{at}")
 
 
 def _index(name: str, t: torch.Tensor, n: int, at: int, dims: int = 1) -> None:
@@ -753,7 +749,7 @@ def rotary_table(positions: int, rot_dim: int, *, theta: float = 10000.0, scalin
         device = torch.device(device)
     with _on(device, stream):
         if out is None:
-            out = torch.empty((int(positions), int(rot_dim)), dtype=torch.float32, device=device)
+            out = torch.empty((positions, rot_dim), dtype=torch.float32, device=device)
         fd_rotary_table(out, positions, rot_dim, theta, ROTARY_SCALINGS[scaling], factor,
                         original_positions, low_turns, high_turns, amplitude)
     return out
@@ -790,8 +786,7 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
     _index("q_start", q_start, batch + 1, at)
     _index("positions", positions, batch, at)
     _layout_index(kv_start_idx, block_table, batch, at)
-    _same_device(at, k_new=k_new, v_new=v_new, v_cache=v_cache, q=q, q_out=q_out, rotary=rotary,
-                 workspace=workspace)
+    _same_device(at, k_new, v_new, v_cache, q, q_out, rotary, workspace)
     kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     QH = qs = 0
     if q is not None:
@@ -840,7 +835,7 @@ def read_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, out_start: torch.Tenso
     if first is not None:
         _index("first", first, batch, at)
     _layout_index(kv_start_idx, block_table, batch, at)
-    _same_device(at, v_cache=v_cache, k_out=k_out, v_out=v_out, workspace=workspace)
+    _same_device(at, v_cache, k_out, v_out, workspace)
     kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else k_cache.dtype if \
@@ -893,7 +888,7 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     _index("q_start", q_start, batch + 1, at)
     _index("seq_len", seq_len, batch, at)
     _layout_index(kv_start_idx, block_table, batch, at)
-    _same_device(at, q=q, v_cache=v_cache, out=out, lse=lse, workspace=workspace)
+    _same_device(at, q, v_cache, out, lse, workspace)
     kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
     if (k_new is None) != (v_new is None) or (k_new is None) != (positions is None):
         raise ValueError("give k_new, v_new and positions, or none of them")

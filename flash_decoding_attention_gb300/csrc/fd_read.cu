@@ -4,9 +4,10 @@
 //   operation; ks per tensor (1), KV head or token.
 //
 // A copy with a widening: the floor is the DRAM traffic of codes, scales and
-// output rows.  A thread takes 16 elements of one head of K and of V (one
-// 16-byte load of 8-bit codes each, two of 16-bit elements), so a head's row
-// is read and written by neighbouring threads in full lines.
+// output rows.  A thread takes 8 elements of one head of K and of V, so its
+// stores are 16 bytes beside its neighbours' (whole lines) and its loads 8 or
+// 16; four rows are in flight at a time.  Its place in a row is fixed, so the
+// head is known once.
 #include <type_traits>
 
 #include "fd_prompt.cuh"
@@ -53,24 +54,24 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
   }
 }
 
+// 8 elements from `at` on: 8-bit codes in w.x, w.y, or 16-bit elements.
 template <int KVT, typename OT>
-__device__ __forceinline__ void load16(const void* cache, long long at, uint4& w0, uint4& w1) {
+__device__ __forceinline__ uint4 load8(const void* cache, long long at) {
   if constexpr (KVT == FD_E4M3 || KVT == FD_I8) {
-    w0 = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + at);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at);
+    return make_uint4(w.x, w.y, 0, 0);
   } else {
-    w0 = *reinterpret_cast<const uint4*>(static_cast<const OT*>(cache) + at);
-    w1 = *reinterpret_cast<const uint4*>(static_cast<const OT*>(cache) + at + 8);
+    return *reinterpret_cast<const uint4*>(static_cast<const OT*>(cache) + at);
   }
 }
 
 template <int KVT, typename OT>
-__device__ __forceinline__ void store16(void* out, long long at, const uint4& w0, const uint4& w1,
-                                        float scale) {
-  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  uint32_t r[8];
+__device__ __forceinline__ uint4 decode8(const uint4& v, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
   if constexpr (KVT == FD_E4M3 || KVT == FD_I8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float x[4];
       decode4(w[i], KVT, x);
       r[2 * i] = round2<OT>(__fmul_rn(x[0], scale), __fmul_rn(x[1], scale));
@@ -78,14 +79,12 @@ __device__ __forceinline__ void store16(void* out, long long at, const uint4& w0
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float2 f = two_of<OT>(w[i]);
       r[i] = round2<OT>(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
     }
   }
-  uint4* d = reinterpret_cast<uint4*>(static_cast<OT*>(out) + at);
-  d[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  d[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 constexpr long long kSkip = -2;   // the row belongs to no sequence: left as it was
@@ -93,7 +92,7 @@ constexpr long long kSkip = -2;   // the row belongs to no sequence: left as it 
 template <int KVT, typename OT, int D>
 __global__ void __launch_bounds__(kThreads) read_kv_kernel(const __grid_constant__ ReadKv p,
                                                            int per_block) {
-  constexpr int TPH = D / 16;
+  constexpr int TPH = D / 8, kFlight = 4;
   __shared__ long long src_row[kMaxRows];
   const int i0 = blockIdx.x * per_block;
   const int n = min(per_block, p.rows - i0);
@@ -119,31 +118,44 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const __grid_constant
     src_row[threadIdx.x] = row;
   }
   __syncthreads();
-  const int per_row = p.num_kv_heads * TPH;
-  const int items = n * per_row;
-  for (int x = threadIdx.x; x < items; x += kThreads) {
-    const int r = x / per_row, e = x - r * per_row;   // e = head * TPH + part
-    const long long row = src_row[r];
-    if (row == kSkip) continue;
-    const long long to = ((long long)(i0 + r) * per_row + e) * 16;
-    uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
-    float ks = p.k_scale, vs = p.v_scale;
-    if (row >= 0) {
-      const long long from = (row * per_row + e) * 16;
-      load16<KVT, OT>(p.k_cache, from, ka, kb);
-      load16<KVT, OT>(p.v_cache, from, va, vb);
-      if (p.scale_kind != FD_SCALE_TENSOR) {
-        const int h = e / TPH;
-        const long long at = p.scale_kind == FD_SCALE_HEAD ? h : row * p.num_kv_heads + h;
-        ks = __fmul_rn(ks, __ldg(p.k_scales + at));
-        vs = __fmul_rn(vs, __ldg(p.v_scales + at));
+  const int per_row = p.num_kv_heads * TPH;   // threads of a row
+  // narrow rows: several at a time; wide ones: several passes over each
+  const int rows_at_once = per_row < kThreads ? kThreads / per_row : 1;
+  const int r0 = per_row < kThreads ? threadIdx.x / per_row : 0;
+  if (r0 >= rows_at_once) return;
+  for (int e = threadIdx.x - r0 * per_row; e < per_row; e += kThreads) {
+    const int h = e / TPH;
+    for (int r = r0; r < n; r += kFlight * rows_at_once) {
+      uint4 k[kFlight], v[kFlight];
+      float ks[kFlight], vs[kFlight];
+      long long row[kFlight];
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        const int q = r + x * rows_at_once;
+        row[x] = q < n ? src_row[q] : kSkip;
+        k[x] = v[x] = make_uint4(0, 0, 0, 0);
+        ks[x] = p.k_scale;
+        vs[x] = p.v_scale;
+        if (row[x] < 0) continue;
+        const long long from = (row[x] * per_row + e) * 8;
+        k[x] = load8<KVT, OT>(p.k_cache, from);
+        v[x] = load8<KVT, OT>(p.v_cache, from);
+        if (p.scale_kind != FD_SCALE_TENSOR) {
+          const long long at = p.scale_kind == FD_SCALE_HEAD ? h : row[x] * p.num_kv_heads + h;
+          ks[x] = __fmul_rn(ks[x], __ldg(p.k_scales + at));
+          vs[x] = __fmul_rn(vs[x], __ldg(p.v_scales + at));
+        }
       }
-      store16<KVT, OT>(p.k_out, to, ka, kb, ks);
-      store16<KVT, OT>(p.v_out, to, va, vb, vs);
-    } else {
-      uint4* dk = reinterpret_cast<uint4*>(static_cast<OT*>(p.k_out) + to);
-      uint4* dv = reinterpret_cast<uint4*>(static_cast<OT*>(p.v_out) + to);
-      dk[0] = dk[1] = dv[0] = dv[1] = ka;
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        if (row[x] == kSkip) continue;
+        const long long to = ((long long)(i0 + r + x * rows_at_once) * per_row + e) * 8;
+        // (a row that is not there: zero bits stay zero)
+        *reinterpret_cast<uint4*>(static_cast<OT*>(p.k_out) + to) =
+            row[x] < 0 ? k[x] : decode8<KVT, OT>(k[x], ks[x]);
+        *reinterpret_cast<uint4*>(static_cast<OT*>(p.v_out) + to) =
+            row[x] < 0 ? v[x] : decode8<KVT, OT>(v[x], vs[x]);
+      }
     }
   }
 }
