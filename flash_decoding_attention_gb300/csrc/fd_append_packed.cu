@@ -115,11 +115,11 @@ __device__ __forceinline__ TokenAt place_token(const AppendPacked& p, int i) {
   return t;
 }
 
-constexpr int kMaxTokens = 8;   // of a block
+constexpr int kMaxTokens = 4;   // of a block
 
 // gridDim.x blocks of `per_block` tokens; gridDim.y parts of a token's heads.
 template <typename XT, int KVT, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kMaxThreads) append_packed_kernel(const __grid_constant__ AppendPacked p,
+__global__ void __launch_bounds__(kMaxThreads, 2) append_packed_kernel(const __grid_constant__ AppendPacked p,
                                                                     int per_block) {
   constexpr int TPH = D / 16;                        // threads per head
   const int hpp = blockDim.x / TPH;                  // heads per pass

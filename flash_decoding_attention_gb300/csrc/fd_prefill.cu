@@ -137,7 +137,7 @@ struct Merge {
     const long long orow = tok * p.num_q_heads + (long long)it.id.y * p.group + r % p.group;
     float vsc = p.v_scale;
     if (p.scale_kind == FD_SCALE_HEAD) vsc *= __ldg(p.v_scales + it.id.y);
-    const float q = st.l > 0.f ? vsc / st.l : 0.f;
+    const float q = st.l == 0.f ? 0.f : vsc / st.l;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack16<BF16>(st.a[2 * i] * q, st.a[2 * i + 1] * q);
@@ -145,7 +145,7 @@ struct Merge {
     o[0] = make_uint4(w[0], w[1], w[2], w[3]);
     o[1] = make_uint4(w[4], w[5], w[6], w[7]);
     if (p.lse && it.dim0 == 0)
-      p.lse[orow] = st.l > 0.f ? (st.m + log2f(st.l)) * kLn2 : -INFINITY;
+      p.lse[orow] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
   }
 };
 

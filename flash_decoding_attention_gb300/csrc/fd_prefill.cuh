@@ -1482,7 +1482,7 @@ struct Softmax {
       }
       const bool writes = !(seg.solo && X == 1);
       if (seg.complete) {
-        const float q = l > 0.f ? vsc / l : 0.f;
+        const float q = l == 0.f ? 0.f : vsc / l;
         osc *= q;
         bsc *= q;
       }
@@ -1567,7 +1567,7 @@ struct Softmax {
           if (!seg.complete) {
             p.part_ml[(long long)(2 * seg.slot + qt) * kRowsTile + r] = make_float2(m_out, l);
           } else if (p.lse) {
-            p.lse[mine_at / D] = l > 0.f ? (m_out + log2f(l)) * kLn2 : -INFINITY;
+            p.lse[mine_at / D] = l == 0.f ? -INFINITY : (m_out + log2f(l)) * kLn2;
           }
         }
       }

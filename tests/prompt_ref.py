@@ -160,6 +160,31 @@ def attention(filled, q, qh, softmax_scale, causal_limit=None):
     return out, lse
 
 
+def attention_blocks(filled, q, qh, softmax_scale):
+    """The same as `attention`, a sequence at a time in matrix form (for
+    batches of many tokens)."""
+    bt = filled.batch
+    group = qh // bt.kvh
+    out = torch.full(q.shape, float("nan"), dtype=torch.float64)
+    lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float64)
+    for b in range(len(bt.new)):
+        n, T = bt.new[b], bt.seq[b]
+        i = int(bt.q_start[b])
+        if n == 0:
+            continue
+        rows = bt.rows_of(b, 0, T)
+        seen = torch.arange(T)[None, :] < (T - n + 1 + torch.arange(n))[:, None]   # [n, T]
+        for h in range(qh):
+            k, v = filled.val["k"][rows, h // group], filled.val["v"][rows, h // group]
+            s = q[i:i + n, h].double() @ k.T * softmax_scale
+            s = torch.where(seen, s, torch.tensor(-math.inf, dtype=torch.float64))
+            z = torch.logsumexp(s, -1) if T else torch.full((n,), -math.inf, dtype=torch.float64)
+            w = torch.exp(s - torch.where(z == -math.inf, torch.zeros_like(z), z)[:, None])
+            lse[i:i + n, h] = z
+            out[i:i + n, h] = torch.where(seen, w, torch.zeros_like(w)) @ v if T else 0.0
+    return out, lse
+
+
 def table(positions, rot, theta, scaling="none", factor=1.0, original=0.0, low=1.0, high=32.0,
           amplitude=1.0):
     f = np.array([theta ** (-2.0 * i / rot) for i in range(rot // 2)])

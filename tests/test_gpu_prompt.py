@@ -347,3 +347,409 @@ def test_attention_rows_without_keys():
     want, wlse = ref.attention(f, q, 4, 64 ** -0.5)
     assert int((wlse == -math.inf).sum()) == 4 * (190 + 3 + 2)
     _compare(f, out, lse, want, wlse, "bf16")
+
+
+def _queries(bt, qh, x16, seed, scale=1.0):
+    q = torch.randn((bt.tokens, qh, bt.d), generator=torch.Generator().manual_seed(seed)) * scale
+    return q.to(ref.T16[x16])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_many_streams(seed):
+    """Random batches of many sequences, so that a CTA passes several streams
+    (with rows in one or both of its query tiles, whole and cut) one after the
+    other: every format, layout, scale kind and head grouping."""
+    fda = lib()
+    rng = np.random.default_rng(1000 + seed)
+    kvh, group = [(8, 1), (2, 8), (1, 16), (4, 3), (8, 4), (3, 5)][seed % 6]
+    d = 64 if seed % 4 else 128
+    x16 = ["f16", "bf16"][seed % 2]
+    kv = [x16, "e4m3", "i8"][(seed // 2) % 3]
+    scales = ["tensor", "head", "token"][(seed // 6) % 3] if kv in ref.QMAX else "tensor"
+    page = [0, 16, 64, 4, 256, 8][(seed // 3) % 6]
+    B = int(rng.integers(30, 90))
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 17, 40, 90], B)]
+    ctx = [int(x) for x in rng.choice([0, 0, 1, 100, 127, 128, 300, -1], B)]
+    new[0], ctx[0] = 200, 40
+    ctx = [max(c, -n) for n, c in zip(new, ctx)]
+    bt = ref.Batch(new, ctx, kvh, d, kv, page, seed=seed, lead=1, tail=2)
+    f = ref.Filled(bt, scales, seed=seed)
+    q = _queries(bt, kvh * group, x16, seed)
+    ws = fda.alloc_prefill_workspace(d)
+    out, lse = _attend(fda, f, q, kvh * group, ws)
+    _ok(fda, ws)
+    want, wlse = ref.attention_blocks(f, q, kvh * group, d ** -0.5)
+    _compare(f, out, lse, want, wlse, x16, f"{kvh}x{group} d{d} {x16}/{kv} {scales} page {page}")
+    # the same bits again: nothing depends on the order CTAs run in
+    again, lagain = _attend(fda, f, q, kvh * group, ws)
+    assert torch.equal(out, again) and torch.equal(lse, lagain)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 2.0])
+@pytest.mark.parametrize("kv,scales", [("f16", "tensor"), ("e4m3", "token"), ("i8", "head")])
+def test_attention_score_scales(scale, kv, scales):
+    """Negative, zero and large softmax scales (the running maximum moves and
+    the accumulator is rescaled)."""
+    fda = lib()
+    bt = ref.Batch([70, 300, 1], [0, 500, 900], 2, 128, kv, 16, seed=5)
+    f = ref.Filled(bt, scales, seed=5)
+    q = _queries(bt, 8, "f16", 5)
+    ws = fda.alloc_prefill_workspace(128)
+    out, lse = _attend(fda, f, q, 8, ws, scale=scale)
+    _ok(fda, ws)
+    want, wlse = ref.attention_blocks(f, q, 8, scale)
+    _compare(f, out, lse, want, wlse, "f16")
+
+
+def test_attention_value_scales_over_a_wide_range():
+    """Per-token V scales from 1e-7 to 1e5 with f16 queries: their exponents
+    are carried beside P."""
+    fda = lib()
+    bt = ref.Batch([40, 3], [500, 900], 2, 64, "i8", 16, seed=6)
+    f = ref.Filled(bt, "token", seed=6)
+    owned = ~torch.isnan(f.kw["v_scales"])
+    g = torch.Generator().manual_seed(9)
+    mag = 10.0 ** (torch.rand(f.kw["v_scales"].shape, generator=g) * 12 - 7)
+    old = f.kw["v_scales"].clone()
+    f.kw["v_scales"][owned] = mag[owned]
+    f.val["v"] = f.val["v"] * (f.kw["v_scales"].double() / old.double())[:, :, None]
+    q = _queries(bt, 4, "f16", 6)
+    # outputs far beyond f16: the caller's v_scale brings them back
+    f.kw["v_scale"] = f.kw["v_scale"] * 1e-3
+    f.val["v"] = f.val["v"] * 1e-3
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 4, ws)
+    _ok(fda, ws)
+    want, wlse = ref.attention_blocks(f, q, 4, 64 ** -0.5)
+    # P is rounded to f16 (half a step: 2^-11 of itself) against the largest
+    # value seen, and the output once more
+    top = float(f.val["v"].abs().nan_to_num().max())
+    mine = ~torch.isnan(wlse)
+    assert torch.all((out - want)[mine].abs() <= 2.0 ** -11 * (top + want[mine].abs()))
+    assert float((lse - wlse)[mine].abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("kv,page", [("bf16", 0), ("f16", 16), ("bf16", 4), ("e4m3", 16),
+                                     ("e4m3", 0), ("e4m3", 2)])
+def test_attention_nonfinite_values_stay_with_their_readers(kv, page):
+    """NaN and infinite V elements of new tokens reach the tokens that see
+    them, and no other; unseen K rows may hold anything."""
+    fda = lib()
+    x16 = kv if kv in ref.T16 else "f16"
+    bt = ref.Batch([90, 300, 30], [20, 0, 400], 2, 64, kv, page, seed=7)
+    f = ref.Filled(bt, seed=7)
+    q = _queries(bt, 4, x16, 7)
+    marks = [(0, 60, 0, 5, float("nan")), (1, 100, 1, 9, float("inf")), (1, 200, 1, 9, -math.inf),
+             (1, 130, 0, 63, float("inf")), (2, 415, 1, 0, float("nan"))]
+    for b, t, h, dim, x in marks:
+        row = bt.row(b, t)
+        if kv == "e4m3":
+            x = float("nan")
+            f.kw["v_cache"].view(bt.rows, 2, 64)[row, h, dim] = 0x7F
+        else:
+            f.kw["v_cache"].view(bt.rows, 2, 64)[row, h, dim] = x
+        f.val["v"][row, h, dim] = x
+    # the last token of each sequence has NaN keys: nobody before it sees them
+    for b, T in enumerate(bt.seq):
+        row = bt.row(b, T - 1)
+        f.kw["k_cache"].view(bt.rows, 2, 64)[row] = 0x7F if kv == "e4m3" else float("nan")
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 4, ws)
+    _ok(fda, ws)
+    want, wlse = ref.attention(f, q, 4, 64 ** -0.5)
+    for b, T in enumerate(bt.seq):
+        i, n = int(bt.q_start[b]), bt.new[b]
+        assert torch.isnan(out[i + n - 1]).all() and torch.isnan(lse[i + n - 1]).all()
+        o, w = out[i:i + n - 1], want[i:i + n - 1]
+        assert torch.equal(torch.isnan(o), torch.isnan(w)), b
+        assert torch.equal(torch.isinf(o), torch.isinf(w)) and torch.equal(o[torch.isinf(o)],
+                                                                           w[torch.isinf(w)])
+        fin = torch.isfinite(w)
+        eps = torch.finfo(ref.T16[x16]).eps
+        assert torch.all((o - w)[fin].abs() <= (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * w[fin].abs())
+
+
+def test_attention_nan_scales_of_unseen_keys():
+    """A later token's per-token scales may be NaN."""
+    fda = lib()
+    for x16 in ("f16", "bf16"):
+        bt = ref.Batch([150, 3], [10, 200], 1, 64, "i8", 16, seed=8)
+        f = ref.Filled(bt, "token", seed=8)
+        for b, T in enumerate(bt.seq):
+            f.kw["k_scales"][bt.row(b, T - 1)] = float("nan")
+            f.kw["v_scales"][bt.row(b, T - 1)] = float("nan")
+        q = _queries(bt, 4, x16, 8)
+        ws = fda.alloc_prefill_workspace(64)
+        out, lse = _attend(fda, f, q, 4, ws)
+        want, wlse = ref.attention_blocks(f, q, 4, 64 ** -0.5)
+        eps = torch.finfo(ref.T16[x16]).eps
+        for b in range(2):
+            i, n = int(bt.q_start[b]), bt.new[b]
+            o, w = out[i:i + n - 1], want[i:i + n - 1]
+            assert torch.all((o - w).abs() <= (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * w.abs())
+            assert torch.isnan(out[i + n - 1]).all()
+
+
+def test_attention_strided_queries_and_no_lse():
+    fda = lib()
+    bt = ref.Batch([33, 7], [0, 50], 2, 128, "bf16", 0, seed=9)
+    f = ref.Filled(bt, seed=9)
+    wide = torch.randn((40, 12, 128), generator=torch.Generator().manual_seed(9)).bfloat16().to(DEV)
+    q = wide[:, 2:10]
+    ws = fda.alloc_prefill_workspace(128)
+    kw, ix = f.device(DEV), bt.index(DEV)
+    qs = torch.from_numpy(bt.q_start).to(DEV)
+    sl = torch.tensor(bt.seq, dtype=torch.int32, device=DEV)
+    out, lse = fda.prefill_attention(q, kw["k_cache"], kw["v_cache"], qs, sl, workspace=ws, **ix)
+    out2, _ = fda.prefill_attention(q.contiguous(), kw["k_cache"], kw["v_cache"], qs, sl,
+                                    workspace=ws, **ix)
+    assert torch.equal(out, out2)
+    out3 = torch.empty_like(out2)
+    fda.fd_prefill_attention(q, 12 * 128, kw["k_cache"], kw["v_cache"], ix["kv_start_idx"], None,
+                             qs, sl, 40, bt.rows, 8, 2, 128, 0, 128 ** -0.5, 1.0, 1.0, 0, None, None,
+                             out3, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out3)
+
+
+def test_attention_what_lies_outside():
+    """A page outside the cache makes its 128-key tile absent and is recorded;
+    a sequence whose start entries are wrong is skipped and recorded; the
+    other sequences are served."""
+    fda = lib()
+    bt = ref.Batch([20, 30], [300, 40], 1, 64, "f16", 16, seed=10)
+    f = ref.Filled(bt, seed=10)
+    q = _queries(bt, 2, "f16", 10)
+    ws = fda.alloc_prefill_workspace(64)
+    want, wlse = ref.attention_blocks(f, q, 2, 0.125)
+    good = bt.block_table.copy()
+    for col, bad in ((3, -7), (9, 10 ** 6)):       # keys 48.., 144..
+        bt.block_table = good.copy()
+        bt.block_table[0, col] = bad
+        out, lse = _attend(fda, f, q, 2, ws)
+        assert fda.fd_check_device_error(ws) == (fda.FD_ERR_DEVICE_BOUNDS, bad)
+        assert torch.allclose(out[20:], want[20:], atol=3e-3)
+        # the tile's keys are left out of the others' softmax
+        bt.block_table = good
+        tile = col * 16 // 128
+        keys = [t for t in range(320) if t // 128 != tile]
+        rows = torch.tensor([bt.row(0, t) for t in keys])
+        for j in (0, 19):
+            seen = [i for i, t in enumerate(keys) if t <= 300 + j]
+            s = q[j].double() @ f.val["k"][rows[seen], 0].T * 0.125
+            w = torch.softmax(s, -1) @ f.val["v"][rows[seen], 0]
+            assert torch.allclose(out[j], w, atol=3e-3)
+    for starts in ([0, -5, 50], [0, 60, 50], [30, 20, 50]):
+        bt.q_start = np.array(starts, np.int32)
+        out, lse = _attend(fda, f, q, 2, ws)
+        st, info = fda.fd_check_device_error(ws)
+        assert st == fda.FD_ERR_DEVICE_BOUNDS and info in starts
+
+
+def test_attention_timeout_is_reported():
+    """A producer that issues nothing: every wait gives up, the timeout is
+    recorded, and the next call is right."""
+    fda = lib()
+    bt = ref.Batch([200, 1], [10, 700], 2, 128, "e4m3", 16, seed=11)
+    f = ref.Filled(bt, seed=11)
+    q = _queries(bt, 8, "f16", 11)
+    ws = fda.alloc_prefill_workspace(128)
+    want, wlse = ref.attention_blocks(f, q, 8, 128 ** -0.5)
+    for kv in ("e4m3", "f16"):
+        fda.fd_debug_set_wait_limit(3_000_000, True)
+        try:
+            if kv == "f16":
+                g = ref.Filled(ref.Batch([200, 1], [10, 700], 2, 128, "f16", 16, seed=11), seed=11)
+                _attend(fda, g, q, 8, ws)
+            else:
+                _attend(fda, f, q, 8, ws)
+        finally:
+            fda.fd_debug_set_wait_limit(0, False)
+        assert fda.fd_check_device_error(ws)[0] == fda.FD_ERR_DEVICE_TIMEOUT
+    out, lse = _attend(fda, f, q, 8, ws)
+    _ok(fda, ws)
+    _compare(f, out, lse, want, wlse, "f16")
+
+
+# ---------------------------------------------------------------------------
+# together, on streams, in graphs
+# ---------------------------------------------------------------------------
+
+def test_prompt_then_decode_then_read_back():
+    """A prompt in two chunks (rotated, written, attended), then decode steps
+    through the same cache, then the cache read back: each stage against a
+    plain statement of the whole."""
+    fda = lib()
+    B, QH, KVH, D, P, rot = 3, 8, 2, 128, 16, 128
+    chunks = [[50, 7, 130], [20, 1, 3]]
+    steps = 3
+    total = [sum(c) + steps for c in zip(*chunks)]
+    g = torch.Generator().manual_seed(3)
+    pages = [-(-t // P) for t in total]
+    perm = torch.randperm(sum(pages) + 2, generator=g).int()
+    bt = torch.zeros((B, max(pages)), dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(pages):
+        bt[b, :n] = perm[at:at + n]
+        at += n
+    kc, vc = (torch.zeros((sum(pages) + 2, P, KVH, D), dtype=torch.bfloat16, device=DEV)
+              for _ in range(2))
+    tab = fda.rotary_table(max(total), rot, theta=10000.0)
+    host = torch.from_numpy(ref.table(max(total), rot, 10000.0))
+    btd = bt.to(DEV)
+    ws = fda.alloc_prefill_workspace(D)
+    K = [torch.zeros((0, KVH, D), dtype=torch.float64) for _ in range(B)]
+    V = [torch.zeros((0, KVH, D), dtype=torch.float64) for _ in range(B)]
+    seq = [0] * B
+
+    def turned(x, pos):   # rounded to bf16, as the cache and q_out are
+        return ref.rotate(x, host, pos, rot, False, torch.float64).bfloat16().double()
+
+    def expect(q, new):
+        outs = []
+        for b, n in enumerate(new):
+            for j in range(n):
+                i = sum(new[:b]) + j
+                pos = torch.tensor([seq[b] - n + j])
+                qq = turned(q[i:i + 1], pos)[0]
+                k, v = K[b][:seq[b] - n + j + 1], V[b][:seq[b] - n + j + 1]
+                k, v = (x.repeat_interleave(QH // KVH, 1) for x in (k, v))
+                w = torch.softmax(torch.einsum("hd,thd->ht", qq, k) * D ** -0.5, -1)
+                outs.append(torch.einsum("ht,thd->hd", w, v))
+        return torch.stack(outs)
+
+    def write(k, v, new):
+        for b, n in enumerate(new):
+            i = sum(new[:b])
+            pos = torch.arange(seq[b], seq[b] + n)
+            K[b] = torch.cat([K[b], turned(k[i:i + n], pos)])
+            V[b] = torch.cat([V[b], v[i:i + n].double()])
+            seq[b] += n
+
+    for new in chunks + [[1] * B] * steps:
+        n = sum(new)
+        q, k, v = (torch.randn((n, h, D), generator=g).bfloat16() for h in (QH, KVH, KVH))
+        pos = torch.tensor(seq, dtype=torch.int32, device=DEV)
+        write(k, v, new)
+        sl = torch.tensor(seq, dtype=torch.int32, device=DEV)
+        qs = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=DEV)
+        if new != [1] * B:
+            out, _ = fda.prefill_attention(q.to(DEV), kc, vc, qs, sl, block_table=btd,
+                                           k_new=k.to(DEV), v_new=v.to(DEV), positions=pos,
+                                           rotary=tab, workspace=ws)
+        else:
+            qt = fda.append_kv(k.to(DEV), v.to(DEV), kc, vc, qs, pos, q=q.to(DEV), rotary=tab,
+                               block_table=btd, workspace=ws)
+            out, _ = fda.decode_attention(qt, kc, vc, sl, block_table=btd)
+        torch.cuda.synchronize()
+        want = expect(q, new)
+        # the cache and the queries may round the other way where fp32 and
+        # 64-bit rotations straddle a tie: one bf16 step in rare elements
+        assert float((out.double().cpu() - want).abs().max()) <= 3e-2
+        assert float((out.double().cpu() - want).norm() / want.norm()) <= 2.0 ** -8
+    ko, vo = fda.read_kv(kc, vc, torch.tensor(np.concatenate([[0], np.cumsum(seq)]),
+                                              dtype=torch.int32, device=DEV), sum(seq),
+                         block_table=btd, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(vo.double().cpu(), torch.cat(V))
+    d = (ko.double().cpu() - torch.cat(K)).abs()
+    assert torch.all(d <= 2.0 ** -7 * torch.cat(K).abs() + 2.0 ** -20)
+    _ok(fda, ws)
+
+
+def test_prompt_path_in_a_graph():
+    """The prompt path captured once and replayed after queries, new rows and
+    lengths change in place; a second graph shares the workspace."""
+    fda = lib()
+    bt = ref.Batch([60, 1, 20], [100, 300, 0], 2, 64, "e4m3", 16, seed=12)
+    f = ref.Filled(bt, seed=12)
+    kw, ix = f.device(DEV), bt.index(DEV)
+    ws = fda.alloc_prefill_workspace(64)
+    qs = torch.from_numpy(bt.q_start).to(DEV)
+    sl = torch.tensor(bt.seq, dtype=torch.int32, device=DEV)
+    bufs = [torch.zeros((bt.tokens, 8, 64), dtype=torch.float16, device=DEV) for _ in range(2)]
+    graphs, outs = [], []
+    for q in bufs:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            fda.prefill_attention(q, kw["k_cache"], kw["v_cache"], qs, sl, k_scale=kw["k_scale"],
+                                  v_scale=kw["v_scale"], workspace=ws, **ix)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fda.prefill_attention(q, kw["k_cache"], kw["v_cache"], qs, sl,
+                                              k_scale=kw["k_scale"], v_scale=kw["v_scale"],
+                                              workspace=ws, **ix))
+        graphs.append(g)
+    for step in range(3):
+        for i in (0, 1):
+            q = _queries(bt, 8, "f16", 20 + 2 * step + i)
+            bufs[i].copy_(q)
+            if step == 2:   # shorter sequences: the last rows are new tokens again
+                bt.seq = [140, 260, 20]
+                sl.copy_(torch.tensor(bt.seq, dtype=torch.int32))
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            want, wlse = ref.attention_blocks(f, q, 8, 0.125)
+            _compare(f, outs[i][0].double().cpu(), outs[i][1].double().cpu(), want, wlse, "f16")
+    _ok(fda, ws)
+
+
+def test_prompt_path_on_other_streams():
+    """Two streams at once, each with its own workspace and inputs; a stream
+    given by its handle."""
+    fda = lib()
+    cases = []
+    for i in range(2):
+        bt = ref.Batch([150, 1, 33], [0, 500, 7], 2, 128, "bf16", 16, seed=30 + i)
+        f = ref.Filled(bt, seed=30 + i)
+        q = _queries(bt, 8, "bf16", 30 + i)
+        cases.append((bt, f, q, f.device(DEV), bt.index(DEV), torch.from_numpy(bt.q_start).to(DEV),
+                      torch.tensor(bt.seq, dtype=torch.int32, device=DEV), q.to(DEV),
+                      fda.alloc_prefill_workspace(128), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    res = []
+    for rep in range(4):
+        for i, (bt, f, q, kw, ix, qs, sl, qd, ws, st) in enumerate(cases):
+            out = fda.prefill_attention(qd, kw["k_cache"], kw["v_cache"], qs, sl, workspace=ws,
+                                        stream=st if rep % 2 else st.cuda_stream, **ix)
+            res.append((i, out))
+    # without a workspace of the caller's, on a stream of its own
+    bt, f, q, kw, ix, qs, sl, qd, ws, st = cases[0]
+    res.append((0, fda.prefill_attention(qd, kw["k_cache"], kw["v_cache"], qs, sl, stream=st, **ix)))
+    torch.cuda.synchronize()
+    for i, (out, lse) in res:
+        bt, f, q = cases[i][:3]
+        want, wlse = ref.attention_blocks(f, q, 8, 128 ** -0.5)
+        _compare(f, out.double().cpu(), lse.double().cpu(), want, wlse, "bf16")
+
+
+def test_prompt_path_far_into_a_large_cache():
+    """Rows whose element offsets pass 32 bits (a 5 GB cache)."""
+    fda = lib()
+    rows, KVH, D = 5 * 10 ** 6, 8, 128
+    kc, vc = (torch.zeros((rows, KVH, D), dtype=torch.uint8, device=DEV) for _ in range(2))
+    start = rows - 300
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn((200, KVH, D), generator=g).half() for _ in range(2))
+    q = torch.randn((200, 8, D), generator=g).half()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    qs, sl = torch.tensor([0, 200], **i32), torch.tensor([200], **i32)
+    first = torch.tensor([start], **i32)
+    ws = fda.alloc_prefill_workspace(D)
+    scale = 5.0 / 448
+    out, lse = fda.prefill_attention(q.to(DEV), kc, vc, qs, sl, kv_start_idx=first,
+                                     k_new=k.to(DEV), v_new=v.to(DEV),
+                                     positions=torch.tensor([0], **i32), k_scale=scale,
+                                     v_scale=scale, workspace=ws)
+    ko, vo = fda.read_kv(kc, vc, qs, 200, kv_start_idx=first, k_scale=scale, v_scale=scale,
+                         workspace=ws)
+    torch.cuda.synchronize()
+    _ok(fda, ws)
+    assert int(kc[:start].count_nonzero()) == 0 and int(kc[start + 200:].count_nonzero()) == 0
+    kd, vd = ko.double().cpu(), vo.double().cpu()
+    assert float((kd - k.double()).abs().max()) <= 2.0 ** -4 * 5     # e4m3: half a step
+    s = torch.einsum("ihd,thd->hit", q.double(), kd) * D ** -0.5
+    s = s.masked_fill(torch.triu(torch.ones(200, 200, dtype=torch.bool), 1), -math.inf)
+    want = torch.einsum("hit,thd->ihd", torch.softmax(s, -1), vd)
+    assert float((out.double().cpu() - want).abs().max()) <= 2.0 ** -10 * 5.5 + 2.0 ** -10
