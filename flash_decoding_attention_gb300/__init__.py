@@ -167,12 +167,13 @@ def load_library(path: Optional[str] = None):
 # The current stream's handle without a Stream object around it (a few
 # microseconds a call); the public way where this torch does not have it.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
         if _current_raw_stream is not None:
-            return _current_raw_stream(torch.cuda.current_device())
+            return _current_raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return stream
@@ -635,7 +636,7 @@ def _on(device, stream):
     """Context in which ``device``, and ``stream`` if one is given, are current:
     what a call allocates for itself then belongs to the stream that uses it."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if device.index == _current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
             torch.cuda.default_stream(device)
