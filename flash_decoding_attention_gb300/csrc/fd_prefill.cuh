@@ -1020,6 +1020,11 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
       if constexpr (TOK) {
         ks = ks1 * p.score_scale;
         vs = vs1;
+        // the V scale of a key that some row does not see: as V's elements
+        if (!isfinite(vs) && j * kTile + t >= unseen) {
+          vs = 0.f;
+          *(volatile int*)&c.nf[sn & 7] = sn + 1;
+        }
         load_scales(j + 1, page2);
         page2 = page_of(seg, j + 2);
       }
@@ -1113,21 +1118,27 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
 // ---------------------------------------------------------------------------
 // Elements of V that are not finite, in the keys [lo, hi) of a sequence: added
 // to this row's 32 dims from d0 (see the file comment; off every fast path).
-template <int D, int KV, bool BF16>
-__device__ __forceinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int lo, int hi,
+template <int D, int KV, bool BF16, bool TOK>
+__device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int lo, int hi,
                                            int d0, float* o) {
   for (int t = lo; t < hi; ++t) {
     const long long row = placed_row(p.at, seg.b, t);
     if (row < 0) continue;
     const long long at = (row * p.num_kv_heads + seg.h) * D + d0;
+    const float scale = TOK ? __ldg(p.v_scales + row * p.num_kv_heads + seg.h) : 1.f;
     for (int i = 0; i < 32; ++i) {
       float x;
       if constexpr (KV == 0) {
         if constexpr (BF16) x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v)[at + i]);
         else x = __half2float(static_cast<const __half*>(p.v)[at + i]);
+      } else if constexpr (KV == 1) {
+        __nv_fp8_e4m3 e;
+        e.__x = static_cast<const uint8_t*>(p.v)[at + i];
+        x = static_cast<float>(e);
       } else {
-        x = (static_cast<const uint8_t*>(p.v)[at + i] & 0x7F) == 0x7F ? NAN : 0.f;
+        x = static_cast<float>(static_cast<const int8_t*>(p.v)[at + i]);
       }
+      x *= scale;
       if (!isfinite(x)) o[i] += x;
     }
   }
@@ -1214,8 +1225,7 @@ struct Softmax {
   // P of scores 32 k .. into 16 columns of tensor memory, over scores that
   // were read before; their sum into `sum`.
   __device__ __forceinline__ void exponents(const float (&x)[32], int k, uint64_t sc2, uint64_t nm2,
-                                            const float* vs, int left, bool all,
-                                            uint64_t (&sum)[4]) const {
+                                            const float* vs, uint64_t (&sum)[4]) const {
     uint32_t pk[16];
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -1231,14 +1241,7 @@ struct Softmax {
         pa = mul2(pa, va);
         pb = mul2(pb, vb);
       }
-      float2 qa = unpack2(pa), qb = unpack2(pb);
-      if (TOK && !all) {   // 0 times an excluded key's scale, whatever that is
-        const int t = 32 * k + i;
-        qa.x = t < left ? qa.x : 0.f;
-        qa.y = t + 1 < left ? qa.y : 0.f;
-        qb.x = t + 2 < left ? qb.x : 0.f;
-        qb.y = t + 3 < left ? qb.y : 0.f;
-      }
+      const float2 qa = unpack2(pa), qb = unpack2(pb);
       pk[i / 2] = pack16<BF16>(qa.x, qa.y);
       pk[i / 2 + 1] = pack16<BF16>(qb.x, qb.y);
     }
@@ -1356,7 +1359,7 @@ struct Softmax {
       tmem_wait_ld();
       arrived(x[k & 1]);
       if (k < 3) fetch(tS, x[(k + 1) & 1], k + 1);
-      exponents(x[k & 1], k, sc2, nm2, vs, left, whole, sum);
+      exponents(x[k & 1], k, sc2, nm2, vs, sum);
       if (k == 1) publish(&c.p_half[X]);
     }
     publish(&c.p_full[X]);
@@ -1529,12 +1532,12 @@ struct Softmax {
             }
           }
           if (!warp_live) continue;
-          if (KV != 2 && nonfinite && mine) {
+          if ((KV != 2 || TOK) && nonfinite && mine) {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = o[i];
             const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
-            add_nonfinite<D, KV, BF16>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
+            add_nonfinite<D, KV, BF16, TOK>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = x[i];
           }
