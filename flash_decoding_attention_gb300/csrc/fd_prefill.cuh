@@ -1144,20 +1144,16 @@ __device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int
   }
 }
 
-// Turns 16-byte chunks among four neighbouring lanes: v[t] of lane 4 i + q
-// becomes v[q] of lane 4 i + t (two rounds of exchanges).
-__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
-  auto swap = [&](uint4& keep0, uint4& keep1, int bit) {   // lanes without `bit` give keep1
-    uint4& give = lane & bit ? keep0 : keep1;
-    give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
-    give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
-    give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
-    give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
-  };
-  swap(v[0], v[1], 1);
-  swap(v[2], v[3], 1);
-  swap(v[0], v[2], 2);
-  swap(v[1], v[3], 2);
+// 32 bytes in one store (a whole sector) where the address allows it.
+__device__ __forceinline__ void store32(void* at, const uint4& a, const uint4& b, bool whole) {
+  if (whole)
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  else {
+    static_cast<uint4*>(at)[0] = a;
+    static_cast<uint4*>(at)[1] = b;
+  }
 }
 
 template <int D, int KV, bool CONV, bool BF16, bool TOK>
@@ -1491,12 +1487,10 @@ struct Softmax {
       }
       const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
       if (writes && (warp_live || swap)) {
-        // this row's place in the output; its lane's four neighbours write each
-        // other's rows, their chunks turned
-        const int lane4 = lane & 3, row4 = r & ~3;
-        const long long mine_at = ((long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
-                                   (long long)seg.h * p.group + rhead) * D;
-#pragma unroll 1
+        const long long out_at = ((long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
+                                  (long long)seg.h * p.group + rhead) * D;
+        const bool sectors = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll(D == 64 ? 2 : 1)
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
           if (any && warp_live) {
@@ -1541,6 +1535,7 @@ struct Softmax {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = x[i];
           }
+          if (!mine) continue;
           if (seg.complete) {
             uint4 v[4];
 #pragma unroll
@@ -1549,15 +1544,10 @@ struct Softmax {
                                 pack16<BF16>(o[8 * i + 2], o[8 * i + 3]),
                                 pack16<BF16>(o[8 * i + 4], o[8 * i + 5]),
                                 pack16<BF16>(o[8 * i + 6], o[8 * i + 7]));
-            transpose4(v, lane);   // four lanes write 64 bytes of one row
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const long long at = __shfl_sync(0xffffffffu, mine_at, t, 4);
-              if (row4 + t < live_rows)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + c0 + 8 * lane4) =
-                    v[t];
-            }
-          } else if (mine) {
+            uint16_t* at = static_cast<uint16_t*>(p.out) + out_at + c0;
+            store32(at, v[0], v[1], sectors);
+            store32(at + 16, v[2], v[3], sectors);
+          } else {
             // partial states: [slot][query tile][dim / 4][row][4]
             float4* pa = reinterpret_cast<float4*>(p.part_acc) +
                          ((long long)(2 * seg.slot + qt) * (D / 4) + c0 / 4) * kRowsTile + r;
@@ -1570,7 +1560,7 @@ struct Softmax {
           if (!seg.complete) {
             p.part_ml[(long long)(2 * seg.slot + qt) * kRowsTile + r] = make_float2(m_out, l);
           } else if (p.lse) {
-            p.lse[mine_at / D] = l == 0.f ? -INFINITY : (m_out + log2f(l)) * kLn2;
+            p.lse[out_at / D] = l == 0.f ? -INFINITY : (m_out + log2f(l)) * kLn2;
           }
         }
       }
