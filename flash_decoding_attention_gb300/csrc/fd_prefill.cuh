@@ -15,17 +15,27 @@
 // the softmax of one runs while the tensor cores work for the other.
 //
 // Split.  (sequence, KV head, pair of query tiles) are the streams.  Their
-// costs (keys to pass, once per active query tile, plus a start) are laid
-// end to end and cut into one equal range per CTA, whatever the lengths: a
-// long prompt's causal triangle, a chunk over a long context and single
-// tokens beside them all fill the GPU.  A stream cut between CTAs leaves
+// costs (keys to pass plus a start) are laid end to end and cut into one
+// equal range per CTA, whatever the lengths: a long prompt's causal triangle,
+// a chunk over a long context and single tokens beside them all fill the GPU.  A stream cut between CTAs leaves
 // partial states (m, l, unnormalised out) that fd_prefill.cu merges in a
-// fixed order.
+// fixed order.  A pair with rows in A only (a solo segment: single tokens, a
+// chunk's end) has its keys shared between the two halves of the CTA instead,
+// which merge their states through shared memory: the time of a tile is a
+// chain (S, softmax, P V), the same for one query tile as for two.
+//
+// What bounds it, on GB300 (152 SMs), bf16, 32 query / 8 KV heads, D = 128:
+// 2048 new tokens over 30000 cached ones run at 1.60 PFLOP/s, 0.83 of the
+// cuBLAS burst rate and 0.93 of its sustained one: the tensor cores (and the
+// power limit).  Whole prompts, with a start and an end for every 33 tiles or
+// so, run at 1.33 PFLOP/s.  With 8-bit caches the widened copies compete with
+// the products for shared memory's port (e4m3 / f16 1.54 PFLOP/s).  Decode-like
+// batches (one token over 4096 keys, bf16) read the cache at 5.5 TB/s.
 //
 // Roles (one persistent CTA per SM):
-//   warps 0-3, 4-7  softmax of query tile A, B: one row per thread, the row's
-//                   128 scores in registers; P overwrites S in tensor memory
-//                   as 16-bit pairs;
+//   warps 0-3, 4-7  softmax of query tile A, B: one row per thread, its scores
+//                   read from tensor memory twice (maximum, probabilities);
+//                   P overwrites S there as 16-bit pairs;
 //   warp 8          TMA producer: Q tiles, K and V tiles through one ring;
 //   warp 9          issues S = Q K^T and O += P V for A and B as their inputs
 //                   become ready (O and S: 2 x 128 columns each, all 512);
@@ -69,7 +79,9 @@ constexpr int kRowsPair = 2 * kRowsTile;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
 constexpr int kPages = 20;          // block-table entries staged at a time (a tile has 16)
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
-// Cost of a segment start (Q load, first product, epilogue), in keys.
+// Cost of a segment start (Q load, first product, epilogue), in keys.  Four
+// bf16 prompts of 8192 tokens in all: 480 us at 320 and 480, 438 at 640, 495
+// at 800, 448 at 1000.
 constexpr long long kStartCost = 640;
 
 // ---------------------------------------------------------------------------
@@ -109,8 +121,8 @@ __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   s.T = max(0, __ldg(p.seq_len + b));
   s.q0 = lo;
   s.n = hi - lo;
-  if (lo < 0 || hi < lo || hi > p.tokens) {
-    if (report) raise_error(p.at.ws, kErrBounds, lo < 0 ? lo : hi);
+  if (lo < 0 || hi < lo || hi > p.tokens || s.T > 0x7fffff00) {   // (tile ends stay int)
+    if (report) raise_error(p.at.ws, kErrBounds, lo < 0 ? lo : hi < lo || hi > p.tokens ? hi : s.T);
     s.n = 0;
   }
   s.ctx = s.T - s.n;
@@ -311,7 +323,8 @@ struct Control {
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], fin;
   uint64_t x_full, x_empty;   // exchange between the softmax halves of a solo segment
   int info[8];      // what the tensor cores do with tile j (slot j mod 8), kInfo bits
-  int nf[8];        // segment i (slot i mod 8) + 1 when its V held masked non-finite elements
+  int nf[8];        // i + 1 (slot i mod 8) when V of segment i, of those with tiles, held
+                    // non-finite elements that some row does not see
   int abort_flag;
   int swaps;        // exchanges of solo segments that are over
   uint32_t tmem_base;
@@ -371,15 +384,6 @@ __device__ __forceinline__ bool wait_for(Control& c, const Prefill& p, uint64_t*
 __device__ __forceinline__ bool wait_warp(Control& c, const Prefill& p, uint64_t* bar,
                                           uint32_t parity, int role) {
   return __all_sync(0xffffffffu, wait_for(c, p, bar, parity, role));
-}
-
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------------------
@@ -892,7 +896,8 @@ __device__ __forceinline__ void fixers(const Prefill& p, Walk walk, Control& c,
   const int lane = threadIdx.x & 31, ft = threadIdx.x - kFixWarp0 * 32;
   Seg seg;
   int n = 0, fixes = 0, sn = 0;
-  for (; walk.next(p, seg); ++sn) {
+  // (sn counts the segments that have tiles)
+  for (; walk.next(p, seg); sn += seg.te > seg.tb) {
     const int unseen = first_unseen(seg, 2 * p.tile_tokens);
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
 #pragma unroll 1
@@ -996,7 +1001,7 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
   };
   Seg seg;
   int n = 0, sn = 0;
-  for (; walk.next(p, seg); ++sn) {
+  for (; walk.next(p, seg); sn += seg.te > seg.tb) {
     const int unseen = first_unseen(seg, 2 * p.tile_tokens);
     const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
     // per-token scales run one tile ahead, their block-table entries two
@@ -1372,7 +1377,6 @@ struct Softmax {
   }
 
   __device__ void run(Walk walk) {
-    const int rows = p.tile_tokens * p.group;
     const int rtok = r / p.group, rhead = r - rtok * p.group;
     Seg seg;
     int n = 0, done = 0, segs = 0, sn = 0;
@@ -1380,10 +1384,10 @@ struct Softmax {
     // streams of the two partial slots, for the merge
     int4 used0 = make_int4(-1, 0, 0, 0), used1 = used0;
     bool dead = false;
-    for (; !dead && walk.next(p, seg); ++sn) {
+    for (; !dead && walk.next(p, seg); sn += seg.te > seg.tb) {
       const int qt = seg.solo ? 0 : X;                     // query tile of this half
       const int tok0 = (2 * seg.m + qt) * p.tile_tokens;   // its first token
-      const int live_rows = min(rows, max(0, (seg.n - tok0) * p.group));
+      const int live_rows = min(p.tile_tokens, max(0, seg.n - tok0)) * p.group;
       const bool mine = r < live_rows;
       const bool warp_live = 32 * w4 < live_rows;
       // keys this row sees; a row of nobody never restricts its warp
@@ -1485,7 +1489,7 @@ struct Softmax {
         osc *= q;
         bsc *= q;
       }
-      const bool nonfinite = *(volatile int*)&c.nf[sn & 7] == sn + 1;
+      const bool nonfinite = seg.te > seg.tb && *(volatile int*)&c.nf[sn & 7] == sn + 1;
       if (writes && (warp_live || swap)) {
         const long long out_at = ((long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
                                   (long long)seg.h * p.group + rhead) * D;
@@ -1606,7 +1610,10 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   float* scales = reinterpret_cast<float*>(base + SH::kOffCtl + kCtlBytes);
   const int warp = threadIdx.x >> 5;
   if (smem_u32(base) & 1023u) {   // the swizzled operands need whole atoms
-    if (threadIdx.x == 0) raise_error(p.at.ws, kErrPlan, 0);
+    if (threadIdx.x == 0) {
+      raise_error(p.at.ws, kErrPlan, 0);
+      p.meta[2 * blockIdx.x].x = p.meta[2 * blockIdx.x + 1].x = -1;
+    }
     return;
   }
   if (threadIdx.x == 0) {
