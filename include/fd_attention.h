@@ -576,6 +576,8 @@ fd_status fd_debug_gather_kv(const void *cache, const int32_t *kv_start_idx,
  * one-second bound and reports FD_ERR_DEVICE_TIMEOUT too when it gives up.
  * Process-wide, from the next call on; wait_ns outside [0, 1e10] is
  * FD_ERR_INVALID_ARG.  The CUDA-core split kernel has no such waits.
+ * fd_prefill_attention's waits keep the same limit, and its producer the same
+ * switch.
  */
 fd_status fd_debug_set_wait_limit(int64_t wait_ns, int starve_first_stage);
 

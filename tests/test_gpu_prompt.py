@@ -46,6 +46,23 @@ def test_rotary_table(positions, rot, theta, scaling, factor, amplitude):
     assert np.all(got[0, :rot // 2] == np.float32(amplitude)) and np.all(got[0, rot // 2:] == 0)
 
 
+@pytest.mark.parametrize("positions,rot", [(2432, 128), (2433, 128), (38913, 128), (320007, 128),
+                                           (155649, 16), (25537, 96)])
+def test_rotary_table_in_many_steps(positions, rot):
+    """Tables of one step, of several and of more blocks than fit at once, with
+    ends inside a step; every 61st row and the last ones."""
+    fda = lib()
+    got = fda.rotary_table(positions, rot, theta=1e6)
+    at = torch.cat([torch.arange(0, positions, 61), torch.arange(positions - 40, positions)])
+    f = 1e6 ** (-2 * torch.arange(rot // 2, dtype=torch.float64) / rot)
+    x = at.double()[:, None] * f
+    want = torch.cat([x.cos(), x.sin()], dim=1)
+    # as above (its bound covers the two levels of sums too: 4.43 * 2^-24); the
+    # angles of this statement are good to p * 2^-52 (f) and p * 2^-53 (product)
+    tol = (math.pi / 2 + 3) * 2.0 ** -24 + positions * 2.0 ** -51
+    assert (got[at.to(DEV)].double().cpu() - want).abs().max().item() <= tol
+
+
 def test_rotary_table_keeps_small_angles_and_a_given_buffer():
     fda = lib()
     buf = torch.full((3, 128), 7.0, device=DEV)

@@ -1,6 +1,9 @@
 """CPU checks of the prompt path's arguments: the C entry points refuse bad
 ones on the host, before any device work (fake pointers are never
 dereferenced), and the torch wrappers refuse bad tensors."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -119,6 +122,17 @@ def _prefill(c, **over):
 ])
 def test_prefill_refusals(c, over, status):
     assert _prefill(c, **over) == status
+
+
+def test_binding_has_the_headers_rotary_values():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                        "fd_attention.h")
+    with open(path) as f:
+        values = dict(re.findall(r"(FD_ROTARY_\w+) = (\d+)", f.read()))
+    assert len(values) == 3 and set(int(x) for x in values.values()) == \
+        set(fda.ROTARY_SCALINGS.values())
+    for name, x in values.items():
+        assert getattr(fda, name) == int(x)
 
 
 def test_prefill_workspace_of_a_bad_head_dim(c):
