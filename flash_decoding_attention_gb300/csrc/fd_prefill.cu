@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
         int parts = 2;   // the beginning and this continuation
         while (c + parts - 1 < p.grid && same(first[c + parts - 1], id)) ++parts;
         parts_of[c] = (short)parts;
-        const Seq s = load_seq(p, id.x, false);
+        const Seq s = load_seq<false>(p, id.x, false);
         const int blocks = (mg.live_rows(s, id.z, 0) + 31) / 32 + (mg.live_rows(s, id.z, 1) + 31) / 32;
         items[parts <= kFew ? 0 : 1] = blocks * (D / 16);
       }
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   for (int item = blockIdx.x * kMergeWarps + warp; item < carry[0];
        item += gridDim.x * kMergeWarps) {
     Part it = part_at(0, item);
-    const Seq s = load_seq(p, it.id.x, false);
+    const Seq s = load_seq<false>(p, it.id.x, false);
     const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
     it.X = it.row0 >= rows_a ? 1 : 0;
     if (it.X) it.row0 -= rows_a;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
   for (int item = blockIdx.x; item < carry[1]; item += gridDim.x) {
     Part it = part_at(1, item);
-    const Seq s = load_seq(p, it.id.x, false);
+    const Seq s = load_seq<false>(p, it.id.x, false);
     const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
     it.X = it.row0 >= rows_a ? 1 : 0;
     if (it.X) it.row0 -= rows_a;

@@ -40,6 +40,7 @@
 //   warp 9          issues S = Q K^T and O += P V for A and B as their inputs
 //                   become ready (O and S: 2 x 128 columns each, all 512);
 //   warps 10-11     repair V tiles that some row may not see (see below);
+//                   With a scale per token they fetch the scales instead;
 //   warps 12-15     (8-bit caches, or pages of fewer than 8 rows) widen or
 //                   copy the cache rows into the ring; the producer then feeds
 //                   raw tiles to them.
@@ -81,8 +82,12 @@ constexpr int kPages = 20;          // block-table entries staged at a time (a t
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
 // Cost of a segment start (Q load, first product, epilogue), in keys.  Four
 // bf16 prompts of 8192 tokens in all: 480 us at 320 and 480, 438 at 640, 495
-// at 800, 448 at 1000.
-constexpr long long kStartCost = 640;
+// at 800, 448 at 1000.  With a scale per token a tile takes longer, its start
+// does not: a mixed INT8 batch takes 264 us at 320, 269 at 480, 279 at 640.
+template <bool TOK>
+struct Cost {
+  static constexpr int kStart = TOK ? 320 : 640;
+};
 
 // ---------------------------------------------------------------------------
 // Streams and their split
@@ -99,13 +104,16 @@ __device__ __forceinline__ int pair_end(const Seq& s, int m) {
   return e > 0 ? e : 0;
 }
 
+template <bool TOK>
 __device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
-  return kStartCost + (long long)pair_end(s, m);
+  const long long end = pair_end(s, m);
+  return Cost<TOK>::kStart + end;
 }
 
 // Cost of pairs 0 .. m - 1 (m < pairs: all of them are full).
+template <bool TOK>
 __device__ __forceinline__ long long pairs_before(const Seq& s, int m) {
-  long long c = (long long)m * kStartCost;
+  long long c = (long long)m * Cost<TOK>::kStart;
   const int m0 = s.ctx >= 0 ? 0 : -s.ctx / s.span;   // pairs without keys
   if (m > m0) {
     const long long a = m, b = m0;
@@ -114,6 +122,7 @@ __device__ __forceinline__ long long pairs_before(const Seq& s, int m) {
   return c;
 }
 
+template <bool TOK>
 __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   Seq s;
   s.b = b;
@@ -128,7 +137,7 @@ __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   s.ctx = s.T - s.n;
   s.span = 2 * p.tile_tokens;
   s.pairs = (int)(((unsigned)s.n + (unsigned)s.span - 1u) / (unsigned)s.span);
-  s.head = s.n > 0 ? pairs_before(s, s.pairs - 1) + pair_cost(s, s.pairs - 1) : 0;
+  s.head = s.n > 0 ? pairs_before<TOK>(s, s.pairs - 1) + pair_cost<TOK>(s, s.pairs - 1) : 0;
   return s;
 }
 
@@ -139,12 +148,13 @@ struct Plan {
 };
 
 // Every thread of the CTA gets the plan; `red` is 34 long longs of shared memory.
+template <bool TOK>
 __device__ inline Plan make_plan(const Prefill& p, long long* red) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int B = p.at.batch;
   long long mine = 0, v0 = 0;
   for (int b = tid; b < B; b += blockDim.x) {
-    const long long v = load_seq(p, b, blockIdx.x == 0).head * p.num_kv_heads;
+    const long long v = load_seq<TOK>(p, b, blockIdx.x == 0).head * p.num_kv_heads;
     if (b == tid) v0 = v;
     mine += v;
   }
@@ -167,7 +177,7 @@ __device__ inline Plan make_plan(const Prefill& p, long long* red) {
   long long carry = 0;
   for (int base = 0; base < B; base += blockDim.x) {
     const int b = base + tid;
-    const long long v = b >= B ? 0 : base == 0 ? v0 : load_seq(p, b, false).head * p.num_kv_heads;
+    const long long v = b >= B ? 0 : base == 0 ? v0 : load_seq<TOK>(p, b, false).head * p.num_kv_heads;
     long long x = v;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -206,6 +216,7 @@ struct Seg {
 };
 
 // The segments of this CTA, in order; every role walks its own copy.
+template <bool TOK>
 struct Walk {
   long long g, g_end, ps;
   Seq s;
@@ -216,29 +227,29 @@ struct Walk {
     g_end = min(g + pl.per_cta, pl.total);
     ps = g_end;
     if (g >= pl.total || pl.b >= p.at.batch) return;
-    s = load_seq(p, pl.b, false);
+    s = load_seq<TOK>(p, pl.b, false);
     const long long off = g - pl.first;
     h = (int)(off / s.head);
     const long long r = off - h * s.head;
     int lo = 0, hi = s.pairs;   // the last pair that begins at or before r
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pairs_before(s, mid) <= r) lo = mid;
+      if (pairs_before<TOK>(s, mid) <= r) lo = mid;
       else hi = mid;
     }
     m = lo;
-    ps = pl.first + h * s.head + pairs_before(s, m);
+    ps = pl.first + h * s.head + pairs_before<TOK>(s, m);
   }
 
   __device__ __forceinline__ bool next(const Prefill& p, Seg& o) {
     while (ps < g_end) {
       const int end = pair_end(s, m);
-      const long long cost = kStartCost + end;
+      const long long cost = pair_cost<TOK>(s, m);
       const int n = (end + kTile - 1) / kTile;
       const long long a = g > ps ? g : ps, e = ps + cost < g_end ? ps + cost : g_end;
-      // tile i stands at ps + kStartCost + 128 i and belongs to the range that
-      // holds this point
-      const long long xa = a - ps - kStartCost, xe = e - ps - kStartCost;
+      // tile i stands at ps + the start + i times its cost and belongs to the
+      // range that holds this point
+      const long long xa = a - ps - Cost<TOK>::kStart, xe = e - ps - Cost<TOK>::kStart;
       const int tb = xa <= 0 ? 0 : min(n, (int)((xa + kTile - 1) >> 7));
       const int te = xe <= 0 ? 0 : min(n, (int)((xe + kTile - 1) >> 7));
       const bool yields = n > 0 ? te > tb : g <= ps;
@@ -267,7 +278,7 @@ struct Walk {
           h = 0;
           int b = s.b + 1;
           for (; ps < g_end && b < p.at.batch; ++b) {
-            s = load_seq(p, b, false);
+            s = load_seq<TOK>(p, b, false);
             if (s.n > 0) break;
           }
         }
@@ -506,8 +517,8 @@ struct TileCopy {
   static constexpr int kBoxElems = KV == 0 ? 64 : D;
 };
 
-template <int D, int KV, bool CONV>
-__device__ __forceinline__ void producer(const Prefill& p, Walk walk, Control& c,
+template <int D, int KV, bool CONV, bool TOK>
+__device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Control& c,
                                          uint8_t* base, const CUtensorMap* tmq,
                                          const CUtensorMap* tmk, const CUtensorMap* tmv) {
   using SH = Shape<D, KV, CONV>;
@@ -889,7 +900,7 @@ struct Mma {
 // Repair of V tiles in the ring (16-bit caches by TMA)
 // ---------------------------------------------------------------------------
 template <int D, bool BF16>
-__device__ __forceinline__ void fixers(const Prefill& p, Walk walk, Control& c,
+__device__ __forceinline__ void fixers(const Prefill& p, Walk<false> walk, Control& c,
                                        uint8_t* base) {
   using SH = Shape<D, 0, false>;
   constexpr int NS = SH::kSlots;
@@ -971,68 +982,20 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 // Converter warps: thread = key of the tile
 // ---------------------------------------------------------------------------
 template <int D, int KV, bool BF16, bool TOK>
-__device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control& c,
-                                           uint8_t* base, float* scales) {
+__device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Control& c,
+                                           uint8_t* base) {
   using SH = Shape<D, KV, true>;
   constexpr int NS = SH::kSlots;
   constexpr int NR = SH::kRawSlots > 0 ? SH::kRawSlots : 1;
   constexpr int kChunks = KV == 0 ? D / 8 : D / 16;   // 16-byte chunks of a cache row
   const int lane = threadIdx.x & 31, t = threadIdx.x - kConvWarp0 * 32;
   const uint32_t ring = smem_u32(base) + SH::kOffSlot, raw = smem_u32(base) + SH::kOffRaw;
-  using SR = ScaleRing<D, KV>;
-  // key of tile j that this thread carries: its cache row (unchecked), or -1
-  // behind the stream's last key; in two steps so that loads can run ahead
-  auto page_of = [&](const Seg& g, int j) -> int {
-    const int k = j * kTile + t;
-    if (j >= g.te || k >= g.end) return -1;
-    if (!p.at.block_table) return 0;
-    const int col = k >> p.at.page_shift;
-    return col < p.at.bt_stride
-               ? __ldg(p.at.block_table + (long long)g.b * p.at.bt_stride + col)
-               : -1;
-  };
-  auto row_of = [&](const Seg& g, int j, int page, long long start) -> long long {
-    const int k = j * kTile + t;
-    if (page < 0) return -1;
-    const long long row = p.at.block_table ? ((long long)page << p.at.page_shift) +
-                                                 (k & (p.at.page_size - 1))
-                                           : start + k;
-    return row >= 0 && row < p.at.kv_rows ? row : -1;
-  };
   Seg seg;
   int n = 0, sn = 0;
   for (; walk.next(p, seg); sn += seg.te > seg.tb) {
     const int unseen = first_unseen(seg, 2 * p.tile_tokens);
-    const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
-    // per-token scales run one tile ahead, their block-table entries two
-    float ks1 = 0.f, vs1 = 0.f;
-    int page2 = -1;
-    auto load_scales = [&](int j, int page) {
-      const long long row = row_of(seg, j, page, start);
-      ks1 = vs1 = 0.f;
-      if (row >= 0) {
-        ks1 = __ldg(p.k_scales + row * p.num_kv_heads + seg.h);
-        vs1 = __ldg(p.v_scales + row * p.num_kv_heads + seg.h);
-      }
-    };
-    if constexpr (TOK) {
-      load_scales(seg.tb, page_of(seg, seg.tb));
-      page2 = page_of(seg, seg.tb + 1);
-    }
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
       const int valid = min(kTile, seg.end - j * kTile);
-      float ks = 0.f, vs = 0.f;
-      if constexpr (TOK) {
-        ks = ks1 * p.score_scale;
-        vs = vs1;
-        // the V scale of a key that some row does not see: as V's elements
-        if (!isfinite(vs) && j * kTile + t >= unseen) {
-          vs = 0.f;
-          *(volatile int*)&c.nf[sn & 7] = sn + 1;
-        }
-        load_scales(j + 1, page2);
-        page2 = page_of(seg, j + 2);
-      }
       long long row = -1;
       int bad = 0;
       if (p.gather) {
@@ -1100,13 +1063,11 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
             sts128(dst + kmajor_chunk(kTile, t, 2 * i + 1), make_uint4(d.x, d.y, f.x, f.y));
           }
         }
-        if constexpr (TOK) scales[(kv ? SR::val(n) : SR::key(n)) + t] = kv ? vs : ks;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           if (!p.gather && KV != 0) mbar_arrive(&c.raw_empty[rs]);
           mbar_arrive(&c.full[slot]);
-          if (TOK && kv == 1) mbar_arrive(&c.fixed[n % SR::kValRing]);
         }
       }
     }
@@ -1115,6 +1076,87 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk walk, Control&
   if (!wait_warp(c, p, &c.empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 22)) return;
   if (t == 0) c.info[n & 7] = kInfoStop;
   __syncwarp();
+  if (lane == 0) mbar_arrive(&c.full[slot]);
+}
+
+// ---------------------------------------------------------------------------
+// Per-token scales: warps 10 and 11, keys t and t + 64 of the tile per thread
+// ---------------------------------------------------------------------------
+// Values are loaded one tile ahead, their block-table entries two.  Loaded by
+// the converters, between their other loads, they cost each tile a memory
+// latency: single tokens over INT8, 2.56 us a tile in place of 1.92 (the time
+// without scales per token), full tiles 2.88 in place of 2.69.  Widening is not
+// a work for these two warps: with six warps at it e4m3 under f16 fell from
+// 1500 to 1150 TFLOP/s.
+template <int D, int KV>
+__device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, Control& c,
+                                             float* scales) {
+  using SH = Shape<D, KV, true>;
+  using SR = ScaleRing<D, KV>;
+  constexpr int NS = SH::kSlots;
+  static_assert(NS % 2 == 0, "K tiles lie in the even slots");
+  const int lane = threadIdx.x & 31, t = threadIdx.x - kFixWarp0 * 32;
+  // page of key k of the stream, or -1 behind the last key of the segment
+  auto page_of = [&](const Seg& g, int j, int k) -> int {
+    if (j >= g.te || k >= g.end) return -1;
+    if (!p.at.block_table) return 0;
+    const int col = k >> p.at.page_shift;
+    return col < p.at.bt_stride
+               ? __ldg(p.at.block_table + (long long)g.b * p.at.bt_stride + col)
+               : -1;
+  };
+  Seg seg;
+  int n = 0, sn = 0;
+  for (; walk.next(p, seg); sn += seg.te > seg.tb) {
+    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
+    float ks[2], vs[2];
+    int page[2];
+    auto load = [&](int j) {   // of tile j, whose pages are at hand
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = j * kTile + t + 64 * i;
+        const long long row = p.at.block_table
+                                  ? ((long long)page[i] << p.at.page_shift) + (k & (p.at.page_size - 1))
+                                  : start + k;
+        ks[i] = vs[i] = 0.f;
+        if (page[i] >= 0 && row >= 0 && row < p.at.kv_rows) {
+          ks[i] = __ldg(p.k_scales + row * p.num_kv_heads + seg.h);
+          vs[i] = __ldg(p.v_scales + row * p.num_kv_heads + seg.h);
+        }
+        page[i] = page_of(seg, j + 1, k + kTile);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) page[i] = page_of(seg, seg.tb, seg.tb * kTile + t + 64 * i);
+    if (seg.te > seg.tb) load(seg.tb);
+    for (int j = seg.tb; j < seg.te; ++j, ++n) {
+      float k[2], v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        k[i] = ks[i] * p.score_scale;
+        v[i] = vs[i];
+        // the V scale of a key that some row does not see: as V's elements
+        if (!isfinite(v[i]) && j * kTile + t + 64 * i >= unseen) {
+          v[i] = 0.f;
+          *(volatile int*)&c.nf[sn & 7] = sn + 1;
+        }
+      }
+      load(j + 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = 2 * n + kv, slot = e % NS;
+        if (!wait_warp(c, p, &c.empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 23)) return;
+        float* to = scales + (kv ? SR::val(n) : SR::key(n)) + t;
+        to[0] = kv ? v[0] : k[0];
+        to[64] = kv ? v[1] : k[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv ? &c.fixed[n % SR::kValRing] : &c.full[slot]);
+      }
+    }
+  }
+  const int e = 2 * n, slot = e % NS;   // the end
+  if (!wait_warp(c, p, &c.empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 23)) return;
   if (lane == 0) mbar_arrive(&c.full[slot]);
 }
 
@@ -1376,7 +1418,7 @@ struct Softmax {
     return reinterpret_cast<float4*>(base + SH::kQTile) + d4 * kRowsTile + r;
   }
 
-  __device__ void run(Walk walk) {
+  __device__ void run(Walk<TOK> walk) {
     const int rtok = r / p.group, rhead = r - rtok * p.group;
     Seg seg;
     int n = 0, done = 0, segs = 0, sn = 0;
@@ -1618,14 +1660,15 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < SH::kSlots; ++i) {
-      mbar_init(&c.full[i], CONV ? 4 : 1);        // converter warps, or the producer
+      // the producer, or the converter warps and, with K tiles, the scale warps
+      mbar_init(&c.full[i], !CONV ? 1 : TOK && i % 2 == 0 ? 6 : 4);
       mbar_init(&c.empty[i], CONV ? 1 : 3);       // the last product (and the two repair warps)
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&c.raw_full[i], 1);
       mbar_init(&c.raw_empty[i], 4);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&c.fixed[i], CONV ? 4 : 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&c.fixed[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
@@ -1657,9 +1700,9 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
     }
   }
   tc_fence_before();
-  const Plan plan = make_plan(p, reinterpret_cast<long long*>(base));   // (barriers)
+  const Plan plan = make_plan<TOK>(p, reinterpret_cast<long long*>(base));   // (barriers)
   tc_fence_after();
-  Walk walk;   // every role walks its own copy
+  Walk<TOK> walk;   // every role walks its own copy
   walk.init(p, plan);
   const uint32_t tbase = c.tmem_base;
   allow_dependent_launch();
@@ -1673,15 +1716,17 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
     sm.run(walk);
   } else if (warp < kConvWarp0) {
     if (warp == kProducerWarp) {
-      producer<D, KV, CONV>(p, walk, c, base, &tmq, &tmk, &tmv);
+      producer<D, KV, CONV, TOK>(p, walk, c, base, &tmq, &tmk, &tmv);
     } else if (warp == kMmaWarp) {
       Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one(), {0, 0}, {0, 0}, 0};
       mm.run();
     } else if constexpr (!CONV) {
       fixers<D, BF16>(p, walk, c, base);
+    } else if constexpr (TOK) {
+      token_scales<D, KV>(p, walk, c, scales);
     }
   } else if constexpr (CONV) {
-    converters<D, KV, BF16, TOK>(p, walk, c, base, scales);
+    converters<D, KV, BF16, TOK>(p, walk, c, base);
   }
   tc_fence_before();
   __syncthreads();
