@@ -534,7 +534,7 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
   uint64_t keep;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
   Seg seg;
-  int n = 0, qn[2] = {0, 0}, swaps = 0;
+  int n = 0, issued = 0, qn[2] = {0, 0}, swaps = 0;   // issued: stages of the ring
   bool stop = p.starve != 0;
   const int box_rows = p.at.block_table && p.at.page_size < kTile ? p.at.page_size : kTile;
   while (!stop && walk.next(p, seg)) {
@@ -610,6 +610,7 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
           stop = true;
           break;
         }
+        issued = e + 1;
         uint8_t* dst = ring + (size_t)slot * kSlot;
         if (bad) {
           // a row outside the cache: the tile counts as absent (all scores
@@ -640,24 +641,23 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
     }
     stop = __any_sync(0xffffffffu, stop);
   }
+  // copies in flight must land before the CTA ends, which after a timeout the
+  // other warps do not wait for
+  if (lane == 0) {
+    bool late = false;
+    for (int e = max(0, issued - NS); e < issued; ++e)
+      late |= !mbar_wait(&full[e % NS], (uint32_t)((e / NS) & 1), mma::kDrainNs);
+    for (int x = 0; x < 2; ++x)
+      if (qn[x] > 0)
+        late |= !mbar_wait(&c.q_full[x], (uint32_t)((qn[x] - 1) & 1), mma::kDrainNs);
+    if (late) raise_error(p.at.ws, kErrDrain, 3);
+  }
+  __syncwarp();
   if (!stop && KV == 0 && !CONV) {   // (with converters they write the end)
     const int e = 2 * n, slot = e % NS;
     if (wait_warp(c, p, &empty[slot], (uint32_t)(((e / NS) & 1) ^ 1), 2) && lane == 0) {
       c.info[n & 7] = kInfoStop;
       mbar_arrive(&full[slot]);
-    }
-  }
-  if (stop && !p.starve) {
-    // copies in flight must land before the CTA ends
-    if (lane == 0) {
-      bool late = false;
-      if (tiles)
-        for (int e = max(0, 2 * n - NS); e < 2 * n; ++e)
-          late |= !mbar_wait(&full[e % NS], (uint32_t)((e / NS) & 1), mma::kDrainNs);
-      for (int x = 0; x < 2; ++x)
-        if (qn[x] > 0)
-          late |= !mbar_wait(&c.q_full[x], (uint32_t)((qn[x] - 1) & 1), mma::kDrainNs);
-      if (late) raise_error(p.at.ws, kErrDrain, 3);
     }
   }
   __syncwarp();

@@ -588,6 +588,29 @@ def test_attention_timeout_is_reported():
     _compare(f, out, lse, want, wlse, "f16")
 
 
+@pytest.mark.parametrize("kv,scales", [("f16", "tensor"), ("e4m3", "tensor"), ("i8", "token")])
+def test_attention_waits_that_run_out_in_the_middle(kv, scales):
+    """Limits so short that waits run out with copies and products in flight:
+    the call ends, reports it, and the next one is right."""
+    fda = lib()
+    bt = ref.Batch([300, 1, 64, 3], [40, 2000, 0, 900], 2, 128, kv, 64, seed=21)
+    f = ref.Filled(bt, seed=21, scales=scales)
+    q = _queries(bt, 8, "f16", 21)
+    ws = fda.alloc_prefill_workspace(128)
+    want, wlse = ref.attention_blocks(f, q, 8, 128 ** -0.5)
+    for limit in (1, 100, 1000, 5000, 30000):
+        fda.fd_debug_set_wait_limit(limit, False)
+        try:
+            for _ in range(4):
+                _attend(fda, f, q, 8, ws)
+                assert fda.fd_check_device_error(ws)[0] in (fda.FD_OK, fda.FD_ERR_DEVICE_TIMEOUT)
+        finally:
+            fda.fd_debug_set_wait_limit(0, False)
+    out, lse = _attend(fda, f, q, 8, ws)
+    _ok(fda, ws)
+    _compare(f, out, lse, want, wlse, "f16")
+
+
 # ---------------------------------------------------------------------------
 # together, on streams, in graphs
 # ---------------------------------------------------------------------------
