@@ -269,6 +269,11 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
   if (!std::isfinite(softmax_scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return FD_ERR_INVALID_ARG;
   if (kv_rows >= kMaxPacked) return FD_ERR_UNSUPPORTED;   // 32-bit TMA coordinates
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t width = (uintptr_t)num_q_heads * head_dim * 2;
+  if (num_tokens > 0 && q0 < o0 + (uintptr_t)num_tokens * width &&
+      o0 < q0 + (uintptr_t)(num_tokens - 1) * q_stride * 2 + width)
+    return FD_ERR_INVALID_ARG;
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
   if (workspace_bytes < prefill_layout(head_dim, sms).total) return FD_ERR_WORKSPACE_TOO_SMALL;

@@ -467,7 +467,8 @@ size_t fd_prefill_workspace_bytes(int head_dim);
  *
  * q          [num_tokens, num_q_heads, head_dim] of q_dtype, tokens q_stride
  *            elements apart (a multiple of 8, at least one token's heads).
- * out        dense [num_tokens, num_q_heads, head_dim] of q_dtype.
+ * out        dense [num_tokens, num_q_heads, head_dim] of q_dtype; must not
+ *            overlap q, whose rows are read by more than one thread block.
  * lse        fp32 [num_tokens, num_q_heads], or NULL.
  * num_tokens rows of q, out and lse (0: nothing to do); < 2^31.
  * workspace  >= fd_prefill_workspace_bytes(head_dim), 256-byte aligned.

@@ -119,6 +119,7 @@ def _prefill(c, **over):
     (dict(kv_start=None), 1), (dict(qdt=3), 1), (dict(qdt=1), 2),
     (dict(kind=1, kss=0xA000, vss=0xB000), 2), (dict(kind=2, kvdt=3, kss=0xA002, vss=0xB000), 1),
     (dict(kv_start=None, bt=0xC000, bts=4, page=512, rows=1024), 2),
+    (dict(out=0x1000), 1), (dict(out=0x5ff0), 1), (dict(q=0x7000 + 10 * 2048 - 16), 1),   # overlaps
 ])
 def test_prefill_refusals(c, over, status):
     assert _prefill(c, **over) == status
