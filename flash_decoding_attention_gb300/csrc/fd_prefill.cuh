@@ -80,13 +80,18 @@ constexpr int kRowsPair = 2 * kRowsTile;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
 constexpr int kPages = 20;          // block-table entries staged at a time (a tile has 16)
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
-// Cost of a segment start (Q load, first product, epilogue), in keys.  Four
-// bf16 prompts of 8192 tokens in all: 480 us at 320 and 480, 438 at 640, 495
-// at 800, 448 at 1000.  With a scale per token a tile takes longer, its start
-// does not: a mixed INT8 batch takes 264 us at 320, 269 at 480, 279 at 640.
+// What the split counts, in keys: a segment's start (Q load, first product,
+// epilogue) and a tile that only query tile A passes.  Four bf16 prompts of
+// 8192 tokens in all: 480 us with a start of 320 and 480, 438 with 640, 495
+// with 800, 448 with 1000.  Without a scale per token a solo tile costs as
+// much as a full one where it matters (8-bit: the widening bounds both; long
+// e4m3 contexts take 145 us with 128, 165 with 96).  With one, the softmax of a
+// full tile is the longer chain: a mixed INT8 batch takes 271 us with 320 and
+// 128, 257 with 320 and 104, 261 with 256 and 92, 255 with 448 and 92.
 template <bool TOK>
 struct Cost {
-  static constexpr int kStart = TOK ? 320 : 640;
+  static constexpr int kStart = TOK ? 448 : 640;
+  static constexpr int kSolo = TOK ? 92 : kTile;
 };
 
 // ---------------------------------------------------------------------------
@@ -94,6 +99,7 @@ struct Cost {
 // ---------------------------------------------------------------------------
 struct Seq {
   int b, q0, n, T, ctx, pairs, span;   // span: tokens of a pair
+  bool solo;                           // (TOK) the last pair has rows in A only
   long long head;                      // cost of one KV head
 };
 
@@ -107,6 +113,10 @@ __device__ __forceinline__ int pair_end(const Seq& s, int m) {
 template <bool TOK>
 __device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
   const long long end = pair_end(s, m);
+  if constexpr (TOK) {
+    if (s.solo && m == s.pairs - 1)
+      return Cost<TOK>::kStart + (end * Cost<TOK>::kSolo + kTile - 1) / kTile;
+  }
   return Cost<TOK>::kStart + end;
 }
 
@@ -137,6 +147,8 @@ __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   s.ctx = s.T - s.n;
   s.span = 2 * p.tile_tokens;
   s.pairs = (int)(((unsigned)s.n + (unsigned)s.span - 1u) / (unsigned)s.span);
+  if constexpr (TOK)
+    s.solo = s.n > 0 && s.n - (long long)(s.pairs - 1) * s.span <= p.tile_tokens;
   s.head = s.n > 0 ? pairs_before<TOK>(s, s.pairs - 1) + pair_cost<TOK>(s, s.pairs - 1) : 0;
   return s;
 }
@@ -250,8 +262,15 @@ struct Walk {
       // tile i stands at ps + the start + i times its cost and belongs to the
       // range that holds this point
       const long long xa = a - ps - Cost<TOK>::kStart, xe = e - ps - Cost<TOK>::kStart;
-      const int tb = xa <= 0 ? 0 : min(n, (int)((xa + kTile - 1) >> 7));
-      const int te = xe <= 0 ? 0 : min(n, (int)((xe + kTile - 1) >> 7));
+      auto tiles_at = [&](long long x) -> int {   // (a stream costs less than 2^32)
+        if constexpr (TOK) {
+          constexpr unsigned kSolo = Cost<TOK>::kSolo;
+          if (s.solo && m == s.pairs - 1) return (int)(((unsigned)x + kSolo - 1u) / kSolo);
+        }
+        return (int)((x + kTile - 1) >> 7);
+      };
+      const int tb = xa <= 0 ? 0 : min(n, tiles_at(xa));
+      const int te = xe <= 0 ? 0 : min(n, tiles_at(xe));
       const bool yields = n > 0 ? te > tb : g <= ps;
       if (yields) {
         o.b = s.b;
@@ -517,6 +536,23 @@ struct TileCopy {
   static constexpr int kBoxElems = KV == 0 ? 64 : D;
 };
 
+// Copies in flight must land before the CTA ends, which after a timeout the
+// other warps do not wait for.  By one lane.
+static __device__ __forceinline__ void land_copies(Control& c, const Prefill& p, uint64_t* full,
+                                                   int slots, int issued, int q0, int q1) {
+  bool late = false;
+  for (int e = max(0, issued - slots); e < issued; ++e)
+    late |= !mbar_wait(&full[e % slots], (uint32_t)((e / slots) & 1), mma::kDrainNs);
+  if (q0 > 0) late |= !mbar_wait(&c.q_full[0], (uint32_t)((q0 - 1) & 1), mma::kDrainNs);
+  if (q1 > 0) late |= !mbar_wait(&c.q_full[1], (uint32_t)((q1 - 1) & 1), mma::kDrainNs);
+  if (late) raise_error(p.at.ws, kErrDrain, 3);
+}
+
+static __device__ __noinline__ void land_copies_call(Control& c, const Prefill& p, uint64_t* full,
+                                                     int slots, int issued, int q0, int q1) {
+  land_copies(c, p, full, slots, issued, q0, q1);
+}
+
 template <int D, int KV, bool CONV, bool TOK>
 __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Control& c,
                                          uint8_t* base, const CUtensorMap* tmq,
@@ -641,16 +677,11 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
     }
     stop = __any_sync(0xffffffffu, stop);
   }
-  // copies in flight must land before the CTA ends, which after a timeout the
-  // other warps do not wait for
+  // (a call or not moves the registers of the whole kernel: four bf16 prompts
+  // 421 us with the call, 454 without; e4m3 chunks 147 with it, 140 without)
   if (lane == 0) {
-    bool late = false;
-    for (int e = max(0, issued - NS); e < issued; ++e)
-      late |= !mbar_wait(&full[e % NS], (uint32_t)((e / NS) & 1), mma::kDrainNs);
-    for (int x = 0; x < 2; ++x)
-      if (qn[x] > 0)
-        late |= !mbar_wait(&c.q_full[x], (uint32_t)((qn[x] - 1) & 1), mma::kDrainNs);
-    if (late) raise_error(p.at.ws, kErrDrain, 3);
+    if constexpr (CONV) land_copies(c, p, full, NS, issued, qn[0], qn[1]);
+    else land_copies_call(c, p, full, NS, issued, qn[0], qn[1]);
   }
   __syncwarp();
   if (!stop && KV == 0 && !CONV) {   // (with converters they write the end)
