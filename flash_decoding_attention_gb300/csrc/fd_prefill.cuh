@@ -29,8 +29,8 @@
 // cuBLAS burst rate and 0.93 of its sustained one: the tensor cores (and the
 // power limit).  Whole prompts, with a start and an end for every 33 tiles or
 // so, run at 1.33 PFLOP/s.  With 8-bit caches the widened copies compete with
-// the products for shared memory's port (e4m3 / f16 1.54 PFLOP/s).  Decode-like
-// batches (one token over 4096 keys, bf16) read the cache at 5.5 TB/s.
+// the products for shared memory's port (e4m3 / f16 1.51 PFLOP/s).  Decode-like
+// batches (one token over 4096 keys, bf16) read the cache at 5.6 TB/s.
 //
 // Roles (one persistent CTA per SM):
 //   warps 0-3, 4-7  softmax of query tile A, B: one row per thread, its scores

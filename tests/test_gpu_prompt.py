@@ -1,6 +1,7 @@
 """GPU tests of the prompt path (rotary table, packed append, read-back,
 attention of packed new tokens) against plain 64-bit statements."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -762,6 +763,55 @@ def test_prompt_path_on_other_streams():
         bt, f, q = cases[i][:3]
         want, wlse = ref.attention_blocks(f, q, 8, 128 ** -0.5)
         _compare(f, out.double().cpu(), lse.double().cpu(), want, wlse, "bf16")
+
+
+def test_prompt_path_from_several_threads():
+    """Three host threads at once, each with its own stream, workspace, format
+    and shape (descriptors, kernel variants and limits set for the first time
+    by whoever comes first)."""
+    fda = lib()
+    jobs = []
+    for i, (kv, x16, d, page, scales) in enumerate([("e4m3", "f16", 128, 64, "tensor"),
+                                                    ("bf16", "bf16", 64, 0, "tensor"),
+                                                    ("i8", "f16", 128, 16, "token")]):
+        bt = ref.Batch([90 + 40 * i, 1, 17], [600, 33, 0], 2, d, kv, page, seed=70 + i)
+        f = ref.Filled(bt, seed=70 + i, scales=scales)
+        q = _queries(bt, 8, x16, 70 + i)
+        kw = f.device(DEV)
+        args = (q.to(DEV), kw.pop("k_cache"), kw.pop("v_cache"),
+                torch.from_numpy(bt.q_start).to(DEV),
+                torch.tensor(bt.seq, dtype=torch.int32, device=DEV))
+        jobs.append((f, q, x16, args, {**kw, **bt.index(DEV)}, fda.alloc_prefill_workspace(d),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    res, wrong = [None] * len(jobs), []
+    gate = threading.Barrier(len(jobs))
+
+    def work(i):
+        try:
+            f, q, x16, args, kw, ws, st = jobs[i]
+            gate.wait()
+            for _ in range(25):
+                table = fda.rotary_table(300 + i, 32, stream=st)
+                res[i] = (*fda.prefill_attention(*args, workspace=ws, stream=st, **kw), table)
+            st.synchronize()
+        except Exception as e:      # noqa: BLE001 (shown by the assertion below)
+            wrong.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    torch.cuda.synchronize()
+    for i, (f, q, x16, _, _, ws, _) in enumerate(jobs):
+        _ok(fda, ws)
+        out, lse, table = res[i]
+        want, wlse = ref.attention_blocks(f, q, 8, f.batch.d ** -0.5)
+        _compare(f, out.double().cpu(), lse.double().cpu(), want, wlse, x16)
+        ang = ref.table(300 + i, 32, 10000.0)
+        assert np.abs(table.double().cpu().numpy() - ang).max() <= 5 * 2.0 ** -24 + 300 * 2.0 ** -52
 
 
 def test_prompt_path_far_into_a_large_cache():
