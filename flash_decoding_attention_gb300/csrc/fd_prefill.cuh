@@ -27,8 +27,8 @@
 // What bounds it, on GB300 (152 SMs), bf16, 32 query / 8 KV heads, D = 128:
 // 2048 new tokens over 30000 cached ones run at 1.60 PFLOP/s, 0.83 of the
 // cuBLAS burst rate and 0.93 of its sustained one: the tensor cores (and the
-// power limit).  Whole prompts, with a start and an end for every 33 tiles or
-// so, run at 1.33 PFLOP/s.  With 8-bit caches the widened copies compete with
+// power limit).  Whole prompts, with a start and an end for every 26 tiles or
+// so, run at 1.38 PFLOP/s.  With 8-bit caches the widened copies compete with
 // the products for shared memory's port (e4m3 / f16 1.51 PFLOP/s).  Decode-like
 // batches (one token over 4096 keys, bf16) read the cache at 5.6 TB/s.
 //
