@@ -57,7 +57,10 @@
 // size of the output's own rounding), and the output.  With f16, P is scaled
 // by 2^6 so that small probabilities stay above f16's subnormals; the
 // running maximum is moved only when exceeded by 2^8 (O is then rescaled in
-// tensor memory), which keeps P below 2^14.
+// tensor memory), which keeps P below 2^14.  With a scale per token as well,
+// P times the V scale is what is rounded, divided by the power of two of the
+// largest scale that the row itself has seen: taken over the whole tile, a
+// later token's scale would push an earlier row's P out of f16's range.
 #pragma once
 
 #include "fd_prompt.cuh"
@@ -1252,7 +1255,8 @@ struct Softmax {
   uint32_t tS, tO;
   // the row's state in the segment
   float m_ref, l, sc;
-  int vexp;   // TOK with f16: P's factor carries 2^-vexp against the V scales
+  int vexp;   // TOK with f16: P's factor carries 2^-vexp against the V scales that
+              // the row has seen in the segment
 
   // P and l carry a factor 2^lift()
   __device__ __forceinline__ float lift() const { return TOK && !BF16 ? kLift - vexp : kLift; }
@@ -1322,6 +1326,31 @@ struct Softmax {
     tmem_st16u(tS + 16 * k, pk);
   }
 
+  // Largest |V scale| among a tile's first `left` keys, per lane: prefix maxima
+  // over four keys a lane, of which each row takes its own.
+  static __device__ __forceinline__ float seen_scale(const float* vs, int left) {
+    const int lane = threadIdx.x & 31;
+    float4 v = reinterpret_cast<const float4*>(vs)[lane];
+    v.x = fabsf(v.x);
+    v.y = fmaxf(v.x, fabsf(v.y));
+    v.z = fmaxf(v.y, fabsf(v.z));
+    v.w = fmaxf(v.z, fabsf(v.w));
+    float before = v.w;   // of this lane's keys and all earlier ones
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before = fmaxf(before, y);
+    }
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    if (lane == 0) before = 0.f;
+    const int last = max(left - 1, 0), src = last >> 2;
+    const float b = __shfl_sync(0xffffffffu, before, src);
+    const float x = __shfl_sync(0xffffffffu, v.x, src), y = __shfl_sync(0xffffffffu, v.y, src);
+    const float z = __shfl_sync(0xffffffffu, v.z, src), w = __shfl_sync(0xffffffffu, v.w, src);
+    const int i = last & 3;
+    return left > 0 ? fmaxf(b, i == 0 ? x : i == 1 ? y : i == 2 ? z : w) : 0.f;
+  }
+
   // P is in tensor memory up to here: one of this warp's two arrivals a tile.
   __device__ __forceinline__ void publish(uint64_t* bar) const {
     tmem_wait_st();
@@ -1333,7 +1362,7 @@ struct Softmax {
   // One tile (tile jn of the CTA), of whose 128 keys the row sees the first
   // `left`.  False after a timeout.  The scores are read from tensor memory
   // twice, 32 at a time: a thread that kept all 128 would spill.
-  __device__ __forceinline__ bool tile(int jn, int left, bool fresh, bool mine) {
+  __device__ __forceinline__ bool tile(int jn, int left, bool mine) {
     const bool whole = __all_sync(0xffffffffu, left == kTile);
     const float* ks = scales + SR::key(jn);   // written before the tile's S was issued
     const float* vs = scales + SR::val(jn);
@@ -1375,8 +1404,9 @@ struct Softmax {
     const float mt = smax == -INFINITY ? -INFINITY : smax * scl;
     float fac = 1.f;
     bool resc = false;
-    if (mt > m_ref + 8.f || m_ref == -INFINITY) {
-      if (m_ref != -INFINITY) {
+    const bool fresh = m_ref == -INFINITY;   // nothing has reached the row's O yet
+    if (mt > m_ref + 8.f || fresh) {
+      if (!fresh) {
         fac = exp2f(m_ref - mt);
         l *= fac;
         resc = mine;
@@ -1387,13 +1417,17 @@ struct Softmax {
       if (!wait_warp(c, p, &c.fixed[jn % SR::kValRing], (uint32_t)((jn / SR::kValRing) & 1), 12))
         return false;
       if constexpr (!BF16) {
-        // largest V scale of the tile -> its exponent, which P's factor takes
-        // back, so that P times a V scale stays below 2^15
+        // largest V scale that the row sees in the tile -> its exponent, which
+        // P's factor takes back, so that P times a V scale stays below 2^15
         float vm = 0.f;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vs[lane + 32 * i]));
+          for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vs[lane + 32 * i]));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        } else {
+          vm = seen_scale(vs, left);
+        }
         int ev = (int)((__float_as_uint(vm) >> 23) & 255u) - 127;
         ev = max(-60, min(60, ev));
         if (fresh) {
@@ -1485,7 +1519,7 @@ struct Softmax {
         tc_fence_after();
         if (warp_live) {
           const bool bad = (*(volatile int*)&c.info[jn & 7] & kInfoBad) != 0;
-          if (!tile(jn, bad ? 0 : max(0, min(kTile, lim - j * kTile)), j == first, mine)) {
+          if (!tile(jn, bad ? 0 : max(0, min(kTile, lim - j * kTile)), mine)) {
             dead = true;
             break;
           }

@@ -1,0 +1,85 @@
+"""GPU tests of the prompt path at its edges: finite and non-finite scales and
+values in places a row may not see, absent tiles, empty calls, wrong starts,
+refusals that leave the caches alone, waits that run out in the middle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import prompt_ref as ref
+from gpu_util import lib
+from test_gpu_prompt import DEV, _attend, _compare, _ok, _queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("x16", ["f16", "bf16"])
+@pytest.mark.parametrize("kv,page,d", [("i8", 16, 64), ("e4m3", 0, 128), ("i8", 2, 128)])
+def test_attention_scales_of_unseen_keys_have_no_effect(kv, page, d, x16):
+    """However large the K and V scales of a token are, the tokens before it get
+    the same bits; and each row is right against the keys that it sees."""
+    fda = lib()
+    bt = ref.Batch([100, 40, 200, 1], [0, 300, 70, 500], 2, d, kv, page, seed=31)
+    f = ref.Filled(bt, "token", seed=31)
+    q = _queries(bt, 8, x16, 31)
+    ws = fda.alloc_prefill_workspace(d)
+    base, lbase = _attend(fda, f, q, 8, ws)
+    late = {b: int(bt.seq[b] - min(17, bt.new[b])) for b in range(len(bt.new))}   # first large one
+    for big in (2.0 ** 20, 1e12, 3e38):
+        for b, T in enumerate(bt.seq):
+            rows = bt.rows_of(b, late[b], T)
+            f.kw["v_scales"][rows] = big
+            f.kw["k_scales"][rows] = big
+        out, lse = _attend(fda, f, q, 8, ws)
+        _ok(fda, ws)
+        for b, n in enumerate(bt.new):
+            i = int(bt.q_start[b])
+            m = n - (bt.seq[b] - late[b])     # rows that see none of them
+            assert torch.equal(out[i:i + m], base[i:i + m]), (big, b)
+            assert torch.equal(lse[i:i + m], lbase[i:i + m]), (big, b)
+
+
+def test_attention_value_scales_row_by_row():
+    """V scales that grow along the sequence, f16 queries: each row against the
+    largest value that it sees itself."""
+    fda = lib()
+    bt = ref.Batch([128, 300, 7], [0, 100, 600], 2, 64, "i8", 16, seed=32)
+    f = ref.Filled(bt, "token", seed=32)
+    old = f.kw["v_scales"].clone()
+    for b, T in enumerate(bt.seq):
+        rows = bt.rows_of(b, 0, T)
+        grow = 2.0 ** (torch.arange(T, dtype=torch.float64) * (28.0 / T) - 16)
+        f.kw["v_scales"][rows] = (old[rows].double() * grow[:, None]).float()
+    ratio = f.kw["v_scales"].double() / old.double()
+    f.val["v"] = f.val["v"] * ratio[:, :, None]
+    q = _queries(bt, 4, "f16", 32)
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 4, ws)
+    _ok(fda, ws)
+    want, wlse = ref.attention_blocks(f, q, 4, 0.125)
+    assert float((lse - wlse).abs().max()) <= 1e-4
+    # sum p |v| of every row, and the largest |v| that it sees
+    mag = ref.Filled(bt, "token", seed=32)
+    mag.val["v"] = f.val["v"].abs()
+    weight, _ = ref.attention_blocks(mag, q, 4, 0.125)
+    top = torch.zeros(want.shape[:2], dtype=torch.float64)
+    seen = torch.zeros(want.shape[0], dtype=torch.float64)
+    for b, n in enumerate(bt.new):
+        for j in range(n):
+            i, t = int(bt.q_start[b]) + j, bt.seq[b] - n + j + 1
+            seen[i] = t
+            if j == 0:
+                run = f.val["v"][bt.rows_of(b, 0, t)].abs().amax(dim=(0, 2))
+            else:
+                run = torch.maximum(run, f.val["v"][bt.row(b, t - 1)].abs().amax(-1))
+            top[i] = run.repeat_interleave(2)
+    # P times a V scale is rounded to f16: half a step, 2^-11 of itself, or
+    # below f16's normal range 2^-25, with P lifted by 2^6 against the largest
+    # scale seen: 2^-31 of that scale times the key's code, which is below eight
+    # times the largest code of the key with that scale: 2^-28 of the largest
+    # |v| for every key.  The output is rounded once more (2^-11, or half of its
+    # own subnormal step); fp32 sums and ex2 2^-18.
+    tol = ((2.0 ** -11 + 2.0 ** -18) * weight + (seen[:, None] * 2.0 ** -28 * top)[..., None] +
+           2.0 ** -11 * want.abs() + 2.0 ** -25)
+    assert torch.all((out - want).abs() <= tol), float(((out - want).abs() / tol).max())
