@@ -136,15 +136,18 @@ fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, cons
       kv_rows, batch, num_kv_heads, head_dim, page_size, scale_kind, k_scales, v_scales, new_dtype,
       kv_dtype, workspace);
   if (chk != FD_OK) return chk;
-  if (!k_new || !v_new || !positions || !aligned(positions, 4)) return FD_ERR_INVALID_ARG;
+  if (!positions || !aligned(positions, 4)) return FD_ERR_INVALID_ARG;
+  // (packed arrays without rows may have no address)
+  if (num_tokens > 0 && (!k_new || !v_new)) return FD_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !stride_ok(kv_stride, num_kv_heads, head_dim))
     return FD_ERR_INVALID_ARG;
   if (q) {
-    if (!q_out || num_q_heads <= 0 || num_q_heads > 4096) return FD_ERR_INVALID_ARG;
+    if ((!q_out && num_tokens > 0) || num_q_heads <= 0 || num_q_heads > 4096)
+      return FD_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(q_out, 16) || !stride_ok(q_stride, num_q_heads, head_dim))
       return FD_ERR_INVALID_ARG;
     // in place only where a token's rows are its own
-    if (q == q_out && q_stride != (int64_t)num_q_heads * head_dim) return FD_ERR_INVALID_ARG;
+    if (q == q_out && num_tokens > 0 && q_stride != (int64_t)num_q_heads * head_dim) return FD_ERR_INVALID_ARG;
   }
   if (rotary) {
     if (!aligned(rotary, 16) || rotary_positions <= 0) return FD_ERR_INVALID_ARG;
@@ -204,7 +207,8 @@ fd_status fd_read_kv(const void* k_cache, const void* v_cache, const int32_t* kv
       kv_rows, batch, num_kv_heads, head_dim, page_size, scale_kind, k_scales, v_scales, out_dtype,
       kv_dtype, workspace);
   if (chk != FD_OK) return chk;
-  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+  if (num_rows > 0 && (!k_out || !v_out)) return FD_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) ||
       (first && !aligned(first, 4)))
     return FD_ERR_INVALID_ARG;
   if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return FD_ERR_INVALID_ARG;
@@ -260,7 +264,7 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
       kv_rows, batch, num_kv_heads, head_dim, page_size, scale_kind, k_scales, v_scales, q_dtype,
       kv_dtype, workspace);
   if (chk != FD_OK) return chk;
-  if (!q || !out || !seq_len) return FD_ERR_INVALID_ARG;
+  if (!seq_len || (num_tokens > 0 && (!q || !out))) return FD_ERR_INVALID_ARG;
   if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return FD_ERR_INVALID_ARG;
   if (num_q_heads / num_kv_heads > 128 || num_q_heads > 4096) return FD_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seq_len, 4) || (lse && !aligned(lse, 4)) ||

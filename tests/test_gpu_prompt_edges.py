@@ -83,3 +83,28 @@ def test_attention_value_scales_row_by_row():
     tol = ((2.0 ** -11 + 2.0 ** -18) * weight + (seen[:, None] * 2.0 ** -28 * top)[..., None] +
            2.0 ** -11 * want.abs() + 2.0 ** -25)
     assert torch.all((out - want).abs() <= tol), float(((out - want).abs() / tol).max())
+
+
+def test_calls_of_nothing():
+    """No packed tokens, no rows: empty results, nothing written."""
+    fda = lib()
+    k = torch.full((8, 2, 64), 3.0, dtype=torch.float16, device=DEV)
+    v = k.clone()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    start, zero = torch.zeros(3, **i32), torch.zeros(2, **i32)
+    for base in (torch.empty((0, 4, 64), dtype=torch.float16, device=DEV),
+                 torch.ones((9, 4, 64), dtype=torch.float16, device=DEV)[4:4]):
+        new = base[:, :2]
+        q = fda.append_kv(new, new, k, v, start, zero, q=base, kv_start_idx=zero)
+        assert tuple(q.shape) == (0, 4, 64)
+        assert fda.append_kv(new, new, k, v, start, zero, kv_start_idx=zero) is None
+        out, lse = fda.prefill_attention(base, k, v, start, zero, kv_start_idx=zero)
+        assert tuple(out.shape) == (0, 4, 64) and tuple(lse.shape) == (0, 4)
+        out, lse = fda.prefill_attention(base, k, v, start, zero, kv_start_idx=zero, k_new=new,
+                                         v_new=new, positions=zero,
+                                         rotary=fda.rotary_table(4, 64))
+        assert tuple(out.shape) == (0, 4, 64) and tuple(lse.shape) == (0, 4)
+    ko, vo = fda.read_kv(k, v, start, 0, kv_start_idx=zero)
+    assert tuple(ko.shape) == tuple(vo.shape) == (0, 2, 64)
+    torch.cuda.synchronize()
+    assert bool((k == 3).all()) and bool((v == 3).all())
