@@ -101,10 +101,7 @@ __device__ __forceinline__ TokenAt place_token(const AppendPacked& p, int i) {
   const int b = owner_of(p.q_start, p.at.batch, i);
   if (b < 0) return t;
   const int lo = __ldg(p.q_start + b), hi = __ldg(p.q_start + b + 1);
-  if (lo < 0 || hi > p.tokens) {
-    raise_error(p.at.ws, kErrBounds, lo < 0 ? lo : hi);
-    return t;
-  }
+  if (lo < 0 || hi > p.tokens) return t;   // (recorded by check_starts)
   const int first = __ldg(p.positions + b);
   if (first < 0) return t;
   const long long pos = (long long)first + (i - lo);
@@ -129,6 +126,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) append_packed_kernel(const __g
   const int t0 = blockIdx.x * per_block;
   const int n = min(per_block, p.tokens - t0);
   if (threadIdx.x < n) at[threadIdx.x] = place_token(p, t0 + threadIdx.x);
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_starts(p.at, p.q_start, p.tokens);
   __syncthreads();
   const int u = threadIdx.x % TPH, h0 = threadIdx.x / TPH;
   const int half = p.rot_dim / 2;

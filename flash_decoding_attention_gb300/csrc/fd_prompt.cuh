@@ -56,6 +56,16 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int batch, int i) 
   return i < __ldg(start + lo + 1) ? lo : -1;
 }
 
+// Records the sequences whose starts descend or lie outside the `rows` packed
+// rows, by the threads of one block.  (The search of a token's owner never
+// meets a sequence that owns no token.)
+__device__ __forceinline__ void check_starts(const Placement& pl, const int32_t* start, int rows) {
+  for (int b = threadIdx.x; b < pl.batch; b += blockDim.x) {
+    const int lo = __ldg(start + b), hi = __ldg(start + b + 1);
+    if (lo < 0 || hi < lo || hi > rows) raise_error(pl.ws, kErrBounds, lo < 0 ? lo : hi);
+  }
+}
+
 struct AppendPacked {
   Placement at;
   const void *q, *k_new, *v_new;

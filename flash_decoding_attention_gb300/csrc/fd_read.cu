@@ -104,9 +104,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const __grid_constant
     if (b >= 0) {
       const int lo = __ldg(p.out_start + b), hi = __ldg(p.out_start + b + 1);
       const int f = p.first ? __ldg(p.first + b) : 0;
-      if (lo < 0 || hi > p.rows) {
-        raise_error(p.at.ws, kErrBounds, lo < 0 ? lo : hi);
-      } else if (f >= 0) {
+      if (lo >= 0 && hi <= p.rows && f >= 0) {   // (else recorded by check_starts)
         const long long t = (long long)f + (i - lo);
         if (t > 0x7fffffffll) {
           raise_error(p.at.ws, kErrBounds, t);
@@ -118,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const __grid_constant
     }
     src_row[threadIdx.x] = row;
   }
+  if (blockIdx.x == 0) check_starts(p.at, p.out_start, p.rows);
   __syncthreads();
   const int per_row = p.num_kv_heads * TPH;   // threads of a row
   // narrow rows: several at a time; wide ones: several passes over each

@@ -342,8 +342,10 @@ fd_status fd_decode_attention_noalloc(const void *q, const void *k_cache, const 
  * q_start[batch]) belong to no sequence: nothing is read for them and their
  * rows of every output are left as they were.  A sequence whose entries
  * descend or lie outside the packed arrays is skipped and recorded as
- * FD_ERR_DEVICE_BOUNDS (info: the offending entry).  A call of no packed rows
- * has nothing to do; its packed arrays may then be NULL.
+ * FD_ERR_DEVICE_BOUNDS (info: the offending entry); where entries descend,
+ * tokens outside that range, or claimed by two of the other sequences, are
+ * served for one of them or not at all.  A call of no packed rows has nothing
+ * to do; its packed arrays may then be NULL.
  *
  * Caches, block tables, scales, dtypes, workspaces, streams and errors are
  * those of the decode entry points above, and so are the addressing rules:

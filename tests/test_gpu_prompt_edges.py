@@ -108,3 +108,39 @@ def test_calls_of_nothing():
     assert tuple(ko.shape) == tuple(vo.shape) == (0, 2, 64)
     torch.cuda.synchronize()
     assert bool((k == 3).all()) and bool((v == 3).all())
+
+
+@pytest.mark.parametrize("starts,served", [
+    ([0, -5, 50], []), ([0, 60, 50], []), ([30, 20, 50], [1]), ([0, 50, 60], [0]),
+    ([0, 20, 70], [0]), ([0, 20, 20, 10, 50], [0])])
+def test_wrong_starts_are_recorded(starts, served):
+    """Starts that descend or lie outside the packed arrays: recorded by every
+    packed call; rows behind the last start and before the first stay."""
+    fda = lib()
+    n, d, B = 50, 64, len(starts) - 1
+    i32 = dict(dtype=torch.int32, device=DEV)
+    qs = torch.tensor(starts, **i32)
+    first = torch.arange(B, **i32) * 100
+    pos = torch.zeros(B, **i32)
+    new = torch.ones((n, 1, d), dtype=torch.float16, device=DEV)
+    kc, vc = (torch.zeros((100 * B, 1, d), dtype=torch.float16, device=DEV) for _ in range(2))
+    q_out = torch.zeros((n, 2, d), dtype=torch.float16, device=DEV)
+    ws = fda.alloc_prefill_workspace(d)
+    fda.append_kv(new, new, kc, vc, qs, pos, q=new.expand(n, 2, d).contiguous(), q_out=q_out,
+                  kv_start_idx=first, workspace=ws)
+    st, info = fda.fd_check_device_error(ws)
+    assert st == fda.FD_ERR_DEVICE_BOUNDS and info in starts
+    rows = kc[:, 0, 0].view(B, 100).sum(1).tolist()
+    for b in served:
+        lo = max(starts[b], starts[0])
+        assert rows[b] == starts[b + 1] - lo, rows
+    assert bool((q_out[starts[-1]:] == 0).all()) and bool((q_out[:starts[0]] == 0).all())
+    ko, vo = (torch.full((n, 1, d), 9.0, dtype=torch.float16, device=DEV) for _ in range(2))
+    fda.read_kv(kc, vc, qs, n, kv_start_idx=first, k_out=ko, v_out=vo, workspace=ws)
+    st, info = fda.fd_check_device_error(ws)
+    assert st == fda.FD_ERR_DEVICE_BOUNDS and info in starts
+    assert bool((ko[starts[-1]:] == 9).all()) and bool((ko[:starts[0]] == 9).all())
+    fda.prefill_attention(torch.ones((n, 2, d), dtype=torch.float16, device=DEV), kc, vc, qs,
+                          torch.full((B,), 40, **i32), kv_start_idx=first, workspace=ws)
+    st, info = fda.fd_check_device_error(ws)
+    assert st == fda.FD_ERR_DEVICE_BOUNDS and info in starts
