@@ -71,6 +71,15 @@ bool stride_ok(int64_t stride, int heads, int head_dim) {
   return stride >= (int64_t)heads * head_dim && stride % 8 == 0 && stride < (int64_t(1) << 32);
 }
 
+// Do `tokens` dense rows of `width` bytes at `a` and rows of `b_width` bytes,
+// `b_stride` apart, at `b` share an address range?
+bool overlap(const void* a, int64_t width, const void* b, int64_t b_width, int64_t b_stride,
+             int64_t tokens) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return tokens > 0 && a0 < b0 + (uintptr_t)((tokens - 1) * b_stride + b_width) &&
+         b0 < a0 + (uintptr_t)(tokens * width);
+}
+
 }  // namespace
 }  // namespace fd
 
@@ -157,6 +166,14 @@ fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, cons
   if (kv_elem_bytes(kv_dtype) == 1 && !(k_scale > 0.f && v_scale > 0.f)) return FD_ERR_INVALID_ARG;
   if (workspace_bytes < sizeof(WsHeader)) return FD_ERR_WORKSPACE_TOO_SMALL;
   if (num_tokens == 0) return FD_OK;
+  if (q) {   // written by blocks while others read (in place: their own rows)
+    const int64_t width = (int64_t)num_q_heads * head_dim * 2;
+    const int64_t kv_width = (int64_t)num_kv_heads * head_dim * 2;
+    if ((q != q_out && overlap(q_out, width, q, width, 2 * q_stride, num_tokens)) ||
+        overlap(q_out, width, k_new, kv_width, 2 * kv_stride, num_tokens) ||
+        overlap(q_out, width, v_new, kv_width, 2 * kv_stride, num_tokens))
+      return FD_ERR_INVALID_ARG;
+  }
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
 
@@ -273,11 +290,8 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
   if (!std::isfinite(softmax_scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return FD_ERR_INVALID_ARG;
   if (kv_rows >= kMaxPacked) return FD_ERR_UNSUPPORTED;   // 32-bit TMA coordinates
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
-  const uintptr_t width = (uintptr_t)num_q_heads * head_dim * 2;
-  if (num_tokens > 0 && q0 < o0 + (uintptr_t)num_tokens * width &&
-      o0 < q0 + (uintptr_t)(num_tokens - 1) * q_stride * 2 + width)
-    return FD_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)num_q_heads * head_dim * 2;
+  if (overlap(out, width, q, width, 2 * q_stride, num_tokens)) return FD_ERR_INVALID_ARG;
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
   if (workspace_bytes < prefill_layout(head_dim, sms).total) return FD_ERR_WORKSPACE_TOO_SMALL;

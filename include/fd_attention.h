@@ -401,7 +401,8 @@ fd_status fd_rotary_table(float *table, int64_t positions, int rot_dim, double t
  * q          [num_tokens, num_q_heads, head_dim] of new_dtype, tokens
  *            q_stride elements apart, or NULL (only k and v are written).
  * q_out      dense [num_tokens, num_q_heads, head_dim]; may equal q when q is
- *            dense.  Required with q.
+ *            dense, and must not overlap q (otherwise), k_new or v_new.
+ *            Required with q.
  * k_new, v_new  [num_tokens, num_kv_heads, head_dim] of new_dtype, tokens
  *            kv_stride elements apart.
  * q_stride, kv_stride  multiples of 8 elements, at least one token's heads

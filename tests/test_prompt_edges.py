@@ -22,3 +22,16 @@ def test_packed_arrays_without_rows_may_be_null(c):  # noqa: F811
     assert _read(c, n=0, ko=None, vo=None, os=None) == fda.FD_ERR_INVALID_ARG
     assert _prefill(c, n=0, q=None, out=None, sl=None) == fda.FD_ERR_INVALID_ARG
     assert _prefill(c, n=0, q=None, out=None, qh=7) == fda.FD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    dict(qo=0x100000 + 2048), dict(qo=0x100000 - 16),               # q, not in place
+    dict(qst=9 * 128, qo=0x100000 + 9 * 9 * 256),                   # the last of strided tokens
+    dict(qo=0x200000), dict(qo=0x200000 + 9 * 512 + 256), dict(qo=0x200000 - 10 * 2048 + 16),
+    dict(qo=0x300000 + 512),
+])
+def test_turned_queries_may_not_overlap_what_is_read(c, over):  # noqa: F811
+    """q_out is written by blocks while others still read q, k_new and v_new."""
+    a = dict(q=0x100000, kn=0x200000, vn=0x300000, qo=0x400000)
+    a.update(over)
+    assert _append(c, **a) == fda.FD_ERR_INVALID_ARG
