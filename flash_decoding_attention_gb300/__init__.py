@@ -744,10 +744,12 @@ def rotary_table(positions: int, rot_dim: int, *, theta: float = 10000.0, scalin
         raise ValueError(f"out must be dense fp32 [{positions}, {rot_dim}]")
     if out is not None:
         device = out.device
-    elif device is None or torch.device(device).index is None:
+    elif device is None or torch.device(device) == torch.device("cuda"):
         device = torch.device("cuda", torch.cuda.current_device())
     else:
         device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"the table is made on a GPU, not on {device}")
     with _on(device, stream):
         if out is None:
             out = torch.empty((positions, rot_dim), dtype=torch.float32, device=device)

@@ -35,3 +35,14 @@ def test_turned_queries_may_not_overlap_what_is_read(c, over):  # noqa: F811
     a = dict(q=0x100000, kn=0x200000, vn=0x300000, qo=0x400000)
     a.update(over)
     assert _append(c, **a) == fda.FD_ERR_INVALID_ARG
+
+
+def test_rotary_table_is_made_on_a_gpu():
+    with pytest.raises(ValueError, match="GPU"):
+        fda.rotary_table(10, 16, out=torch.empty((10, 16)))
+    with pytest.raises(ValueError, match="GPU"):
+        fda.rotary_table(10, 16, out=torch.empty((10, 16)), stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        fda.rotary_table(10, 16, device="cpu")
+    with pytest.raises(ValueError, match="GPU"):
+        fda.rotary_table(10, 16, device="cpu", stream=0)
