@@ -708,6 +708,15 @@ def _index(name: str, t: torch.Tensor, n: int, at: int, dims: int = 1) -> None:
         raise ValueError(f"{name} is on {t.device}, the caches on cuda:{at}")
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors' address ranges meet (strides >= 0)."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1
+        return t.data_ptr(), t.data_ptr() + (last * t.element_size() if t.numel() else 0)
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 def _layout_index(kv_start_idx, block_table, batch: int, at: int) -> None:
     if block_table is not None:
         _index("block_table", block_table, batch, at, 2)
@@ -878,8 +887,12 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     tokens, causal) over a contiguous or paged cache; returns (out, lse).
     With ``k_new`` / ``v_new`` [tokens, KVH, D] and ``positions`` the new tokens
     are first written into the caches by ``append_kv`` (queries and keys turned
-    by ``rotary`` if given); ``seq_len`` counts them.  Without ``k_new`` the
-    caches hold them already and ``q`` is taken as it is."""
+    by ``rotary`` if given); ``seq_len`` counts them.  Arguments are checked
+    before anything is written.  With ``rotary``, tokens that ``append_kv``
+    leaves alone have no turned query: their rows of ``out`` and ``lse`` are
+    undefined (zero and -inf where ``seq_len`` gives them no key).  Without
+    ``k_new`` the caches hold the new tokens already and ``q`` is taken as it
+    is."""
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
     dev, at = k_cache.device, k_cache.get_device()
     shape = q.shape
@@ -897,6 +910,8 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         raise ValueError("give k_new, v_new and positions, or none of them")
     if rotary is not None and k_new is None:
         raise ValueError("rotary turns queries together with new keys: give k_new")
+    if k_new is not None and k_new.shape[0] != n:
+        raise ValueError(f"k_new must have q's {n} tokens, got {k_new.shape[0]}")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if out is not None and (out.shape != q.shape or out.dtype != q.dtype or
@@ -913,6 +928,13 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         if workspace is None:
             workspace = alloc_prefill_workspace(D, dev)
         if k_new is not None:
+            # a call that the attention refuses leaves the caches as they were:
+            # its checks (of no tokens) come before the append
+            if rotary is None and _overlap(out, q):
+                raise ValueError("out must not overlap q")
+            fd_prefill_attention(q, qs, k_cache, v_cache, kv_start_idx, block_table, q_start,
+                                 seq_len, 0, kv_rows, QH, KVH, D, P, softmax_scale, k_scale,
+                                 v_scale, kind, k_scales, v_scales, out, lse, workspace)
             turned = append_kv(k_new, v_new, k_cache, v_cache, q_start, positions,
                                q=q if rotary is not None else None, rotary=rotary,
                                interleaved=interleaved, kv_start_idx=kv_start_idx,

@@ -144,3 +144,34 @@ def test_wrong_starts_are_recorded(starts, served):
                           torch.full((B,), 40, **i32), kv_start_idx=first, workspace=ws)
     st, info = fda.fd_check_device_error(ws)
     assert st == fda.FD_ERR_DEVICE_BOUNDS and info in starts
+
+
+def test_refused_prompt_calls_write_nothing():
+    """prefill_attention with new keys: every refusal comes before the caches
+    are written."""
+    fda = lib()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    kc, vc = (torch.zeros((40, 2, 64), dtype=torch.float16, device=DEV) for _ in range(2))
+    q = torch.ones((6, 4, 64), dtype=torch.float16, device=DEV)
+    new = torch.ones((6, 2, 64), dtype=torch.float16, device=DEV)
+    at = dict(kv_start_idx=torch.zeros(1, **i32), positions=torch.zeros(1, **i32))
+    starts, lens = torch.tensor([0, 6], **i32), torch.tensor([6], **i32)
+
+    def call(q=q, k_new=new, v_new=new, **kw):
+        return fda.prefill_attention(q, kc, vc, starts, lens, k_new=k_new, v_new=v_new, **at, **kw)
+
+    for error, kw in (
+            (ValueError, dict(k_new=new[:5], v_new=new[:5])),       # fewer keys than queries
+            (ValueError, dict(k_new=new[:5], v_new=new[:5], rotary=fda.rotary_table(8, 64))),
+            (fda.FdError, dict(workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))),
+            (fda.FdError, dict(softmax_scale=float("nan"))),
+            ((ValueError, fda.FdError), dict(out=q))):               # read by other blocks
+        with pytest.raises(error):
+            call(**kw)
+    torch.cuda.synchronize()
+    assert int(kc.count_nonzero()) == 0 and int(vc.count_nonzero()) == 0
+    # with a table the queries are turned into a tensor of the call's own
+    mine = q.clone()
+    out, lse = call(q=mine, out=mine, rotary=fda.rotary_table(8, 64))
+    again, lagain = call(rotary=fda.rotary_table(8, 64))
+    assert out is mine and torch.equal(out, again) and torch.equal(lse, lagain)
