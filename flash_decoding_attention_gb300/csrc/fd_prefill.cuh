@@ -1113,6 +1113,15 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
   if (lane == 0) mbar_arrive(&c.full[slot]);
 }
 
+// Does tile j of the segment's stream hold a row outside the cache?  By one
+// thread; off every fast path.
+static __device__ __noinline__ bool tile_absent(const Prefill& p, const Seg& seg, int j) {
+  const int end = min(seg.end - j * kTile, kTile);
+  for (int k = 0; k < end; ++k)
+    if (placed_row(p.at, seg.b, j * kTile + k) < 0) return true;
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // Per-token scales: warps 10 and 11, keys t and t + 64 of the tile per thread
 // ---------------------------------------------------------------------------
@@ -1171,9 +1180,13 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
         k[i] = ks[i] * p.score_scale;
         v[i] = vs[i];
         // the V scale of a key that some row does not see: as V's elements
-        if (!isfinite(v[i]) && j * kTile + t + 64 * i >= unseen) {
-          v[i] = 0.f;
-          *(volatile int*)&c.nf[sn & 7] = sn + 1;
+        if (!isfinite(v[i])) {
+          if (j * kTile + t + 64 * i >= unseen) {
+            v[i] = 0.f;
+            *(volatile int*)&c.nf[sn & 7] = sn + 1;
+          } else if (tile_absent(p, seg, j)) {   // (its P is zero: 0 * NaN would be seen)
+            v[i] = 0.f;
+          }
         }
       }
       load(j + 1);

@@ -85,6 +85,44 @@ def test_attention_value_scales_row_by_row():
     assert torch.all((out - want).abs() <= tol), float(((out - want).abs() / tol).max())
 
 
+def _absent_statement(f, q, qh, b, tile, scale):
+    """Sequence b without the keys of one 128-key tile: [new, qh, d] in 64 bits."""
+    bt = f.batch
+    n, T, g = bt.new[b], bt.seq[b], qh // bt.kvh
+    keys = torch.tensor([t for t in range(T) if t // 128 != tile])
+    rows = torch.tensor([bt.row(b, int(t)) for t in keys])
+    out = torch.zeros((n, qh, bt.d), dtype=torch.float64)
+    for j in range(n):
+        see = keys <= T - n + j
+        if not bool(see.any()):
+            continue
+        for h in range(qh):
+            s = q[int(bt.q_start[b]) + j, h].double() @ f.val["k"][rows[see], h // g].T * scale
+            out[j, h] = torch.softmax(s, -1) @ f.val["v"][rows[see], h // g]
+    return out
+
+
+@pytest.mark.parametrize("x16", ["f16", "bf16"])
+def test_attention_absent_tile_with_bad_scales(x16):
+    """A tile with a row outside the cache is absent, whatever the scales of its
+    other rows are."""
+    fda = lib()
+    bt = ref.Batch([30], [300], 1, 64, "i8", 16, seed=33)
+    f = ref.Filled(bt, "token", seed=33)
+    q = _queries(bt, 2, x16, 33)
+    want = _absent_statement(f, q, 2, 0, 1, 0.125)
+    for t, bad in ((130, float("nan")), (131, float("inf")), (132, 3e38)):
+        f.kw["v_scales"][bt.row(0, t)] = bad
+    good = bt.block_table.copy()
+    bt.block_table[0, 10] = 10 ** 6                # keys 160 .. 175
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 2, ws)
+    assert fda.fd_check_device_error(ws) == (fda.FD_ERR_DEVICE_BOUNDS, 10 ** 6)
+    bt.block_table = good
+    eps = torch.finfo(ref.T16[x16]).eps
+    assert torch.all((out - want).abs() <= (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * want.abs())
+
+
 def test_calls_of_nothing():
     """No packed tokens, no rows: empty results, nothing written."""
     fda = lib()
