@@ -1113,12 +1113,12 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
   if (lane == 0) mbar_arrive(&c.full[slot]);
 }
 
-// Does tile j of the segment's stream hold a row outside the cache?  By one
-// thread; off every fast path.
-static __device__ __noinline__ bool tile_absent(const Prefill& p, const Seg& seg, int j) {
-  const int end = min(seg.end - j * kTile, kTile);
+// Does tile j of sequence b's stream, which ends at key `end`, hold a row
+// outside the cache?  By one thread; off every fast path.
+static __device__ __noinline__ bool tile_absent(const Prefill& p, int b, int end, int j) {
+  end = min(end - j * kTile, kTile);
   for (int k = 0; k < end; ++k)
-    if (placed_row(p.at, seg.b, j * kTile + k) < 0) return true;
+    if (placed_row(p.at, b, j * kTile + k) < 0) return true;
   return false;
 }
 
@@ -1184,7 +1184,7 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
           if (j * kTile + t + 64 * i >= unseen) {
             v[i] = 0.f;
             *(volatile int*)&c.nf[sn & 7] = sn + 1;
-          } else if (tile_absent(p, seg, j)) {   // (its P is zero: 0 * NaN would be seen)
+          } else if (tile_absent(p, seg.b, seg.end, j)) {   // (its P is zero: 0 * NaN would be seen)
             v[i] = 0.f;
           }
         }
@@ -1655,7 +1655,13 @@ struct Softmax {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = o[i];
             const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
-            add_nonfinite<D, KV, BF16, TOK>(p, seg, lo, min(lim, seg.te * kTile), c0, x);
+            const int hi = min(lim, seg.te * kTile);
+            // tile by tile: an absent one has no elements
+#pragma unroll 1
+            for (int j = lo / kTile; j * kTile < hi; ++j)
+              if (!tile_absent(p, seg.b, seg.end, j))
+                add_nonfinite<D, KV, BF16, TOK>(p, seg, max(lo, j * kTile),
+                                                min(hi, (j + 1) * kTile), c0, x);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = x[i];
           }

@@ -123,6 +123,41 @@ def test_attention_absent_tile_with_bad_scales(x16):
     assert torch.all((out - want).abs() <= (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * want.abs())
 
 
+@pytest.mark.parametrize("kv,page", [("f16", 16), ("bf16", 4), ("e4m3", 16)])
+def test_attention_absent_tile_with_bad_values(kv, page):
+    """Non-finite V elements of an absent tile reach nobody, though the pair of
+    query tiles repairs those of another tile."""
+    fda = lib()
+    x16 = kv if kv in ref.T16 else "f16"
+    # streams enough that whole pairs of query tiles, two tiles each, stay in one
+    # block's segment
+    bt = ref.Batch([250] * 24, [0] * 24, 8, 64, kv, page, seed=34)
+    f = ref.Filled(bt, seed=34)
+    q = _queries(bt, 8, x16, 34)
+    cache = f.kw["v_cache"].view(bt.rows, 8, 64)
+    nan = 0x7F if kv == "e4m3" else float("nan")
+    good = bt.block_table.copy()
+    some = range(3, 24, 5)
+    want = {}
+    for b in some:
+        cache[bt.row(b, 5), :, 9] = nan            # in the absent tile
+        cache[bt.row(b, 200), :, 3] = nan
+        f.val["v"][bt.row(b, 200), :, 3] = float("nan")
+        want[b] = _absent_statement(f, q, 8, b, 0, 0.125)
+        bt.block_table[b, 64 // page] = -9         # keys from 64 on
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 8, ws)
+    assert fda.fd_check_device_error(ws) == (fda.FD_ERR_DEVICE_BOUNDS, -9)
+    bt.block_table = good
+    eps = torch.finfo(ref.T16[x16]).eps
+    for b in some:
+        o, w = out[int(bt.q_start[b]):int(bt.q_start[b + 1])], want[b]
+        assert torch.equal(torch.isnan(o), torch.isnan(w)), b
+        fin = torch.isfinite(w)
+        assert torch.all((o - w)[fin].abs() <=
+                         (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * w[fin].abs())
+
+
 def test_calls_of_nothing():
     """No packed tokens, no rows: empty results, nothing written."""
     fda = lib()
