@@ -1215,6 +1215,11 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
 template <int D, int KV, bool BF16, bool TOK>
 __device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int lo, int hi,
                                            int d0, float* o) {
+  float vsc = 1.f;   // (a cut stream's merge brings v_scale)
+  if (seg.complete) {
+    vsc = p.v_scale;
+    if (KV != 0 && p.scale_kind == FD_SCALE_HEAD) vsc *= __ldg(p.v_scales + seg.h);
+  }
   for (int t = lo; t < hi; ++t) {
     const long long row = placed_row(p.at, seg.b, t);
     if (row < 0) continue;
@@ -1233,7 +1238,7 @@ __device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int
         x = static_cast<float>(static_cast<const int8_t*>(p.v)[at + i]);
       }
       x *= scale;
-      if (!isfinite(x)) o[i] += x;
+      if (!isfinite(x)) o[i] += x * vsc;
     }
   }
 }

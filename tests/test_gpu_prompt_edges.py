@@ -158,6 +158,42 @@ def test_attention_absent_tile_with_bad_values(kv, page):
                          (eps / 2 + 2.0 ** -18) * 5.5 + eps / 2 * w[fin].abs())
 
 
+@pytest.mark.parametrize("kv,scales", [("f16", "tensor"), ("bf16", "tensor"), ("i8", "token")])
+def test_attention_infinite_values_under_a_negative_scale(kv, scales):
+    """v_scale times an infinite V element: the sign is that of the product, in
+    streams of one block and in cut ones."""
+    fda = lib()
+    x16 = kv if kv in ref.T16 else "bf16"
+    bt = ref.Batch([90, 300], [0, 2000], 2, 64, kv, 16, seed=35)
+    f = ref.Filled(bt, scales, seed=35)
+    q = _queries(bt, 4, x16, 35)
+    for b, t, h, x in ((0, 40, 0, math.inf), (0, 60, 1, -math.inf), (1, 2100, 0, math.inf),
+                       (1, 2290, 1, -math.inf)):
+        row = bt.row(b, t)
+        if scales == "token":      # every element of the row: by its code's sign
+            f.kw["v_scales"][row, h] = x
+            f.val["v"][row, h] = f.val["v"][row, h].sign() * x
+        else:
+            f.kw["v_cache"].view(bt.rows, 2, 64)[row, h, 7] = x
+            f.val["v"][row, h, 7] = x
+    if scales == "token":
+        f.val["v"] = torch.where(torch.isnan(f.val["v"]), 1.0, f.val["v"])
+    f.kw["v_scale"] = -0.5 * f.kw["v_scale"]
+    f.val["v"] = -0.5 * f.val["v"]
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = _attend(fda, f, q, 4, ws)
+    _ok(fda, ws)
+    want, wlse = ref.attention(f, q, 4, 0.125)
+    inf = torch.isinf(want)
+    assert int(inf.sum()) > 0 and torch.equal(out[inf], want[inf])
+    fin = torch.isfinite(want) & torch.isfinite(out)
+    if scales != "token":      # (there 0 * inf is NaN where a code is zero)
+        assert torch.equal(torch.isfinite(out), torch.isfinite(want))
+    eps = torch.finfo(ref.T16[x16]).eps
+    assert torch.all((out - want)[fin].abs() <=
+                     (eps / 2 + 2.0 ** -18) * 5.5 * 0.5 + eps / 2 * want[fin].abs())
+
+
 def test_calls_of_nothing():
     """No packed tokens, no rows: empty results, nothing written."""
     fda = lib()
