@@ -400,8 +400,12 @@ __device__ __forceinline__ void record_abort(Control& c, const Prefill& p, int r
 
 static __device__ __noinline__ bool wait_slow(Control& c, const Prefill& p, uint64_t* bar,
                                        uint32_t parity, int role) {
-  if (aborted(c)) return false;
-  if (mbar_wait(bar, parity, p.wait_ns)) return true;
+  // a try takes a microsecond at most; once a warp has given up, all do
+  const unsigned long long t0 = mma::global_ns();
+  do {
+    if (aborted(c)) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (mma::global_ns() - t0 <= p.wait_ns);
   record_abort(c, p, role);
   return false;
 }

@@ -284,3 +284,40 @@ def test_refused_prompt_calls_write_nothing():
     out, lse = call(q=mine, out=mine, rotary=fda.rotary_table(8, 64))
     again, lagain = call(rotary=fda.rotary_table(8, 64))
     assert out is mine and torch.equal(out, again) and torch.equal(lse, lagain)
+
+
+@pytest.mark.parametrize("kv,page,scales", [("f16", 0, "tensor"), ("bf16", 64, "tensor"),
+                                            ("f16", 4, "tensor"), ("e4m3", 64, "tensor"),
+                                            ("i8", 16, "token"), ("e4m3", 2, "token")])
+def test_attention_waits_do_run_out(kv, page, scales):
+    """With limits of a few tries of a barrier (a microsecond each), waits run
+    out in a call at work: behind rows gathered one by one, and where the
+    producer passes many empty sequences and then fills its ring for a block
+    that has given up.  Every such call ends and says so, and the next one is
+    right."""
+    fda = lib()
+    x16 = kv if kv in ref.T16 else "f16"
+    none = [0] * 1500
+    bt = ref.Batch([300, 1] + none + [64, 3] + none + [1, 200],
+                   [40, 3000] + none + [0, 900] + none + [5000, 1500], 4, 128, kv, page, seed=36)
+    f = ref.Filled(bt, scales, seed=36)
+    q = _queries(bt, 16, x16, 36)
+    ws = fda.alloc_prefill_workspace(128)
+    want, wlse = ref.attention_blocks(f, q, 16, 128 ** -0.5)
+    junk = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    seen = []
+    for limit in (1, 1000, 3000, 10000):
+        fda.fd_debug_set_wait_limit(limit, False)
+        try:
+            for _ in range(4):
+                junk.fill_(limit & 7)        # the caches' rows come from memory again
+                _attend(fda, f, q, 16, ws)
+                seen.append(fda.fd_check_device_error(ws)[0])
+        finally:
+            fda.fd_debug_set_wait_limit(0, False)
+    print(kv, page, scales, seen)
+    assert set(seen) <= {fda.FD_OK, fda.FD_ERR_DEVICE_TIMEOUT}
+    assert fda.FD_ERR_DEVICE_TIMEOUT in seen[:4], seen
+    out, lse = _attend(fda, f, q, 16, ws)
+    _ok(fda, ws)
+    _compare(f, out, lse, want, wlse, x16)
