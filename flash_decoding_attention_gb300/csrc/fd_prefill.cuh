@@ -230,6 +230,19 @@ struct Seg {
   int slot;                  // partial slot otherwise
 };
 
+// The first sequence behind b whose entries differ, or the batch's end; by a
+// whole warp, 32 sequences at a time (a batch may hold millions of empty ones,
+// and the other warps' waits have their limit).
+static __device__ __forceinline__ int next_owner(const int32_t* start, int batch, int b) {
+  for (++b; b < batch; b += 32) {
+    const int i = b + (threadIdx.x & 31);
+    const bool owns = i < batch && __ldg(start + i) != __ldg(start + i + 1);
+    const unsigned any = __ballot_sync(0xffffffffu, owns);
+    if (any) return b + __ffs(any) - 1;
+  }
+  return batch;
+}
+
 // The segments of this CTA, in order; every role walks its own copy.
 template <bool TOK>
 struct Walk {
@@ -298,10 +311,13 @@ struct Walk {
         m = 0;
         if (++h == p.num_kv_heads) {
           h = 0;
-          int b = s.b + 1;
-          for (; ps < g_end && b < p.at.batch; ++b) {
-            s = load_seq<TOK>(p, b, false);
-            if (s.n > 0) break;
+          if (ps < g_end) {
+            int b = s.b;
+            do {
+              b = next_owner(p.q_start, p.at.batch, b);
+              if (b >= p.at.batch) break;
+              s = load_seq<TOK>(p, b, false);
+            } while (s.n == 0);
           }
         }
       }

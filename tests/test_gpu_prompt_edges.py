@@ -297,7 +297,7 @@ def test_attention_waits_do_run_out(kv, page, scales):
     right."""
     fda = lib()
     x16 = kv if kv in ref.T16 else "f16"
-    none = [0] * 1500
+    none = [0] * (16000 if page in (0, 16, 64) else 0)
     bt = ref.Batch([300, 1] + none + [64, 3] + none + [1, 200],
                    [40, 3000] + none + [0, 900] + none + [5000, 1500], 4, 128, kv, page, seed=36)
     f = ref.Filled(bt, scales, seed=36)
@@ -321,3 +321,26 @@ def test_attention_waits_do_run_out(kv, page, scales):
     out, lse = _attend(fda, f, q, 16, ws)
     _ok(fda, ws)
     _compare(f, out, lse, want, wlse, x16)
+
+
+def test_attention_passes_millions_of_empty_sequences():
+    """A batch of empty sequences with two prompts far apart: no wait for the
+    warp that looks for the next prompt runs out."""
+    fda = lib()
+    B = 12 * 10 ** 6
+    bt = ref.Batch([70, 50], [0, 0], 2, 64, "f16", 0, seed=37)
+    f = ref.Filled(bt, seed=37)
+    q = _queries(bt, 4, "f16", 37)
+    kw = f.device(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    starts, lens, first = torch.full((B + 1,), 70, **i32), torch.zeros(B, **i32), torch.zeros(B, **i32)
+    starts[0], starts[B] = 0, 120
+    lens[0], lens[B - 1] = 70, 50
+    first[0], first[B - 1] = int(bt.kv_start_idx[0]), int(bt.kv_start_idx[1])
+    ws = fda.alloc_prefill_workspace(64)
+    out, lse = fda.prefill_attention(q.to(DEV), kw["k_cache"], kw["v_cache"], starts, lens,
+                                     kv_start_idx=first, workspace=ws)
+    torch.cuda.synchronize()
+    _ok(fda, ws)
+    want, wlse = ref.attention_blocks(f, q, 4, 0.125)
+    _compare(f, out.double().cpu(), lse.double().cpu(), want, wlse, "f16")
