@@ -103,8 +103,9 @@ struct Merge {
         const int k = k0 + u * step;
         ml[u] = make_float2(-INFINITY, 0.f);
         if (live && k < it.parts) {
-          // (written as a sum: with a choice between two addresses the
-          // compiled loop read the wrong slot from its second state on)
+          // (a sum, not a choice by k: nvcc 13.0 translates
+          // k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1) wrongly where such a loop
+          // is unrolled by four; a kernel of nothing else shows it)
           const int slot = 2 * (it.c - 1 + k) + (k == 0 ? 1 : 0);
           const long long tile = 2ll * slot + it.X;
           ml[u] = p.part_ml[tile * kRowsTile + it.row0 + lane];

@@ -17,20 +17,21 @@
 // Split.  (sequence, KV head, pair of query tiles) are the streams.  Their
 // costs (keys to pass plus a start) are laid end to end and cut into one
 // equal range per CTA, whatever the lengths: a long prompt's causal triangle,
-// a chunk over a long context and single tokens beside them all fill the GPU.  A stream cut between CTAs leaves
-// partial states (m, l, unnormalised out) that fd_prefill.cu merges in a
-// fixed order.  A pair with rows in A only (a solo segment: single tokens, a
+// a chunk over a long context and single tokens beside them all fill the GPU.
+// A stream cut between CTAs leaves partial states (m, l, unnormalised out)
+// that fd_prefill.cu merges in a fixed order.  A pair with rows in A only (a solo segment: single tokens, a
 // chunk's end) has its keys shared between the two halves of the CTA instead,
 // which merge their states through shared memory: the time of a tile is a
 // chain (S, softmax, P V), the same for one query tile as for two.
 //
 // What bounds it, on GB300 (152 SMs), bf16, 32 query / 8 KV heads, D = 128:
-// 2048 new tokens over 30000 cached ones run at 1.60 PFLOP/s, 0.83 of the
-// cuBLAS burst rate and 0.93 of its sustained one: the tensor cores (and the
+// 2048 new tokens over 30000 cached ones run at 1.70 PFLOP/s, 0.87 of the
+// cuBLAS burst rate and 0.99 of its sustained one: the tensor cores (and the
 // power limit).  Whole prompts, with a start and an end for every 26 tiles or
-// so, run at 1.38 PFLOP/s.  With 8-bit caches the widened copies compete with
-// the products for shared memory's port (e4m3 / f16 1.51 PFLOP/s).  Decode-like
-// batches (one token over 4096 keys, bf16) read the cache at 5.6 TB/s.
+// so, run at 1.52 PFLOP/s replayed from a graph, 1.41 called one by one.  With
+// 8-bit caches the widened copies compete with the products for shared
+// memory's port (e4m3 under f16 1.6 PFLOP/s).  Decode-like batches (one token
+// over 4096 keys, bf16) read the cache at 5.5 TB/s.
 //
 // Roles (one persistent CTA per SM):
 //   warps 0-3, 4-7  softmax of query tile A, B: one row per thread, its scores
@@ -39,8 +40,8 @@
 //   warp 8          TMA producer: Q tiles, K and V tiles through one ring;
 //   warp 9          issues S = Q K^T and O += P V for A and B as their inputs
 //                   become ready (O and S: 2 x 128 columns each, all 512);
-//   warps 10-11     repair V tiles that some row may not see (see below);
-//                   With a scale per token they fetch the scales instead;
+//   warps 10-11     repair V tiles that some row may not see (see below); with
+//                   a scale per token they fetch the scales instead;
 //   warps 12-15     (8-bit caches, or pages of fewer than 8 rows) widen or
 //                   copy the cache rows into the ring; the producer then feeds
 //                   raw tiles to them.
@@ -54,10 +55,11 @@
 //
 // Roundings below 32 bits: P to the query's 16-bit type (the tensor cores
 // take 16-bit operands; an error of half a step of each probability, the
-// size of the output's own rounding), and the output.  With f16, P is scaled
-// by 2^6 so that small probabilities stay above f16's subnormals; the
-// running maximum is moved only when exceeded by 2^8 (O is then rescaled in
-// tensor memory), which keeps P below 2^14.  With a scale per token as well,
+// size of the output's own rounding; l sums P unrounded, so that the lse keeps
+// 32 bits), and the output.  With f16, P is scaled by 2^6 so that small
+// probabilities stay above f16's subnormals; the running maximum is moved only
+// when exceeded by 2^8 (O is then rescaled in tensor memory), which keeps P
+// below 2^14 (so P of a row's largest score need not be exact).  With a scale per token as well,
 // P times the V scale is what is rounded, divided by the power of two of the
 // largest scale that the row itself has seen: taken over the whole tile, a
 // later token's scale would push an earlier row's P out of f16's range.
@@ -84,13 +86,14 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9, kFixWarp0 = 10, kConvWarp0 = 12;
 constexpr int kPages = 20;          // block-table entries staged at a time (a tile has 16)
 constexpr int kMaxSlots = 8, kMaxRaw = 4;
 // What the split counts, in keys: a segment's start (Q load, first product,
-// epilogue) and a tile that only query tile A passes.  Four bf16 prompts of
-// 8192 tokens in all: 480 us with a start of 320 and 480, 438 with 640, 495
-// with 800, 448 with 1000.  Without a scale per token a solo tile costs as
-// much as a full one where it matters (8-bit: the widening bounds both; long
-// e4m3 contexts take 145 us with 128, 165 with 96).  With one, the softmax of a
-// full tile is the longer chain: a mixed INT8 batch takes 271 us with 320 and
-// 128, 257 with 320 and 104, 261 with 256 and 92, 255 with 448 and 92.
+// epilogue: about 7 us, against 1.4 to 2.5 for a tile) and a tile that only
+// query tile A passes.  Neither is sharp: four bf16 prompts (10824 tokens) take
+// 421 us with a start of 320, 390 with 400, 382 with 560, 384 with 640, 399 with
+// 800 and 400 with 1000; e4m3 chunks 128, 126, 124, 122, 118 and 122.  Without a
+// scale per token a solo tile costs as much as a full one where it matters
+// (8-bit: the widening bounds both).  With one, the softmax of a full tile is
+// the longer chain, 2.3 against 1.9 us: a mixed INT8 batch takes 243 us with
+// 320 and 128, 239 with 320 and 92, 229 with 384 and 92, 240 with 448 and 92.
 template <bool TOK>
 struct Cost {
   static constexpr int kStart = TOK ? 448 : 640;
@@ -383,10 +386,12 @@ struct Control {
 constexpr uint32_t kCtlBytes = (sizeof(Control) + 15) / 16 * 16;
 
 // Per-token scales of a tile's 128 keys: rings of kKeyRing K arrays, then
-// kValRing V arrays.  Both are written when the converters fill the tile's
-// operand slot.  A K slot is free once S of both query tiles is done, but its
-// scales are read after S, by a softmax that is done once the next S of its
-// query tile is: one array more than the slots hold.
+// kValRing V arrays, written when the tile's operand slots are free.  A V slot
+// is free once P V is done, for which the softmax has read the V scales.  A K
+// slot is free once S is done, but its scales are read after that.  The warps
+// that write tile n's have waited before, for tile n - 1's V, until P V of tile
+// n - 1 - kSlots / 2 was done, whose softmax had read its K scales: one array
+// more than the slots hold, and the order of those waits, keep them apart.
 template <int D, int KV>
 struct ScaleRing {
   static constexpr int kKeyRing = Shape<D, KV, true>::kSlots / 2 + 1;
@@ -550,8 +555,8 @@ __device__ __forceinline__ int tile_info(const Seg& s, int j, int unseen, bool b
 // ---------------------------------------------------------------------------
 // Producer warp
 // ---------------------------------------------------------------------------
-// One K or V tile by TMA into `dst` (16-bit: D / 64 blocks of 128-byte rows;
-// 8-bit: rows of D bytes): the boxes of the tile's rows below `end`.
+// The boxes that bring a K or V tile: of D / 64 blocks of 128-byte rows
+// (16-bit), or of rows of D bytes (8-bit).
 template <int D, int KV>
 struct TileCopy {
   static constexpr int kRowBytes = KV == 0 || D == 128 ? 128 : 64;   // of a box
@@ -569,11 +574,6 @@ static __device__ __forceinline__ void land_copies(Control& c, const Prefill& p,
   if (q0 > 0) late |= !mbar_wait(&c.q_full[0], (uint32_t)((q0 - 1) & 1), mma::kDrainNs);
   if (q1 > 0) late |= !mbar_wait(&c.q_full[1], (uint32_t)((q1 - 1) & 1), mma::kDrainNs);
   if (late) raise_error(p.at.ws, kErrDrain, 3);
-}
-
-static __device__ __noinline__ void land_copies_call(Control& c, const Prefill& p, uint64_t* full,
-                                                     int slots, int issued, int q0, int q1) {
-  land_copies(c, p, full, slots, issued, q0, q1);
 }
 
 template <int D, int KV, bool CONV, bool TOK>
@@ -700,12 +700,7 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
     }
     stop = __any_sync(0xffffffffu, stop);
   }
-  // (a call or not moves the registers of the whole kernel: four bf16 prompts
-  // 421 us with the call, 454 without; e4m3 chunks 147 with it, 140 without)
-  if (lane == 0) {
-    if constexpr (CONV) land_copies(c, p, full, NS, issued, qn[0], qn[1]);
-    else land_copies_call(c, p, full, NS, issued, qn[0], qn[1]);
-  }
+  if (lane == 0) land_copies(c, p, full, NS, issued, qn[0], qn[1]);
   __syncwarp();
   if (!stop && KV == 0 && !CONV) {   // (with converters they write the end)
     const int e = 2 * n, slot = e % NS;
@@ -1147,10 +1142,10 @@ static __device__ __noinline__ bool tile_absent(const Prefill& p, int b, int end
 // ---------------------------------------------------------------------------
 // Values are loaded one tile ahead, their block-table entries two.  Loaded by
 // the converters, between their other loads, they cost each tile a memory
-// latency: single tokens over INT8, 2.56 us a tile in place of 1.92 (the time
-// without scales per token), full tiles 2.88 in place of 2.69.  Widening is not
-// a work for these two warps: with six warps at it e4m3 under f16 fell from
-// 1500 to 1150 TFLOP/s.
+// latency: single tokens over INT8, 2.56 us a tile in place of 1.9 (the time
+// without scales per token), full tiles 0.2 more.  Widening is not a work for
+// these two warps: with six warps at it the products wait for shared memory's
+// port (e4m3 under f16 at three quarters of the rate).
 template <int D, int KV>
 __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, Control& c,
                                              float* scales) {
@@ -1816,7 +1811,6 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   const uint32_t tbase = c.tmem_base;
   allow_dependent_launch();
 
-  // The register shares add up to the launch's registers (168 x 384; 128 x 512).
   if (warp < 8) {
     const int X = warp >> 2, w4 = warp & 3, lane = threadIdx.x & 31;
     const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);

@@ -6,7 +6,8 @@
 // 2^-64): the product with p modulo 2^64 is the exact reduction, and the
 // distance to the nearest quarter turn, at most an eighth, converts to fp32
 // with full relative precision.  There cos and sin are their Taylor sums
-// around zero (remainders below 2^-31), swapped and negated by the quarter.
+// around zero (remainders below 2^-33 and 2^-29), swapped and negated by the
+// quarter.
 //
 // A block takes several steps of a few positions each, the grid's blocks side
 // by side in every step.  Position P + j (P the step's first, j the place of a
@@ -15,8 +16,9 @@
 // so that the series are summed for the steps' P (shared memory) and once for
 // j (registers) instead of for every element: one level of sums, no error
 // that grows with p.  In units of 2^-24 of the amplitude a sum rounds by 0.6
-// (its angle carries a second word), the amplitude by 1, the product and the
-// last sum by 1 of their values: at most 4.43 altogether.  A table of one step
+// (its angle carries a second word) and leaves out 0.03, the amplitude rounds by
+// 1, the product and the last sum by 1 of their values: at most 4.52
+// altogether.  A table of one step
 // sums the series at P + j itself.
 //
 // The stores bound it: 131072 positions of 128 (67 MB) take 12.4 us in a row,
