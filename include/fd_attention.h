@@ -471,9 +471,10 @@ size_t fd_prefill_workspace_bytes(int head_dim);
  * Probabilities are rounded to q_dtype before they multiply V (with
  * FD_SCALE_TOKEN: times their V scale).  With f16 queries a probability below
  * about 2^-20 keeps an absolute error of 2^-31, with FD_SCALE_TOKEN 2^-31 of
- * the largest |V scale| that the token sees: a seen scale above 2^20 times the
- * others costs those precision, even where its own probability is small.  bf16
- * queries have no such floor.
+ * the largest |V scale| that the token sees: a seen scale above about 2^10
+ * times the others (the scale 1 of an appended row of zeros among them, where
+ * v_scale leaves the others far below 1) costs those precision, even where its
+ * own probability is small.  bf16 queries have no such floor.
  *
  * q          [num_tokens, num_q_heads, head_dim] of q_dtype, tokens q_stride
  *            elements apart (a multiple of 8, at least one token's heads).
