@@ -67,7 +67,7 @@ EXPORTED = [
     "fd_append_kv", "fd_decode_attention_append", "fd_decode_attention_multi",
     "fd_debug_set_wait_limit", "fd_debug_plan_segments",
     "fd_rotary_table", "fd_append_kv_packed", "fd_read_kv", "fd_prefill_workspace_bytes",
-    "fd_prefill_attention",
+    "fd_prefill_attention", "fd_decode_attention_window", "fd_prefill_attention_window",
 ]
 
 
@@ -159,6 +159,14 @@ def load_library(path: Optional[str] = None):
         lib.fd_prefill_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, vp, vp, i64, i64, i32,
                                              i32, i32, i32, i32, f32, f32, f32, i32, vp, vp, i32,
                                              i32, vp, vp, vp, sz, vp]
+        lib.fd_decode_attention_window.restype = i32
+        lib.fd_decode_attention_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i64,
+                                                   i32, i32, i32, i32, i32, i32, i32, f32, f32,
+                                                   f32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        lib.fd_prefill_attention_window.restype = i32
+        lib.fd_prefill_attention_window.argtypes = [vp, i64, vp, vp, vp, vp, i32, vp, vp, i64, i64,
+                                                    i32, i32, i32, i32, i32, i32, i32, f32, f32,
+                                                    f32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
         if path is None:
             _lib = lib
         return lib
@@ -349,6 +357,29 @@ def fd_decode_attention_append(q, k_new, v_new, k_cache, v_cache, kv_start_idx, 
     return st
 
 
+def fd_decode_attention_window(q, k_new, v_new, k_cache, v_cache, kv_start_idx, block_table,
+                               positions, seq_len, kv_rows: int, num_q_heads: int,
+                               num_kv_heads: int, head_dim: int, page_size: int, window: int,
+                               sinks: int, softmax_scale: float, k_scale: float, v_scale: float,
+                               scale_kind: int, k_scales, v_scales, out, lse, workspace,
+                               stream=None, q_dtype: Optional[int] = None,
+                               kv_dtype: Optional[int] = None, check: bool = True) -> int:
+    """One query token per sequence that sees its sequence's last ``window``
+    tokens and first ``sinks`` ones; ``k_new`` / ``v_new`` / ``positions`` as
+    in fd_decode_attention_append, or None."""
+    st = (_lib or load_library()).fd_decode_attention_window(
+        q.data_ptr(), _ptr(k_new), _ptr(v_new), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(kv_start_idx), _ptr(block_table), 0 if block_table is None else block_table.shape[1],
+        _ptr(positions), seq_len.data_ptr(), kv_rows, seq_len.shape[0], num_q_heads, num_kv_heads,
+        head_dim, page_size, window, sinks, softmax_scale, k_scale, v_scale, scale_kind,
+        _ptr(k_scales), _ptr(v_scales), _q_dtype(q) if q_dtype is None else q_dtype,
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype, out.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_decode_attention_window")
+    return st
+
+
 def fd_decode_attention_noalloc(q, k_cache, v_cache, kv_start_idx, block_table, seq_len,
                                 kv_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                 page_size: int, softmax_scale: float, k_scale: float,
@@ -455,6 +486,29 @@ def fd_prefill_attention(q, q_stride: int, k_cache, v_cache, kv_start_idx, block
         workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_prefill_attention")
+    return st
+
+
+def fd_prefill_attention_window(q, q_stride: int, k_cache, v_cache, kv_start_idx, block_table,
+                                q_start, seq_len, num_tokens: int, kv_rows: int,
+                                num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                page_size: int, window: int, sinks: int, softmax_scale: float,
+                                k_scale: float, v_scale: float, scale_kind: int, k_scales,
+                                v_scales, out, lse, workspace, stream=None,
+                                q_dtype: Optional[int] = None, kv_dtype: Optional[int] = None,
+                                check: bool = True) -> int:
+    """fd_prefill_attention whose tokens see the last ``window`` keys up to
+    their own and the sequence's first ``sinks`` ones."""
+    st = (_lib or load_library()).fd_prefill_attention_window(
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_start_idx),
+        _ptr(block_table), 0 if block_table is None else block_table.shape[1], q_start.data_ptr(),
+        seq_len.data_ptr(), num_tokens, kv_rows, seq_len.shape[0], num_q_heads, num_kv_heads,
+        head_dim, page_size, window, sinks, softmax_scale, k_scale, v_scale, scale_kind,
+        _ptr(k_scales), _ptr(v_scales), _q_dtype(q) if q_dtype is None else q_dtype,
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype, out.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_prefill_attention_window")
     return st
 
 
@@ -570,7 +624,8 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      k_scales: Optional[torch.Tensor] = None,
                      v_scales: Optional[torch.Tensor] = None,
                      k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
-                     positions: Optional[torch.Tensor] = None):
+                     positions: Optional[torch.Tensor] = None, window: Optional[int] = None,
+                     sinks: int = 0):
     """Decode attention over a contiguous ([rows, KVH, D]) or paged
     ([pages, page_size, KVH, D]) cache; returns (out, lse).  Optional 8-bit
     ``k_scales`` / ``v_scales``: fp32 [KVH] (per KV head) or [kv_rows, KVH]
@@ -581,7 +636,16 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ``q`` ([B, QH, q_len, D]) asks for q_len query tokens per sequence, the
     last q_len cached tokens, causal among themselves (out and lse carry the
     q_len axis too); with it, k_new / v_new are [B, q_len, KVH, D] and
-    ``positions`` holds the first new token's index."""
+    ``positions`` holds the first new token's index.  With ``window`` the query
+    sees its sequence's last ``window`` tokens, itself among them, and the first
+    ``sinks`` ones (3-d ``q`` only; several query tokens with a window are
+    ``prefill_attention``'s)."""
+    if window is not None:
+        return _decode_window(q, k_cache, v_cache, seq_len, kv_start_idx, block_table,
+                              softmax_scale, k_scale, v_scale, workspace, out, lse, stream,
+                              k_scales, v_scales, k_new, v_new, positions, window, sinks)
+    if sinks:
+        raise ValueError("sinks are the first tokens that stay visible behind a window: give window")
     multi = q.dim() == 4              # [B, QH, q_len, D]: multi-token queries
     B, QH, D = q.shape[0], q.shape[1], q.shape[-1]
     q_len = q.shape[2] if multi else 1
@@ -622,6 +686,55 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
         fd_decode_attention_scaled(q, k_cache, v_cache, kv_start_idx, block_table, seq_len,
                                    kv_rows, QH, KVH, D, P, softmax_scale, k_scale, v_scale, kind,
                                    k_scales, v_scales, out, lse, workspace, stream)
+    return out, lse
+
+
+def _window_sizes(window, sinks) -> None:
+    if window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")
+
+
+def _decode_window(q, k_cache, v_cache, seq_len, kv_start_idx, block_table, softmax_scale, k_scale,
+                   v_scale, workspace, out, lse, stream, k_scales, v_scales, k_new, v_new,
+                   positions, window, sinks):
+    """decode_attention with a window (checks, allocations, the call)."""
+    _window_sizes(window, sinks)
+    kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
+    dev, at = k_cache.device, k_cache.get_device()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or not q.is_contiguous():
+        raise ValueError(f"q must be dense [batch, heads, {D}] with a window, got {tuple(shape)} "
+                         f"(strides {q.stride()})")
+    batch, QH = shape[0], shape[1]
+    _index("seq_len", seq_len, batch, at)
+    _layout_index(kv_start_idx, block_table, batch, at)
+    _same_device(at, q, v_cache, out, lse, workspace, k_new, v_new)
+    kind = _scale_kind(k_scales, v_scales, kv_rows, KVH, at)
+    if (k_new is None) != (v_new is None) or (k_new is None) != (positions is None):
+        raise ValueError("give k_new, v_new and positions, or none of them")
+    if k_new is not None:
+        _index("positions", positions, batch, at)
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            if tuple(t.shape) != (batch, KVH, D) or t.dtype != q.dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be dense [{batch}, {KVH}, {D}] of q's dtype")
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or not out.is_contiguous()):
+        raise ValueError("out must be dense and like q")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or
+                            not lse.is_contiguous()):
+        raise ValueError(f"lse must be dense fp32 [{batch}, {QH}]")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((batch, QH), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = alloc_workspace(batch, QH, KVH, D, dev)
+        fd_decode_attention_window(q, k_new, v_new, k_cache, v_cache, kv_start_idx, block_table,
+                                   positions, seq_len, kv_rows, QH, KVH, D, P, window, sinks,
+                                   softmax_scale, k_scale, v_scale, kind, k_scales, v_scales, out,
+                                   lse, workspace)
     return out, lse
 
 
@@ -881,7 +994,8 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                       positions: Optional[torch.Tensor] = None,
                       rotary: Optional[torch.Tensor] = None, interleaved: bool = False,
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                      workspace: Optional[torch.Tensor] = None, stream=None):
+                      workspace: Optional[torch.Tensor] = None, stream=None,
+                      window: Optional[int] = None, sinks: int = 0):
     """Attention of packed new tokens ``q`` [tokens, QH, D] (sequence b's at
     ``q_start[b]`` .. ``q_start[b + 1]`` - 1: the last of its ``seq_len[b]``
     tokens, causal) over a contiguous or paged cache; returns (out, lse).
@@ -892,7 +1006,12 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     leaves alone have no turned query: their rows of ``out`` and ``lse`` are
     undefined (zero and -inf where ``seq_len`` gives them no key).  Without
     ``k_new`` the caches hold the new tokens already and ``q`` is taken as it
-    is."""
+    is.  With ``window`` a token sees the last ``window`` keys up to its own and
+    the sequence's first ``sinks`` ones."""
+    if window is not None:
+        _window_sizes(window, sinks)
+    elif sinks:
+        raise ValueError("sinks are the first tokens that stay visible behind a window: give window")
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
     dev, at = k_cache.device, k_cache.get_device()
     shape = q.shape
@@ -927,14 +1046,23 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             lse = torch.empty((n, QH), dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = alloc_prefill_workspace(D, dev)
+
+        def attend(q, qs, n):
+            if window is None:
+                fd_prefill_attention(q, qs, k_cache, v_cache, kv_start_idx, block_table, q_start,
+                                     seq_len, n, kv_rows, QH, KVH, D, P, softmax_scale, k_scale,
+                                     v_scale, kind, k_scales, v_scales, out, lse, workspace)
+            else:
+                fd_prefill_attention_window(q, qs, k_cache, v_cache, kv_start_idx, block_table,
+                                            q_start, seq_len, n, kv_rows, QH, KVH, D, P, window,
+                                            sinks, softmax_scale, k_scale, v_scale, kind,
+                                            k_scales, v_scales, out, lse, workspace)
         if k_new is not None:
             # a call that the attention refuses leaves the caches as they were:
             # its checks (of no tokens) come before the append
             if rotary is None and _overlap(out, q):
                 raise ValueError("out must not overlap q")
-            fd_prefill_attention(q, qs, k_cache, v_cache, kv_start_idx, block_table, q_start,
-                                 seq_len, 0, kv_rows, QH, KVH, D, P, softmax_scale, k_scale,
-                                 v_scale, kind, k_scales, v_scales, out, lse, workspace)
+            attend(q, qs, 0)
             turned = append_kv(k_new, v_new, k_cache, v_cache, q_start, positions,
                                q=q if rotary is not None else None, rotary=rotary,
                                interleaved=interleaved, kv_start_idx=kv_start_idx,
@@ -942,7 +1070,5 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                                k_scales=k_scales, v_scales=v_scales, workspace=workspace)
             if turned is not None:
                 q, qs = turned, QH * D
-        fd_prefill_attention(q, qs, k_cache, v_cache, kv_start_idx, block_table, q_start, seq_len,
-                             n, kv_rows, QH, KVH, D, P, softmax_scale, k_scale, v_scale, kind,
-                             k_scales, v_scales, out, lse, workspace)
+        attend(q, qs, n)
     return out, lse

@@ -371,7 +371,8 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
                              fd_scale_kind scale_kind, const float* k_scales,
                              const float* v_scales, fd_dtype q_dtype, fd_dtype kv_dtype, void* out,
                              float* lse, void* workspace, size_t workspace_bytes,
-                             fd_stream_t stream, const AppendArgs* app, int q_len = 1) {
+                             fd_stream_t stream, const AppendArgs* app, int q_len = 1,
+                             int window = 0, int sinks = 0) {
   const fd_status chk = check_decode_args(
       q, k_cache, v_cache, kv_start_idx, block_table, block_table_stride, seq_len, kv_rows, batch,
       num_q_heads, num_kv_heads, head_dim, page_size, softmax_scale, k_scale, v_scale, scale_kind,
@@ -387,7 +388,12 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
   Config c;
-  if (!choose(g_kernel.load(), virt_heads, num_kv_heads, head_dim, q_dtype, kv_dtype, paged,
+  int pref = g_kernel.load();
+  if (window) {   // the mma.sync kernel has the window's variants
+    if (pref != FD_KERNEL_AUTO && pref != FD_KERNEL_MMA) return FD_ERR_UNSUPPORTED;
+    pref = FD_KERNEL_MMA;
+  }
+  if (!choose(pref, virt_heads, num_kv_heads, head_dim, q_dtype, kv_dtype, paged,
               page_size, sms, &c, scale_kind == FD_SCALE_TOKEN))
     return FD_ERR_UNSUPPORTED;
   const WsLayout L = ws_layout(batch * c.hg, c.grid, c.hq, head_dim);
@@ -418,6 +424,13 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
   p.page_shift = paged ? log2i(page_size) : 0;
   p.group = virt_heads / num_kv_heads;
   p.q_len = q_len;
+  if (window) {
+    p.window = window;
+    // more first tokens than any sequence has are all of them
+    p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+    p.sink_tokens = (p.sinks + c.tile - 1) / c.tile * c.tile;
+    p.win_align = !paged ? 1 : page_size < c.tile ? page_size : c.tile;
+  }
   p.hc = c.hc;
   p.hg = c.hg;
   p.hq = c.hq;
@@ -505,6 +518,26 @@ fd_status fd_decode_attention_append(const void* q, const void* k_new, const voi
                      kv_rows, batch, num_q_heads, num_kv_heads, head_dim, page_size,
                      softmax_scale, k_scale, v_scale, scale_kind, k_scales, v_scales, q_dtype,
                      kv_dtype, out, lse, workspace, workspace_bytes, stream, &app, q_len);
+}
+
+fd_status fd_decode_attention_window(const void* q, const void* k_new, const void* v_new,
+                                     void* k_cache, void* v_cache, const int32_t* kv_start_idx,
+                                     const int32_t* block_table, int block_table_stride,
+                                     const int32_t* positions, const int32_t* seq_len,
+                                     int64_t kv_rows, int batch, int num_q_heads, int num_kv_heads,
+                                     int head_dim, int page_size, int window, int sinks,
+                                     float softmax_scale, float k_scale, float v_scale,
+                                     fd_scale_kind scale_kind, float* k_scales, float* v_scales,
+                                     fd_dtype q_dtype, fd_dtype kv_dtype, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, fd_stream_t stream) {
+  if (window < 1 || sinks < 0) return FD_ERR_INVALID_ARG;
+  if (!k_new != !v_new || !k_new != !positions) return FD_ERR_INVALID_ARG;
+  const AppendArgs app{k_new, v_new, positions, k_cache, v_cache, k_scales, v_scales};
+  return decode_impl(q, k_cache, v_cache, kv_start_idx, block_table, block_table_stride, seq_len,
+                     kv_rows, batch, num_q_heads, num_kv_heads, head_dim, page_size,
+                     softmax_scale, k_scale, v_scale, scale_kind, k_scales, v_scales, q_dtype,
+                     kv_dtype, out, lse, workspace, workspace_bytes, stream, k_new ? &app : nullptr,
+                     1, window, sinks);
 }
 
 fd_status fd_append_kv(const void* k_new, const void* v_new, void* k_cache, void* v_cache,

@@ -44,7 +44,7 @@ __device__ void stream_prefix(const Params& p, int S, int32_t* sp, int32_t* wsum
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     const int st = tid * PER + k;
-    u[k] = st < S ? (int32_t)stream_units(p, st) : 0;
+    u[k] = st >= S ? 0 : (int32_t)(p.window ? stream_units<true>(p, st) : stream_units(p, st));
     mine += u[k];
   }
   int32_t x = mine;

@@ -103,6 +103,12 @@ struct Params {
   // them): virtual head v = qh * q_len + j is token j of query head qh, and
   // it attends to the first T - (q_len - 1 - j) keys of its sequence.
   int q_len;
+  // Sliding window (one query token): the query sees the tokens of the window,
+  // t >= T - window, and the first `sinks` ones; 0: every token.  Streams then
+  // run over the sequence with the hidden middle left out (see window_gap).
+  int window, sinks;
+  int sink_tokens;   // sinks rounded up to whole tiles
+  int win_align;     // window tiles start at a multiple of this (a box's rows; 1: anywhere)
   // KV append (fd_append.cu); q_dtype is the dtype of k_new / v_new
   const void* k_new;         // [batch][n_new][KVH][D]
   const void* v_new;
@@ -156,17 +162,31 @@ cudaError_t launch_empty(int grid, int threads, int smem, cudaStream_t st);
 // s inside one CTA's range form a segment; a range that holds only some of
 // a stream's A leading units holds no segment of it.
 // ---------------------------------------------------------------------------
+// With a window, a stream's tokens are numbered without the hidden middle:
+// token x of the stream is token x of the sequence below sink_tokens, and
+// x + gap from there on, with gap the (aligned) tokens that lie between the
+// first tokens' last tile and the window's first.  Plan and merge then work on
+// stream tokens alone.
+__device__ __forceinline__ int window_gap(const Params& p, int T) {
+  const int first = T - p.window;   // of the window
+  return first > 0 ? max(0, (first & ~(p.win_align - 1)) - p.sink_tokens) : 0;
+}
+
+template <bool WIN = false>
 __device__ __forceinline__ int stream_tokens(const Params& p, int s) {
   int t = __ldg(p.seq_len + s / p.hg);
-  return t > 0 ? t : 0;
+  t = t > 0 ? t : 0;
+  return WIN ? t - window_gap(p, t) : t;
 }
 
+template <bool WIN = false>
 __device__ __forceinline__ int stream_tiles(const Params& p, int s) {
-  return (stream_tokens(p, s) + p.tile - 1) / p.tile;
+  return (stream_tokens<WIN>(p, s) + p.tile - 1) / p.tile;
 }
 
+template <bool WIN = false>
 __device__ __forceinline__ int stream_units(const Params& p, int s) {
-  const int n = stream_tiles(p, s);
+  const int n = stream_tiles<WIN>(p, s);
   return n > 0 ? n + p.seg_units : 0;
 }
 
@@ -201,13 +221,14 @@ __device__ __forceinline__ void plan_sync(int id, int nthreads) {
 // plan words of the header.  `red` is >= 35 long longs of shared memory.
 // With at most one stream per thread it is one pass (one read of seq_len,
 // and of kv_start alongside it); else two.
+template <bool WIN = false>
 __device__ inline PlanResult compute_plan(const Params& p, long long* red, int nthreads, int bar,
                                           unsigned long long* stamp = nullptr) {
   const int S = p.batch * p.hg;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nwarps = nthreads >> 5;
   if (S <= nthreads) {
-    const long long v = tid < S ? stream_units(p, tid) : 0;
+    const long long v = tid < S ? stream_units<WIN>(p, tid) : 0;
     const long long kvs = tid < S && p.kv_start ? (long long)__ldg(p.kv_start + tid / p.hg) : -1;
     long long x = v;
 #pragma unroll
@@ -255,7 +276,7 @@ __device__ inline PlanResult compute_plan(const Params& p, long long* red, int n
   }
   // pass 1: total units
   long long acc = 0;
-  for (int s = tid; s < S; s += nthreads) acc += stream_units(p, s);
+  for (int s = tid; s < S; s += nthreads) acc += stream_units<WIN>(p, s);
   for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if (lane == 0) red[warp] = acc;
   plan_sync(bar, nthreads);
@@ -277,7 +298,7 @@ __device__ inline PlanResult compute_plan(const Params& p, long long* red, int n
   long long carry = 0;
   for (int base = 0; base < S; base += nthreads) {
     int s = base + tid;
-    long long v = s < S ? stream_units(p, s) : 0;
+    long long v = s < S ? stream_units<WIN>(p, s) : 0;
     long long x = v;
     for (int o = 1; o < 32; o <<= 1) {
       long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -323,7 +344,8 @@ struct Segment {
 
 // Iterates the segments of one CTA; every thread of a warp (or block) that
 // uses it sees the same sequence.
-struct SegmentIter {
+template <bool WIN>
+struct SegmentIterOf {
   long long g, g_end;   // next unit, end of this CTA's range
   int s;                // stream holding unit g
   long long ps;         // prefix (units) of s
@@ -341,19 +363,19 @@ struct SegmentIter {
   __device__ bool next(const Params& p, Segment& seg) {
     for (;;) {
       if (g >= g_end || s >= S) return false;
-      int nu = stream_units(p, s);
+      int nu = stream_units<WIN>(p, s);
       while (g >= ps + nu) {   // skip empty / finished streams
         ps += nu;
         ++s;
         if (s >= S) return false;
-        nu = stream_units(p, s);
+        nu = stream_units<WIN>(p, s);
       }
       const long long a = g, e = ps + nu < g_end ? ps + nu : g_end;
       const long long tb = ps + p.seg_units;   // unit of tile 0
       g = e;
       if (e <= tb) continue;                   // only leading units of s: no segment
       seg.s = s;
-      seg.T = stream_tokens(p, s);
+      seg.T = stream_tokens<WIN>(p, s);
       const long long first = a > tb ? a - tb : 0;
       seg.t_begin = (int)(first * p.tile);
       const long long te = (e - tb) * p.tile;
@@ -366,6 +388,7 @@ struct SegmentIter {
     }
   }
 };
+using SegmentIter = SegmentIterOf<false>;
 
 // ---------------------------------------------------------------------------
 // Cache addressing (the one place the library maps tokens to rows)

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
         int parts = 2;   // the beginning and this continuation
         while (c + parts - 1 < p.grid && same(first[c + parts - 1], id)) ++parts;
         parts_of[c] = (short)parts;
-        const Seq s = load_seq<false>(p, id.x, false);
+        const Seq s = load_seq<false, false>(p, id.x, false);
         const int blocks = (mg.live_rows(s, id.z, 0) + 31) / 32 + (mg.live_rows(s, id.z, 1) + 31) / 32;
         items[parts <= kFew ? 0 : 1] = blocks * (D / 16);
       }
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   for (int item = blockIdx.x * kMergeWarps + warp; item < carry[0];
        item += gridDim.x * kMergeWarps) {
     Part it = part_at(0, item);
-    const Seq s = load_seq<false>(p, it.id.x, false);
+    const Seq s = load_seq<false, false>(p, it.id.x, false);
     const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
     it.X = it.row0 >= rows_a ? 1 : 0;
     if (it.X) it.row0 -= rows_a;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
   for (int item = blockIdx.x; item < carry[1]; item += gridDim.x) {
     Part it = part_at(1, item);
-    const Seq s = load_seq<false>(p, it.id.x, false);
+    const Seq s = load_seq<false, false>(p, it.id.x, false);
     const int rows_a = (mg.live_rows(s, it.id.z, 0) + 31) / 32 * 32;
     it.X = it.row0 >= rows_a ? 1 : 0;
     if (it.X) it.row0 -= rows_a;
@@ -309,11 +309,18 @@ cudaError_t launch_prefill(Prefill p, void* workspace, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   const bool bf16 = p.q_dtype == FD_BF16;
-  cudaError_t e;
-  if (wide) e = pf::launch_16bit(p, maps, stream);
-  else if (p.kv_dtype == FD_E4M3)
-    e = bf16 ? pf::launch_e4m3_bf16(p, maps, stream) : pf::launch_e4m3_f16(p, maps, stream);
-  else e = bf16 ? pf::launch_i8_bf16(p, maps, stream) : pf::launch_i8_f16(p, maps, stream);
+  // [window][format]
+  static pf::Launch* const launch[2][5] = {
+      {pf::launch_plain_16bit, pf::launch_plain_e4m3_f16, pf::launch_plain_e4m3_bf16,
+       pf::launch_plain_i8_f16, pf::launch_plain_i8_bf16},
+      {pf::launch_window_16bit, pf::launch_window_e4m3_f16, pf::launch_window_e4m3_bf16,
+       pf::launch_window_i8_f16, pf::launch_window_i8_bf16}};
+  const int format = wide ? 0 : (p.kv_dtype == FD_E4M3 ? 1 : 3) + (bf16 ? 1 : 0);
+  if (p.window) {
+    p.sink_keys = (p.sinks + pf::kTile - 1) / pf::kTile * pf::kTile;
+    p.win_align = !p.at.block_table ? 1 : p.at.page_size < pf::kTile ? p.at.page_size : pf::kTile;
+  }
+  const cudaError_t e = launch[p.window ? 1 : 0][format](p, maps, stream);
   if (e != cudaSuccess) return e;
   if (p.head_dim == 128)
     return bf16 ? pf::launch_merge<128, true>(p, stream) : pf::launch_merge<128, false>(p, stream);

@@ -109,16 +109,37 @@ struct Seq {
   long long head;                      // cost of one KV head
 };
 
-// Keys that the last token of pair m sees.
+// The last key that a token of pair m sees, plus one.
 __device__ __forceinline__ int pair_end(const Seq& s, int m) {
   const long long t = (long long)(m + 1) * s.span;
   const int e = s.ctx + (t < s.n ? (int)t : s.n);
   return e > 0 ? e : 0;
 }
 
-template <bool TOK>
-__device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
-  const long long end = pair_end(s, m);
+// With a window (WIN; position q sees key t when q - window < t <= q or t <
+// sinks) a pair's stream leaves out the middle that none of its tokens sees:
+// key x of the stream is key x of the sequence below sink_keys (the first
+// tokens, rounded up to whole tiles), and x + gap from there on.
+__device__ __forceinline__ long long window_start(const Prefill& p, const Seq& s, int m) {
+  return (long long)s.ctx + (long long)m * s.span - p.window + 1;   // of its first token
+}
+
+template <bool WIN>
+__device__ __forceinline__ int pair_gap(const Prefill& p, const Seq& s, int m) {
+  if constexpr (!WIN) return 0;
+  const long long first = window_start(p, s, m);
+  return first > 0 ? max(0, ((int)first & ~(p.win_align - 1)) - p.sink_keys) : 0;
+}
+
+// The keys that a pair's cost leaves out: at most the gap (which jumps by
+// win_align, where this grows by one a token and so can be summed).
+__device__ __forceinline__ long long skipped(const Prefill& p, const Seq& s, int m) {
+  return max(0ll, window_start(p, s, m) - p.sink_keys - (p.win_align - 1));
+}
+
+template <bool TOK, bool WIN>
+__device__ __forceinline__ long long pair_cost(const Prefill& p, const Seq& s, int m) {
+  const long long end = pair_end(s, m) - (WIN ? skipped(p, s, m) : 0ll);
   if constexpr (TOK) {
     if (s.solo && m == s.pairs - 1)
       return Cost<TOK>::kStart + (end * Cost<TOK>::kSolo + kTile - 1) / kTile;
@@ -127,18 +148,23 @@ __device__ __forceinline__ long long pair_cost(const Seq& s, int m) {
 }
 
 // Cost of pairs 0 .. m - 1 (m < pairs: all of them are full).
-template <bool TOK>
-__device__ __forceinline__ long long pairs_before(const Seq& s, int m) {
+template <bool TOK, bool WIN>
+__device__ __forceinline__ long long pairs_before(const Prefill& p, const Seq& s, int m) {
   long long c = (long long)m * Cost<TOK>::kStart;
   const int m0 = s.ctx >= 0 ? 0 : -s.ctx / s.span;   // pairs without keys
   if (m > m0) {
     const long long a = m, b = m0;
     c += (a - b) * s.ctx + (long long)s.span * ((a * (a + 1) - b * (b + 1)) / 2);
   }
+  if constexpr (WIN) {   // less skipped(i) = first + i span, i < m, where positive
+    const long long first = window_start(p, s, 0) - p.sink_keys - (p.win_align - 1);
+    const long long a = m, b = first > 0 ? 0 : -first / s.span + 1;
+    if (a > b) c -= (a - b) * first + (long long)s.span * ((a * (a - 1) - b * (b - 1)) / 2);
+  }
   return c;
 }
 
-template <bool TOK>
+template <bool TOK, bool WIN>
 __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   Seq s;
   s.b = b;
@@ -155,7 +181,9 @@ __device__ inline Seq load_seq(const Prefill& p, int b, bool report) {
   s.pairs = (int)(((unsigned)s.n + (unsigned)s.span - 1u) / (unsigned)s.span);
   if constexpr (TOK)
     s.solo = s.n > 0 && s.n - (long long)(s.pairs - 1) * s.span <= p.tile_tokens;
-  s.head = s.n > 0 ? pairs_before<TOK>(s, s.pairs - 1) + pair_cost<TOK>(s, s.pairs - 1) : 0;
+  s.head = s.n > 0 ? pairs_before<TOK, WIN>(p, s, s.pairs - 1) +
+                         pair_cost<TOK, WIN>(p, s, s.pairs - 1)
+                   : 0;
   return s;
 }
 
@@ -166,13 +194,13 @@ struct Plan {
 };
 
 // Every thread of the CTA gets the plan; `red` is 34 long longs of shared memory.
-template <bool TOK>
+template <bool TOK, bool WIN>
 __device__ inline Plan make_plan(const Prefill& p, long long* red) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int B = p.at.batch;
   long long mine = 0, v0 = 0;
   for (int b = tid; b < B; b += blockDim.x) {
-    const long long v = load_seq<TOK>(p, b, blockIdx.x == 0).head * p.num_kv_heads;
+    const long long v = load_seq<TOK, WIN>(p, b, blockIdx.x == 0).head * p.num_kv_heads;
     if (b == tid) v0 = v;
     mine += v;
   }
@@ -195,7 +223,7 @@ __device__ inline Plan make_plan(const Prefill& p, long long* red) {
   long long carry = 0;
   for (int base = 0; base < B; base += blockDim.x) {
     const int b = base + tid;
-    const long long v = b >= B ? 0 : base == 0 ? v0 : load_seq<TOK>(p, b, false).head * p.num_kv_heads;
+    const long long v = b >= B ? 0 : base == 0 ? v0 : load_seq<TOK, WIN>(p, b, false).head * p.num_kv_heads;
     long long x = v;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -226,7 +254,8 @@ __device__ inline Plan make_plan(const Prefill& p, long long* red) {
 struct Seg {
   int b, q0, n, ctx, h, m;   // sequence (first packed token, tokens, cached before), KV head, pair
   int tb, te;                // tiles [tb, te) of the pair's stream
-  int end;                   // keys of the stream
+  int end;                   // the last key of the stream, plus one
+  int gap;                   // (WIN) keys left out behind sink_keys
   int nt[2];                 // tiles of query tile A, B in the stream (0: no rows or no keys)
   bool solo;                 // no rows in B: its softmax takes A's odd tiles (see below)
   bool complete;             // the whole stream
@@ -247,7 +276,7 @@ static __device__ __forceinline__ int next_owner(const int32_t* start, int batch
 }
 
 // The segments of this CTA, in order; every role walks its own copy.
-template <bool TOK>
+template <bool TOK, bool WIN>
 struct Walk {
   long long g, g_end, ps;
   Seq s;
@@ -258,25 +287,26 @@ struct Walk {
     g_end = min(g + pl.per_cta, pl.total);
     ps = g_end;
     if (g >= pl.total || pl.b >= p.at.batch) return;
-    s = load_seq<TOK>(p, pl.b, false);
+    s = load_seq<TOK, WIN>(p, pl.b, false);
     const long long off = g - pl.first;
     h = (int)(off / s.head);
     const long long r = off - h * s.head;
     int lo = 0, hi = s.pairs;   // the last pair that begins at or before r
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pairs_before<TOK>(s, mid) <= r) lo = mid;
+      if (pairs_before<TOK, WIN>(p, s, mid) <= r) lo = mid;
       else hi = mid;
     }
     m = lo;
-    ps = pl.first + h * s.head + pairs_before<TOK>(s, m);
+    ps = pl.first + h * s.head + pairs_before<TOK, WIN>(p, s, m);
   }
 
   __device__ __forceinline__ bool next(const Prefill& p, Seg& o) {
     while (ps < g_end) {
       const int end = pair_end(s, m);
-      const long long cost = pair_cost<TOK>(s, m);
-      const int n = (end + kTile - 1) / kTile;
+      const long long cost = pair_cost<TOK, WIN>(p, s, m);
+      const int gap = pair_gap<WIN>(p, s, m);
+      const int n = (end - gap + kTile - 1) / kTile;
       const long long a = g > ps ? g : ps, e = ps + cost < g_end ? ps + cost : g_end;
       // tile i stands at ps + the start + i times its cost and belongs to the
       // range that holds this point
@@ -301,9 +331,10 @@ struct Walk {
         o.tb = tb;
         o.te = te;
         o.end = end;
+        o.gap = gap;
         const int half = s.span >> 1;
         const int ea = s.ctx + (int)min((long long)s.n, (long long)m * s.span + half);
-        o.nt[0] = ea > 0 ? (ea + kTile - 1) / kTile : 0;
+        o.nt[0] = ea > 0 ? (ea - gap + kTile - 1) / kTile : 0;
         o.solo = (long long)m * s.span + half >= s.n;
         o.nt[1] = o.solo ? 0 : n;
         o.complete = tb == 0 && te == n;
@@ -319,7 +350,7 @@ struct Walk {
             do {
               b = next_owner(p.q_start, p.at.batch, b);
               if (b >= p.at.batch) break;
-              s = load_seq<TOK>(p, b, false);
+              s = load_seq<TOK, WIN>(p, b, false);
             } while (s.n == 0);
           }
         }
@@ -335,6 +366,49 @@ __device__ __forceinline__ int first_unseen(const Seg& s, int span) {
   const long long t = (long long)s.ctx + (long long)s.m * span + 1;
   return t > 0 ? (int)t : 0;
 }
+
+// What the rows of a segment's pair see of its tiles.  Without a window: all
+// rows see the keys below `unseen`, and none those behind the stream's end.
+template <bool WIN>
+struct Sight {
+  int unseen;
+  // with a window: keys [sinks, any) are hidden from some row, [sinks, all) from all
+  int sinks, sink_keys, any, all;
+  __device__ __forceinline__ void init(const Prefill& p, const Seg& s) {
+    const int span = 2 * p.tile_tokens;
+    unseen = first_unseen(s, span);
+    if constexpr (WIN) {
+      sinks = p.sinks;
+      sink_keys = p.sink_keys;
+      const long long first = (long long)s.m * span;
+      const long long last = min((long long)s.n, first + span) - 1;
+      all = (int)max(0ll, s.ctx + first - p.window + 1);
+      any = (int)max(0ll, s.ctx + last - p.window + 1);
+    }
+  }
+  // first key of tile j, and its keys that belong to the stream
+  __device__ __forceinline__ int key(const Seg& s, int j) const {
+    const int x = j * kTile;
+    return WIN && x >= sink_keys ? x + s.gap : x;
+  }
+  __device__ __forceinline__ int valid(const Seg& s, int j) const {
+    if (WIN && s.gap > 0 && j * kTile < sink_keys) return min(kTile, sinks - j * kTile);
+    return min(kTile, s.end - key(s, j));
+  }
+  // keys that some row, or no row, sees (of those that belong to the stream)
+  __device__ __forceinline__ bool partly(int k) const {
+    return k >= unseen || (WIN && k >= sinks && k < any);
+  }
+  __device__ __forceinline__ bool hidden(int k) const { return WIN && k >= sinks && k < all; }
+  __device__ __forceinline__ bool hidden(int k, int n) const {
+    return WIN && k >= sinks && k + n <= all;
+  }
+  // a tile with a key that some row does not see
+  __device__ __forceinline__ bool fix(const Seg& s, int j) const {
+    const int k = key(s, j);
+    return k + kTile > unseen || (WIN && max(k, sinks) < min(k + kTile, any));
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Shape and shared memory
@@ -536,7 +610,7 @@ __device__ __forceinline__ bool wait_swaps(Control& c, const Prefill& p, int wan
   return true;
 }
 
-__device__ __forceinline__ int tile_info(const Seg& s, int j, int unseen, bool bad) {
+__device__ __forceinline__ int tile_info(const Seg& s, int j, bool fix, bool bad) {
   int w = bad ? kInfoBad : 0;
   if (s.solo) {
     const int x = (j - s.tb) & 1;
@@ -548,7 +622,7 @@ __device__ __forceinline__ int tile_info(const Seg& s, int j, int unseen, bool b
   }
   if (j == s.tb) w |= kInfoStart;
   if (j + 1 == s.te) w |= kInfoEnd;
-  if ((j + 1) * kTile > unseen) w |= kInfoFix;
+  if (fix) w |= kInfoFix;
   return w;
 }
 
@@ -576,8 +650,8 @@ static __device__ __forceinline__ void land_copies(Control& c, const Prefill& p,
   if (late) raise_error(p.at.ws, kErrDrain, 3);
 }
 
-template <int D, int KV, bool CONV, bool TOK>
-__device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Control& c,
+template <int D, int KV, bool CONV, bool TOK, bool WIN>
+__device__ __forceinline__ void producer(const Prefill& p, Walk<TOK, WIN> walk, Control& c,
                                          uint8_t* base, const CUtensorMap* tmq,
                                          const CUtensorMap* tmk, const CUtensorMap* tmv) {
   using SH = Shape<D, KV, CONV>;
@@ -624,11 +698,13 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
     if (swaps_in(seg)) ++swaps;
     if (!tiles || stop) continue;
     const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
-    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    Sight<WIN> sight;
+    sight.init(p, seg);
     int win_lo = 0, win_hi = 0;
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
-      const int t0 = j * kTile;
-      const int valid = min(kTile, seg.end - t0);
+      const int t0 = sight.key(seg, j);
+      const int valid = sight.valid(seg, j);
+      const bool fix = sight.fix(seg, j);
       const int nbox = (valid + box_rows - 1) / box_rows;
       if (p.at.block_table) {
         const int lo = t0 >> p.at.page_shift, hi = ((t0 + valid - 1) >> p.at.page_shift) + 1;
@@ -645,12 +721,15 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
         }
       }
       // one box per lane (at most 16): its row, and whether it lies in the cache
+      // (one that no row sees is not loaded: its page may be gone)
       long long row = 0;
-      bool ok = true;
+      bool ok = true, loads = lane < nbox;
       if (lane < nbox) {
         const int t = t0 + lane * box_rows;
         const int nval = min(box_rows, valid - lane * box_rows);
-        if (p.at.block_table) {
+        if (sight.hidden(t, nval)) {
+          loads = false;
+        } else if (p.at.block_table) {
           const int page = c.pages[(t >> p.at.page_shift) - win_lo];
           row = ((long long)page << p.at.page_shift) + (t & (p.at.page_size - 1));
           ok = page >= 0 && row + nval <= p.at.kv_rows;
@@ -662,6 +741,7 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
         }
       }
       const bool bad = __any_sync(0xffffffffu, !ok);
+      const int boxes = WIN ? __popc(__ballot_sync(0xffffffffu, loads)) : nbox;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int e = 2 * n + kv, slot = e % NS;
@@ -677,17 +757,17 @@ __device__ __forceinline__ void producer(const Prefill& p, Walk<TOK> walk, Contr
           for (uint32_t o = lane * 16; o < kSlot; o += 512)
             *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
           fence_async_smem();
-          if (lane == 0 && kv == 0) c.info[n & 7] = tile_info(seg, j, unseen, true);
+          if (lane == 0 && kv == 0) c.info[n & 7] = tile_info(seg, j, fix, true);
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]);
           continue;
         }
         if (lane == 0) {
-          if (kv == 0) c.info[n & 7] = tile_info(seg, j, unseen, false);
-          mbar_arrive_tx(&full[slot], (uint32_t)nbox * box_rows * TC::kRowBytes * TC::kBlocks);
+          if (kv == 0) c.info[n & 7] = tile_info(seg, j, fix, false);
+          mbar_arrive_tx(&full[slot], (uint32_t)boxes * box_rows * TC::kRowBytes * TC::kBlocks);
         }
         __syncwarp();
-        if (lane < nbox) {
+        if (loads) {
 #pragma unroll
           for (int d = 0; d < TC::kBlocks; ++d)
             mma::tma_load_3d_hint(dst + d * (kTile * TC::kRowBytes) +
@@ -948,8 +1028,8 @@ struct Mma {
 // ---------------------------------------------------------------------------
 // Repair of V tiles in the ring (16-bit caches by TMA)
 // ---------------------------------------------------------------------------
-template <int D, bool BF16>
-__device__ __forceinline__ void fixers(const Prefill& p, Walk<false> walk, Control& c,
+template <int D, bool BF16, bool WIN>
+__device__ __forceinline__ void fixers(const Prefill& p, Walk<false, WIN> walk, Control& c,
                                        uint8_t* base) {
   using SH = Shape<D, 0, false>;
   constexpr int NS = SH::kSlots;
@@ -958,15 +1038,17 @@ __device__ __forceinline__ void fixers(const Prefill& p, Walk<false> walk, Contr
   int n = 0, fixes = 0, sn = 0;
   // (sn counts the segments that have tiles)
   for (; walk.next(p, seg); sn += seg.te > seg.tb) {
-    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    Sight<WIN> sight;
+    sight.init(p, seg);
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int e = 2 * n + kv, slot = e % NS;
         if (!wait_warp(c, p, &c.full[slot], (uint32_t)((e / NS) & 1), 20)) return;
-        if (kv == 1 && (j + 1) * kTile > unseen) {
-          const int valid = min(kTile, seg.end - j * kTile);
-          const int from = max(0, unseen - j * kTile);   // rows before it are seen by all
+        if (kv == 1 && sight.fix(seg, j)) {
+          const int k0 = sight.key(seg, j), valid = sight.valid(seg, j);
+          // rows before it are seen by all (with a window it is asked of each)
+          const int from = WIN ? 0 : max(0, sight.unseen - k0);
           uint8_t* v = base + SH::kOffSlot + (size_t)slot * SH::kSlot;
           bool found = false;
           const int items = (kTile - from) * 8;
@@ -975,8 +1057,9 @@ __device__ __forceinline__ void fixers(const Prefill& p, Walk<false> walk, Contr
 #pragma unroll 2
             for (int i = ft; i < items; i += 64) {
               const int r = from + (i >> 3);
+              if (WIN && r < valid && !sight.partly(k0 + r)) continue;
               uint4* at = reinterpret_cast<uint4*>(v + d * (kTile * 128) + r * 128 + (i & 7) * 16);
-              if (r >= valid) {
+              if (r >= valid || sight.hidden(k0 + r)) {
                 *at = make_uint4(0, 0, 0, 0);
               } else {
                 uint4 w = *at;
@@ -1030,8 +1113,8 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 // ---------------------------------------------------------------------------
 // Converter warps: thread = key of the tile
 // ---------------------------------------------------------------------------
-template <int D, int KV, bool BF16, bool TOK>
-__device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Control& c,
+template <int D, int KV, bool BF16, bool TOK, bool WIN>
+__device__ __forceinline__ void converters(const Prefill& p, Walk<TOK, WIN> walk, Control& c,
                                            uint8_t* base) {
   using SH = Shape<D, KV, true>;
   constexpr int NS = SH::kSlots;
@@ -1042,9 +1125,11 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
   Seg seg;
   int n = 0, sn = 0;
   for (; walk.next(p, seg); sn += seg.te > seg.tb) {
-    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    Sight<WIN> sight;
+    sight.init(p, seg);
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
-      const int valid = min(kTile, seg.end - j * kTile);
+      const int k0 = sight.key(seg, j), valid = sight.valid(seg, j);
+      const bool fix = sight.fix(seg, j);
       long long row = -1;
       int bad = 0;
       if (p.gather) {
@@ -1052,10 +1137,10 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
         // at all 128 rows and so comes to the same answer
         bool wrong = false;
         for (int k = lane; k < valid; k += 32)
-          wrong |= placed_row(p.at, seg.b, j * kTile + k) < 0;
+          wrong |= !sight.hidden(k0 + k) && placed_row(p.at, seg.b, k0 + k) < 0;
         bad = __any_sync(0xffffffffu, wrong) ? 1 : 0;
-        if (t < valid) row = placed_row(p.at, seg.b, j * kTile + t);
-        if (t == 0) c.info[n & 7] = tile_info(seg, j, unseen, bad != 0);
+        if (t < valid && !sight.hidden(k0 + t)) row = placed_row(p.at, seg.b, k0 + t);
+        if (t == 0) c.info[n & 7] = tile_info(seg, j, fix, bad != 0);
       }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
@@ -1079,11 +1164,11 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
           }
         }
         // V rows that some query row does not see (see the file comment)
-        if (kv == 1 && (j + 1) * kTile > unseen && j * kTile + t >= unseen) {
+        if (kv == 1 && fix && (sight.partly(k0 + t) || (WIN && t >= valid))) {
           bool found = false;
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
-            if (t >= valid) {
+            if (t >= valid || sight.hidden(k0 + t)) {
               w[i] = make_uint4(0, 0, 0, 0);
             } else if constexpr (KV == 0) {
               found |= drop_nonfinite<BF16>(w[i].x);
@@ -1128,12 +1213,14 @@ __device__ __forceinline__ void converters(const Prefill& p, Walk<TOK> walk, Con
   if (lane == 0) mbar_arrive(&c.full[slot]);
 }
 
-// Does tile j of sequence b's stream, which ends at key `end`, hold a row
-// outside the cache?  By one thread; off every fast path.
-static __device__ __noinline__ bool tile_absent(const Prefill& p, int b, int end, int j) {
-  end = min(end - j * kTile, kTile);
-  for (int k = 0; k < end; ++k)
-    if (placed_row(p.at, b, j * kTile + k) < 0) return true;
+// Does tile j of a segment hold a row outside the cache (that some row sees)?
+// By one thread; off every fast path.
+template <bool WIN>
+static __device__ __noinline__ bool tile_absent(const Prefill& p, const Seg& s,
+                                                const Sight<WIN>& sight, int j) {
+  const int k0 = sight.key(s, j), end = k0 + sight.valid(s, j);
+  for (int k = k0; k < end; ++k)
+    if (!sight.hidden(k) && placed_row(p.at, s.b, k) < 0) return true;
   return false;
 }
 
@@ -1146,8 +1233,8 @@ static __device__ __noinline__ bool tile_absent(const Prefill& p, int b, int end
 // without scales per token), full tiles 0.2 more.  Widening is not a work for
 // these two warps: with six warps at it the products wait for shared memory's
 // port (e4m3 under f16 at three quarters of the rate).
-template <int D, int KV>
-__device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, Control& c,
+template <int D, int KV, bool WIN>
+__device__ __forceinline__ void token_scales(const Prefill& p, Walk<true, WIN> walk, Control& c,
                                              float* scales) {
   using SH = Shape<D, KV, true>;
   using SR = ScaleRing<D, KV>;
@@ -1166,14 +1253,16 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
   Seg seg;
   int n = 0, sn = 0;
   for (; walk.next(p, seg); sn += seg.te > seg.tb) {
-    const int unseen = first_unseen(seg, 2 * p.tile_tokens);
+    Sight<WIN> sight;
+    sight.init(p, seg);
     const long long start = p.at.block_table ? 0 : (long long)__ldg(p.at.kv_start + seg.b);
     float ks[2], vs[2];
     int page[2];
     auto load = [&](int j) {   // of tile j, whose pages are at hand
+      const int k0 = sight.key(seg, j), next = WIN ? sight.key(seg, j + 1) : k0 + kTile;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = j * kTile + t + 64 * i;
+        const int k = k0 + t + 64 * i;
         const long long row = p.at.block_table
                                   ? ((long long)page[i] << p.at.page_shift) + (k & (p.at.page_size - 1))
                                   : start + k;
@@ -1182,11 +1271,12 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
           ks[i] = __ldg(p.k_scales + row * p.num_kv_heads + seg.h);
           vs[i] = __ldg(p.v_scales + row * p.num_kv_heads + seg.h);
         }
-        page[i] = page_of(seg, j + 1, k + kTile);
+        page[i] = page_of(seg, j + 1, next + t + 64 * i);
       }
     };
 #pragma unroll
-    for (int i = 0; i < 2; ++i) page[i] = page_of(seg, seg.tb, seg.tb * kTile + t + 64 * i);
+    for (int i = 0; i < 2; ++i)
+      page[i] = page_of(seg, seg.tb, sight.key(seg, seg.tb) + t + 64 * i);
     if (seg.te > seg.tb) load(seg.tb);
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
       float k[2], v[2];
@@ -1196,10 +1286,10 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
         v[i] = vs[i];
         // the V scale of a key that some row does not see: as V's elements
         if (!isfinite(v[i])) {
-          if (j * kTile + t + 64 * i >= unseen) {
+          if (sight.partly(sight.key(seg, j) + t + 64 * i)) {
             v[i] = 0.f;
             *(volatile int*)&c.nf[sn & 7] = sn + 1;
-          } else if (tile_absent(p, seg.b, seg.end, j)) {   // (its P is zero: 0 * NaN would be seen)
+          } else if (tile_absent<WIN>(p, seg, sight, j)) {   // (its P is zero: 0 * NaN would be seen)
             v[i] = 0.f;
           }
         }
@@ -1227,8 +1317,11 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true> walk, 
 // ---------------------------------------------------------------------------
 // Elements of V that are not finite, in the keys [lo, hi) of a sequence: added
 // to this row's 32 dims from d0 (see the file comment; off every fast path).
-template <int D, int KV, bool BF16, bool TOK>
-__device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int lo, int hi,
+// (with a window: those that the row, whose window starts at `first`, sees and
+// another row does not)
+template <int D, int KV, bool BF16, bool TOK, bool WIN>
+__device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg,
+                                           const Sight<WIN>& sight, int lo, int hi, int first,
                                            int d0, float* o) {
   float vsc = 1.f;   // (a cut stream's merge brings v_scale)
   if (seg.complete) {
@@ -1236,6 +1329,7 @@ __device__ __noinline__ void add_nonfinite(const Prefill& p, const Seg& seg, int
     if (KV != 0 && p.scale_kind == FD_SCALE_HEAD) vsc *= __ldg(p.v_scales + seg.h);
   }
   for (int t = lo; t < hi; ++t) {
+    if (WIN && ((t >= sight.sinks && t < first) || !sight.partly(t))) continue;
     const long long row = placed_row(p.at, seg.b, t);
     if (row < 0) continue;
     const long long at = (row * p.num_kv_heads + seg.h) * D + d0;
@@ -1270,7 +1364,7 @@ __device__ __forceinline__ void store32(void* at, const uint4& a, const uint4& b
   }
 }
 
-template <int D, int KV, bool CONV, bool BF16, bool TOK>
+template <int D, int KV, bool CONV, bool BF16, bool TOK, bool WIN>
 struct Softmax {
   using SH = Shape<D, KV, CONV>;
   using SR = ScaleRing<D, KV>;
@@ -1317,14 +1411,15 @@ struct Softmax {
     }
   }
   // off the straight path: the sign of the scale, and -inf for keys that the
-  // row does not see (`left` of the 32)
-  __device__ __forceinline__ void exclude(float (&x)[32], int left) const {
+  // row does not see (from `left` of the 32 on, and [hl, hh) with a window)
+  __device__ __forceinline__ void exclude(float (&x)[32], int left, int hl, int hh) const {
     if (!TOK && sc <= 0.f) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = sc == 0.f ? 0.f : -x[i];
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = i < left ? x[i] : -INFINITY;
+    for (int i = 0; i < 32; ++i)
+      x[i] = i < left && !(WIN && i >= hl && i < hh) ? x[i] : -INFINITY;
   }
   __device__ __forceinline__ static void row_max(const float (&x)[32], float (&mx)[4]) {
 #pragma unroll
@@ -1384,6 +1479,14 @@ struct Softmax {
     return left > 0 ? fmaxf(b, i == 0 ? x : i == 1 ? y : i == 2 ? z : w) : 0.f;
   }
 
+  // The same with keys [hl, hh) hidden, key by key (the window's edge tiles).
+  static __device__ __noinline__ float seen_scale(const float* vs, int left, int hl, int hh) {
+    float m = 0.f;
+    for (int i = 0; i < kTile; ++i)
+      if (i < left && !(i >= hl && i < hh)) m = fmaxf(m, fabsf(vs[i]));
+    return m;
+  }
+
   // P is in tensor memory up to here: one of this warp's two arrivals a tile.
   __device__ __forceinline__ void publish(uint64_t* bar) const {
     tmem_wait_st();
@@ -1393,10 +1496,10 @@ struct Softmax {
   }
 
   // One tile (tile jn of the CTA), of whose 128 keys the row sees the first
-  // `left`.  False after a timeout.  The scores are read from tensor memory
+  // `left`, less [hl, hh) with a window.  False after a timeout.  The scores are read from tensor memory
   // twice, 32 at a time: a thread that kept all 128 would spill.
-  __device__ __forceinline__ bool tile(int jn, int left, bool mine) {
-    const bool whole = __all_sync(0xffffffffu, left == kTile);
+  __device__ __forceinline__ bool tile(int jn, int left, int hl, int hh, bool mine) {
+    const bool whole = __all_sync(0xffffffffu, left == kTile && !(WIN && hl < min(hh, kTile)));
     const float* ks = scales + SR::key(jn);   // written before the tile's S was issued
     const float* vs = scales + SR::val(jn);
     // |sc| is factored out of the scores (a negative scale: the maximum of -s
@@ -1416,7 +1519,7 @@ struct Softmax {
         tmem_wait_ld();
         arrived(x);
         if constexpr (TOK) key_scales(x, ks + 32 * k);
-        if (!TOK || !whole) exclude(x, left - 32 * k);
+        if (!TOK || !whole) exclude(x, left - 32 * k, hl - 32 * k, hh - 32 * k);
         tmem_st32<128>(tS + 32 * k, x);
         if constexpr (TOK) row_max(x, mx);
       }
@@ -1458,6 +1561,8 @@ struct Softmax {
           for (int i = 0; i < 4; ++i) vm = fmaxf(vm, fabsf(vs[lane + 32 * i]));
 #pragma unroll
           for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        } else if (WIN) {
+          vm = seen_scale(vs, left, hl, hh);
         } else {
           vm = seen_scale(vs, left);
         }
@@ -1516,7 +1621,7 @@ struct Softmax {
     return reinterpret_cast<float4*>(base + SH::kQTile) + d4 * kRowsTile + r;
   }
 
-  __device__ void run(Walk<TOK> walk) {
+  __device__ void run(Walk<TOK, WIN> walk) {
     const int rtok = r / p.group, rhead = r - rtok * p.group;
     Seg seg;
     int n = 0, done = 0, segs = 0, sn = 0;
@@ -1532,6 +1637,11 @@ struct Softmax {
       const bool warp_live = 32 * w4 < live_rows;
       // keys this row sees; a row of nobody never restricts its warp
       const int lim = mine ? max(0, seg.ctx + tok0 + rtok + 1) : 0x7fffffff;
+      // first key of its window (in 64 bits: a window may be longer than any cache)
+      const int wfirst =
+          WIN && mine ? (int)max(0ll, (long long)seg.ctx + tok0 + rtok - p.window + 1) : 0;
+      Sight<WIN> sight;
+      sight.init(p, seg);
       const int te = min(seg.te, qt ? seg.nt[1] : seg.nt[0]);
       const int first = seg.tb + (seg.solo ? X : 0), step = seg.solo ? 2 : 1;
       float vsc = p.v_scale;
@@ -1552,7 +1662,10 @@ struct Softmax {
         tc_fence_after();
         if (warp_live) {
           const bool bad = (*(volatile int*)&c.info[jn & 7] & kInfoBad) != 0;
-          if (!tile(jn, bad ? 0 : max(0, min(kTile, lim - j * kTile)), mine)) {
+          const int k0 = sight.key(seg, j);
+          const int left = WIN ? min(sight.valid(seg, j), lim - k0) : min(kTile, lim - k0);
+          if (!tile(jn, bad ? 0 : max(0, left), WIN ? max(0, p.sinks - k0) : 0, wfirst - k0,
+                    mine)) {
             dead = true;
             break;
           }
@@ -1674,14 +1787,16 @@ struct Softmax {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = o[i];
-            const int lo = max(first_unseen(seg, 2 * p.tile_tokens), seg.tb * kTile);
-            const int hi = min(lim, seg.te * kTile);
             // tile by tile: an absent one has no elements
+            const int lo = WIN ? 0 : sight.unseen;
 #pragma unroll 1
-            for (int j = lo / kTile; j * kTile < hi; ++j)
-              if (!tile_absent(p, seg.b, seg.end, j))
-                add_nonfinite<D, KV, BF16, TOK>(p, seg, max(lo, j * kTile),
-                                                min(hi, (j + 1) * kTile), c0, x);
+            for (int j = max(seg.tb, lo / kTile); j < seg.te; ++j) {
+              const int k0 = sight.key(seg, j);
+              if (k0 >= lim || !sight.fix(seg, j) || tile_absent<WIN>(p, seg, sight, j)) continue;
+              add_nonfinite<D, KV, BF16, TOK, WIN>(
+                  p, seg, sight, max(lo, k0),
+                  min(lim, k0 + (WIN ? sight.valid(seg, j) : kTile)), wfirst, c0, x);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = x[i];
           }
@@ -1745,7 +1860,7 @@ struct Softmax {
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
-template <int D, int KV, bool CONV, bool BF16, bool TOK>
+template <int D, int KV, bool CONV, bool BF16, bool TOK, bool WIN>
 __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
     prefill_kernel(const __grid_constant__ Prefill p, const __grid_constant__ CUtensorMap tmq,
                    const __grid_constant__ CUtensorMap tmk,
@@ -1804,9 +1919,9 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
     }
   }
   tc_fence_before();
-  const Plan plan = make_plan<TOK>(p, reinterpret_cast<long long*>(base));   // (barriers)
+  const Plan plan = make_plan<TOK, WIN>(p, reinterpret_cast<long long*>(base));   // (barriers)
   tc_fence_after();
-  Walk<TOK> walk;   // every role walks its own copy
+  Walk<TOK, WIN> walk;   // every role walks its own copy
   walk.init(p, plan);
   const uint32_t tbase = c.tmem_base;
   allow_dependent_launch();
@@ -1814,22 +1929,22 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   if (warp < 8) {
     const int X = warp >> 2, w4 = warp & 3, lane = threadIdx.x & 31;
     const uint32_t tl = tbase + ((uint32_t)(32 * w4) << 16);
-    Softmax<D, KV, CONV, BF16, TOK> sm{p, c, base, scales, X, lane, w4, 32 * w4 + lane,
+    Softmax<D, KV, CONV, BF16, TOK, WIN> sm{p, c, base, scales, X, lane, w4, 32 * w4 + lane,
                                        tl + X * kTile, tl + (2 + X) * kTile};
     sm.run(walk);
   } else if (warp < kConvWarp0) {
     if (warp == kProducerWarp) {
-      producer<D, KV, CONV, TOK>(p, walk, c, base, &tmq, &tmk, &tmv);
+      producer<D, KV, CONV, TOK, WIN>(p, walk, c, base, &tmq, &tmk, &tmv);
     } else if (warp == kMmaWarp) {
       Mma<D, KV, CONV, BF16> mm{p, c, tbase, smem_u32(base), elect_one(), {0, 0}, {0, 0}, 0};
       mm.run();
     } else if constexpr (!CONV) {
-      fixers<D, BF16>(p, walk, c, base);
+      fixers<D, BF16, WIN>(p, walk, c, base);
     } else if constexpr (TOK) {
-      token_scales<D, KV>(p, walk, c, scales);
+      token_scales<D, KV, WIN>(p, walk, c, scales);
     }
   } else if constexpr (CONV) {
-    converters<D, KV, BF16, TOK>(p, walk, c, base);
+    converters<D, KV, BF16, TOK, WIN>(p, walk, c, base);
   }
   tc_fence_before();
   __syncthreads();
@@ -1840,11 +1955,11 @@ __global__ void __launch_bounds__(Shape<D, KV, CONV>::kThreads, 1)
   }
 }
 
-template <int D, int KV, bool CONV, bool BF16, bool TOK>
+template <int D, int KV, bool CONV, bool BF16, bool TOK, bool WIN>
 cudaError_t launch_one(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
   constexpr uint32_t smem = smem_bytes<D, KV, CONV, TOK>();
   static std::atomic<unsigned long long> limit_set{0};
-  const auto kern = prefill_kernel<D, KV, CONV, BF16, TOK>;
+  const auto kern = prefill_kernel<D, KV, CONV, BF16, TOK, WIN>;
   const cudaError_t e = ensure_smem_limit(kern, (int)smem, &limit_set);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)p.grid, Shape<D, KV, CONV>::kThreads, smem, stream>>>(p, maps[0], maps[1],
@@ -1853,25 +1968,38 @@ cudaError_t launch_one(const Prefill& p, const CUtensorMap* maps, cudaStream_t s
 }
 
 // 16-bit caches: by TMA, or gathered row by row.
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN>
 cudaError_t launch_16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
-  return p.gather ? launch_one<D, 0, true, BF16, false>(p, maps, stream)
-                  : launch_one<D, 0, false, BF16, false>(p, maps, stream);
+  return p.gather ? launch_one<D, 0, true, BF16, false, WIN>(p, maps, stream)
+                  : launch_one<D, 0, false, BF16, false, WIN>(p, maps, stream);
 }
 
 // 8-bit caches: with per-token scales or not.
-template <int D, int KV, bool BF16>
+template <int KV, bool BF16, bool WIN>
 cudaError_t launch_8(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
-  return p.scale_kind == FD_SCALE_TOKEN ? launch_one<D, KV, true, BF16, true>(p, maps, stream)
-                                        : launch_one<D, KV, true, BF16, false>(p, maps, stream);
+  const bool tok = p.scale_kind == FD_SCALE_TOKEN;
+  if (p.head_dim == 128)
+    return tok ? launch_one<128, KV, true, BF16, true, WIN>(p, maps, stream)
+               : launch_one<128, KV, true, BF16, false, WIN>(p, maps, stream);
+  return tok ? launch_one<64, KV, true, BF16, true, WIN>(p, maps, stream)
+             : launch_one<64, KV, true, BF16, false, WIN>(p, maps, stream);
 }
 
-// One per translation unit.
-cudaError_t launch_16bit(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
-cudaError_t launch_e4m3_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
-cudaError_t launch_e4m3_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
-cudaError_t launch_i8_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
-cudaError_t launch_i8_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+// One per translation unit; WIN: with a window.
+template <bool WIN>
+cudaError_t launch_16bit(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  if (p.q_dtype == FD_BF16)
+    return p.head_dim == 128 ? launch_16<128, true, WIN>(p, maps, stream)
+                             : launch_16<64, true, WIN>(p, maps, stream);
+  return p.head_dim == 128 ? launch_16<128, false, WIN>(p, maps, stream)
+                           : launch_16<64, false, WIN>(p, maps, stream);
+}
+
+using Launch = cudaError_t(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream);
+Launch launch_plain_16bit, launch_plain_e4m3_f16, launch_plain_e4m3_bf16, launch_plain_i8_f16,
+    launch_plain_i8_bf16;
+Launch launch_window_16bit, launch_window_e4m3_f16, launch_window_e4m3_bf16, launch_window_i8_f16,
+    launch_window_i8_bf16;
 
 }  // namespace pf
 }  // namespace fd

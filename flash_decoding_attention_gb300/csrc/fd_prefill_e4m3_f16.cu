@@ -5,9 +5,8 @@
 namespace fd {
 namespace pf {
 
-cudaError_t launch_e4m3_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
-  return p.head_dim == 128 ? launch_8<128, 1, false>(p, maps, stream)
-                           : launch_8<64, 1, false>(p, maps, stream);
+cudaError_t launch_plain_e4m3_f16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  return launch_8<1, false, false>(p, maps, stream);
 }
 
 }  // namespace pf

@@ -5,9 +5,8 @@
 namespace fd {
 namespace pf {
 
-cudaError_t launch_i8_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
-  return p.head_dim == 128 ? launch_8<128, 2, true>(p, maps, stream)
-                           : launch_8<64, 2, true>(p, maps, stream);
+cudaError_t launch_plain_i8_bf16(const Prefill& p, const CUtensorMap* maps, cudaStream_t stream) {
+  return launch_8<2, true, false>(p, maps, stream);
 }
 
 }  // namespace pf

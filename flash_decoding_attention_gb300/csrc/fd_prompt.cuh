@@ -115,6 +115,10 @@ struct Prefill {
   int scale_kind;
   const float *k_scales, *v_scales;
   int q_dtype, kv_dtype;
+  // Sliding window (0: none): position q sees keys t with q - window < t <= q
+  // and the first `sinks` ones.  sink_keys: sinks rounded up to whole tiles;
+  // win_align: window tiles start at a multiple of it (a box's rows; 1: anywhere)
+  int window, sinks, sink_keys, win_align;
   unsigned long long wait_ns;
   int starve;
   int grid;            // CTAs of the attention kernel

@@ -265,17 +265,17 @@ size_t fd_prefill_workspace_bytes(int head_dim) {
   return sms > 0 ? prefill_layout(head_dim, sms).total : 0;
 }
 
-fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_cache,
-                               const void* v_cache, const int32_t* kv_start_idx,
-                               const int32_t* block_table, int block_table_stride,
-                               const int32_t* q_start, const int32_t* seq_len,
-                               int64_t num_tokens, int64_t kv_rows, int batch, int num_q_heads,
-                               int num_kv_heads, int head_dim, int page_size,
-                               float softmax_scale, float k_scale, float v_scale,
-                               fd_scale_kind scale_kind, const float* k_scales,
-                               const float* v_scales, fd_dtype q_dtype, fd_dtype kv_dtype,
-                               void* out, float* lse, void* workspace, size_t workspace_bytes,
-                               fd_stream_t stream) {
+static fd_status prefill_impl(const void* q, int64_t q_stride, const void* k_cache,
+                              const void* v_cache, const int32_t* kv_start_idx,
+                              const int32_t* block_table, int block_table_stride,
+                              const int32_t* q_start, const int32_t* seq_len,
+                              int64_t num_tokens, int64_t kv_rows, int batch, int num_q_heads,
+                              int num_kv_heads, int head_dim, int page_size,
+                              float softmax_scale, float k_scale, float v_scale,
+                              fd_scale_kind scale_kind, const float* k_scales,
+                              const float* v_scales, fd_dtype q_dtype, fd_dtype kv_dtype,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              fd_stream_t stream, int window, int sinks) {
   const fd_status chk = check_placement(
       k_cache, v_cache, kv_start_idx, block_table, block_table_stride, q_start, num_tokens,
       kv_rows, batch, num_kv_heads, head_dim, page_size, scale_kind, k_scales, v_scales, q_dtype,
@@ -321,12 +321,50 @@ fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_ca
   p.v_scales = v_scales;
   p.q_dtype = q_dtype;
   p.kv_dtype = kv_dtype;
+  p.window = window;
+  // more first tokens than any sequence has are all of them
+  p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   p.wait_ns = wait_limit_ns();
   p.starve = starve_switch();
   p.grid = sms;
   return launch_prefill(p, workspace, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FD_OK
              : FD_ERR_CUDA;
+}
+
+fd_status fd_prefill_attention(const void* q, int64_t q_stride, const void* k_cache,
+                               const void* v_cache, const int32_t* kv_start_idx,
+                               const int32_t* block_table, int block_table_stride,
+                               const int32_t* q_start, const int32_t* seq_len,
+                               int64_t num_tokens, int64_t kv_rows, int batch, int num_q_heads,
+                               int num_kv_heads, int head_dim, int page_size, float softmax_scale,
+                               float k_scale, float v_scale, fd_scale_kind scale_kind,
+                               const float* k_scales, const float* v_scales, fd_dtype q_dtype,
+                               fd_dtype kv_dtype, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, fd_stream_t stream) {
+  return prefill_impl(q, q_stride, k_cache, v_cache, kv_start_idx, block_table, block_table_stride,
+                      q_start, seq_len, num_tokens, kv_rows, batch, num_q_heads, num_kv_heads,
+                      head_dim, page_size, softmax_scale, k_scale, v_scale, scale_kind, k_scales,
+                      v_scales, q_dtype, kv_dtype, out, lse, workspace, workspace_bytes, stream,
+                      0, 0);
+}
+
+fd_status fd_prefill_attention_window(const void* q, int64_t q_stride, const void* k_cache,
+                                      const void* v_cache, const int32_t* kv_start_idx,
+                                      const int32_t* block_table, int block_table_stride,
+                                      const int32_t* q_start, const int32_t* seq_len,
+                                      int64_t num_tokens, int64_t kv_rows, int batch, int num_q_heads,
+                                      int num_kv_heads, int head_dim, int page_size, int window, int sinks, float softmax_scale,
+                                      float k_scale, float v_scale, fd_scale_kind scale_kind,
+                                      const float* k_scales, const float* v_scales, fd_dtype q_dtype,
+                                      fd_dtype kv_dtype, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, fd_stream_t stream) {
+  if (window < 1 || sinks < 0) return FD_ERR_INVALID_ARG;
+  return prefill_impl(q, q_stride, k_cache, v_cache, kv_start_idx, block_table, block_table_stride,
+                      q_start, seq_len, num_tokens, kv_rows, batch, num_q_heads, num_kv_heads,
+                      head_dim, page_size, softmax_scale, k_scale, v_scale, scale_kind, k_scales,
+                      v_scales, q_dtype, kv_dtype, out, lse, workspace, workspace_bytes, stream,
+                      window, sinks);
 }
 
 }  // extern "C"

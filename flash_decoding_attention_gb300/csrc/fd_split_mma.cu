@@ -264,6 +264,11 @@ cudaError_t launch_split_mma(const Params& p, cudaStream_t stream) {
       get_scale_map(p.k_scales, p.kv_rows, p.num_kv_heads, sh.hc, sh.box_rows, &maps.ks) &&
       get_scale_map(p.v_scales, p.kv_rows, p.num_kv_heads, sh.hc, sh.box_rows, &maps.vs))
     sh.scale_tma = 1;
+  if (p.window) {
+    if (p.kv_dtype == FD_E4M3) return launch_window_e4m3(p, sh, maps, stream);
+    if (p.kv_dtype == FD_I8) return launch_window_i8(p, sh, maps, stream);
+    return launch_window_16bit(p, sh, maps, stream);
+  }
   if (p.kv_dtype == FD_E4M3) return launch_e4m3(p, sh, maps, stream);
   if (p.kv_dtype == FD_I8) return launch_i8(p, sh, maps, stream);
   return launch_16bit(p, sh, maps, stream);

@@ -432,6 +432,41 @@ __device__ __forceinline__ void zero_rows_past_end(W& w0, W& w1, W& w2, W& w3, i
   if (tk + 9 >= left) w3 = W{};
 }
 
+// The same for the window kernels, where the sub-tile's tokens [hl, hh) are
+// hidden as well.
+template <typename W>
+__device__ __forceinline__ void zero_hidden_rows(W& w0, W& w1, W& w2, W& w3, int tk, int left,
+                                                 int hl, int hh) {
+  auto out = [&](int t) { return t >= left || (t >= hl && t < hh); };
+  if (out(tk)) w0 = W{};
+  if (out(tk + 1)) w1 = W{};
+  if (out(tk + 8)) w2 = W{};
+  if (out(tk + 9)) w3 = W{};
+}
+
+// A window segment's view of its sequence: stream token x stands for token
+// x + (x < sink_tokens ? 0 : gap); tokens [hide_lo, hide_hi) are hidden.
+struct WindowView {
+  int gap, hide_lo, hide_hi, sink_tokens;
+  __device__ __forceinline__ void init(const Params& p, int b) {
+    const int T = max(0, __ldg(p.seq_len + b));
+    gap = window_gap(p, T);
+    hide_lo = p.sinks;
+    hide_hi = max(p.sinks, T - p.window);
+    sink_tokens = p.sink_tokens;
+  }
+  __device__ __forceinline__ int token(int x) const { return x < sink_tokens ? x : x + gap; }
+  // valid tokens of the tile at stream token x: up to the segment's end, and
+  // in front of a gap up to the last of the first tokens
+  __device__ __forceinline__ int valid(int x, int tile, int end) const {
+    const int v = min(tile, end - x);
+    return gap > 0 && x < sink_tokens ? min(v, hide_lo - x) : v;
+  }
+  __device__ __forceinline__ bool hides(int t, int n) const {   // all of t .. t + n - 1
+    return t >= hide_lo && t + n <= hide_hi;
+  }
+};
+
 #ifdef FD_STAMPS
 // (one array per translation unit that instantiates kernels)
 // 0 entry, 1 plan done, 2 first copy issued, 3 first stage landed (warp 0),
@@ -477,7 +512,12 @@ struct Shared {
 // FLIP: at most 8 query heads per KV head, one warp per head tile
 // (head_dim 128, one query token): the MMAs take tokens as M and the heads
 // as N (see the FLIP branch of the sub-tile loop).
-template <int KVT, typename QT, int D, bool TOK, int QROWS, bool CAUSAL, bool FLIP = false>
+// WIN: a sliding window and first tokens (one query token): streams leave out
+// the tiles of the hidden middle (WindowView), and the tokens of the remaining
+// ones that are hidden are treated like those past a segment's end.  A box
+// all of whose rows are hidden is not loaded: its page may be gone.
+template <int KVT, typename QT, int D, bool TOK, int QROWS, bool CAUSAL, bool FLIP = false,
+          bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
     mma_split_kernel(const Params p, const Shape sh, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
@@ -529,11 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   prefetch_index_arrays(p);
   if (threadIdx.x == 0) FD_STAMP(g_split_stamps, 11, stamp_ns());
 #ifdef FD_STAMPS
-  const PlanResult plan = compute_plan(
+  const PlanResult plan = compute_plan<WIN>(
       p, sm.red, kThreads, 0,
       blockIdx.x < kStampCtas ? &g_split_stamps[blockIdx.x * kStampSlots + 8] : nullptr);
 #else
-  const PlanResult plan = compute_plan(p, sm.red, kThreads, 0);
+  const PlanResult plan = compute_plan<WIN>(p, sm.red, kThreads, 0);
 #endif
   if (threadIdx.x == 0) FD_STAMP(g_split_stamps, 1, stamp_ns());
   allow_dependent_launch();
@@ -550,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // K/V lines are read once: they leave L2 first, before Q rows, index
     // data and partial states
 
-    SegmentIter it;
+    SegmentIterOf<WIN> it;
     it.init(p, plan);
     Segment seg;
     int n = 0;
@@ -573,13 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n == 0 && lane == 0 && start >= 0) FD_STAMP(g_split_stamps, 10, stamp_ns());
 #endif
       int win_lo = 0, win_hi = 0;   // logical pages [win_lo, win_hi) held in sm.pages
-      for (int t0 = seg.t_begin; t0 < seg.t_end; t0 += sh.tile, ++n) {
-        const int valid = min(sh.tile, seg.t_end - t0);
+      WindowView wv;
+      if constexpr (WIN) wv.init(p, b);
+      for (int x0 = seg.t_begin; x0 < seg.t_end; x0 += sh.tile, ++n) {
+        const int t0 = WIN ? wv.token(x0) : x0;
+        const int valid = WIN ? wv.valid(x0, sh.tile, seg.t_end) : min(sh.tile, seg.t_end - x0);
         if (p.block_table) {
           const int pg_lo = t0 >> p.page_shift;
           const int pg_hi = ((t0 + valid - 1) >> p.page_shift) + 1;
           if (pg_lo < win_lo || pg_hi > win_hi) {
-            const int last = ((seg.t_end - 1) >> p.page_shift) + 1;
+            const int last = ((WIN ? wv.token(seg.t_end - 1) : seg.t_end - 1) >> p.page_shift) + 1;
             win_lo = pg_lo;
             win_hi = min(pg_lo + kPageWindow, last);
             __syncwarp();
@@ -616,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = t0 + i * sh.box_rows;
                 if (t - t0 >= valid) break;
                 const int nval = min(sh.box_rows, valid - (t - t0));
+                if (WIN && wv.hides(t, nval)) continue;
                 long long row;
                 bool ok;
                 if (p.block_table) {
@@ -691,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t dcol = (size_t)(x * sh.hc + h) * sh.region_bytes;
             for (int tt = lane / lpr; tt < valid; tt += rstep) {
               const int t = t0 + tt;
+              if (WIN && wv.hides(t, 1)) continue;
               long long row;
               if (p.block_table) {
                 const int page = sm.pages[(t >> p.page_shift) - win_lo];
@@ -734,14 +779,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n == n_seg0 + S - 1) {   // the next copy waits for a released stage anyway
           // the next segment's row data ahead: its kv_start into a register,
           // or its first window of block-table entries into L2
-          SegmentIter ahead = it;
+          SegmentIterOf<WIN> ahead = it;
           Segment sn;
           if (ahead.next(p, sn)) {
             const int bn = sn.s / p.hg;
             if (!p.block_table) {
               next_start = __ldg(p.kv_start + bn);
             } else {
-              const int pg0 = sn.t_begin >> p.page_shift, pg1 = (sn.t_end - 1) >> p.page_shift;
+              int f0 = sn.t_begin, f1 = sn.t_end - 1;
+              if constexpr (WIN) {
+                WindowView wn;
+                wn.init(p, bn);
+                f0 = wn.token(f0);
+                f1 = wn.token(f1);
+              }
+              const int pg0 = f0 >> p.page_shift, pg1 = f1 >> p.page_shift;
               if (lane < kPageWindow / 32 && pg0 + 32 * lane <= pg1)
                 prefetch_l2(p.block_table + (long long)bn * p.bt_stride + pg0 + 32 * lane);
             }
@@ -804,12 +856,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this head tile's Q fragments in shared memory: [kk][lane] x 16 bytes
     const uint32_t qf = qfrag0 + (uint32_t)ht * KSTEPS * (QROWS * 32) + lane * (QROWS);
 
-    SegmentIter it;
+    SegmentIterOf<WIN> it;
     it.init(p, plan);
     {
       // the Q rows of this head tile for the CTA's later segments, into L2
       // (kept there): a segment start then waits for L2, not for DRAM
-      SegmentIter ahead = it;
+      SegmentIterOf<WIN> ahead = it;
       Segment sa;
       const int row = lane >> 1, lh = mtile * 16 + row;
       for (int k = 0; k < 8 && ahead.next(p, sa); ++k) {
@@ -855,6 +907,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
       int last_stg = 0;
+      WindowView wv;
+      if constexpr (WIN) wv.init(p, b);
 
       for (int t0 = seg.t_begin; t0 < seg.t_end; t0 += sh.tile, ++n) {
         const int stg = (int)(n % S);
@@ -873,7 +927,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int rr = 0; rr < sh.r; ++rr) {
             const int sub = ts * SUB * sh.r + SUB * rr;   // first token of the sub-tile in the tile
-            const int left = seg.t_end - (t0 + sub);      // valid tokens from the sub-tile start
+            // valid tokens from the sub-tile start; with a window, hidden ones [hl, hh)
+            int left = seg.t_end - (t0 + sub), hl = 0, hh = 0;
+            if constexpr (WIN) {
+              left = wv.valid(t0, sh.tile, seg.t_end) - sub;
+              const int first = wv.token(t0) + sub;
+              hl = max(0, wv.hide_lo - first);
+              hh = wv.hide_hi - first;
+              if (hl == 0 && hh >= min(left, SUB)) {   // nothing to see (or past the end)
+                if (left <= 0) break;
+                continue;
+              }
+            }
             if (left <= 0) break;
             int left0 = left, left1 = left;   // valid keys of rows r and r + 8 (see below)
             if (TOK && p.q_len > 1) {
@@ -881,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               left0 = min(left, tail - (p.q_len - 1 - h0 % p.q_len));
               left1 = min(left, tail - (p.q_len - 1 - h1 % p.q_len));
             }
-            const bool edge = min(left0, left1) < SUB;
+            const bool holes = WIN && hl < min(hh, SUB);
+            const bool edge = min(left0, left1) < SUB || holes;
             if constexpr (FLIP) {
               // ---- S^T = K Q^T: MT m-tiles of 16 tokens (8-bit: this lane's
               //      tokens r, r + 8, r + 16, r + 24 of the sub-tile; 16-bit:
@@ -960,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   float ksc = sc;
                   if constexpr (TOK) ksc *= lds_f32(tsk + 4u * (uint32_t)(tok * sh.hc));
                   float va = st[mt][2 * hf] * ksc, vb = st[mt][2 * hf + 1] * ksc;
-                  if (edge && tok >= left) va = vb = -INFINITY;
+                  if (edge && (tok >= left || (WIN && tok >= hl && tok < hh))) va = vb = -INFINITY;
                   st[mt][2 * hf] = va;
                   st[mt][2 * hf + 1] = vb;
                   mx0 = fmaxf(mx0, va);
@@ -997,7 +1063,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int hf = 0; hf < 2; ++hf) {
                     const int tok = 16 * mt + r + 8 * hf;
-                    const float vs = tok < left ? lds_f32(tsv + 4u * (uint32_t)(tok * sh.hc)) : 0.f;
+                    const bool seen = tok < left && !(WIN && tok >= hl && tok < hh);
+                    const float vs = seen ? lds_f32(tsv + 4u * (uint32_t)(tok * sh.hc)) : 0.f;
                     st[mt][2 * hf] *= vs;
                     st[mt][2 * hf + 1] *= vs;
                   }
@@ -1042,7 +1109,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   uint4 w1 = lds128(chunk_addr(reg, u1, r, sh.row_bytes));
                   uint4 w2 = lds128(chunk_addr(reg, u2, r, sh.row_bytes));
                   uint4 w3 = lds128(chunk_addr(reg, u3, r, sh.row_bytes));
-                  if (left < SUB) zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                  if constexpr (WIN) {
+                    if (edge) zero_hidden_rows(w0, w1, w2, w3, 16 * kt + 2 * q, left, hl, hh);
+                  } else if (left < SUB) {
+                    zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                  }
                   const uint32_t A[4] = {w0.x, w0.y, w0.z, w0.w}, B[4] = {w1.x, w1.y, w1.z, w1.w};
                   const uint32_t C[4] = {w2.x, w2.y, w2.z, w2.w}, E[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
@@ -1177,7 +1248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tok = 8 * jn + 2 * q + (e & 1);
                 float v = s[jn][e] * sc;
                 if constexpr (TOK) v *= (e & 1) ? kk2.y : kk2.x;
-                if (edge && tok >= ((e & 2) ? left1 : left0)) v = -INFINITY;
+                if (edge && (tok >= ((e & 2) ? left1 : left0) || (WIN && tok >= hl && tok < hh)))
+                  v = -INFINITY;
                 pr[jn][e] = v;
               }
               mx0 = fmaxf(mx0, fmaxf(pr[jn][0], pr[jn][1]));
@@ -1227,8 +1299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int jn = 0; jn < NJ; ++jn) {
                 // tokens past the end: their scale slot may hold anything
                 const int tk = 8 * jn + 2 * q;
-                const float vx = tk < left ? lds_f32(tsv + 4u * (uint32_t)(tk * sh.hc)) : 0.f;
-                const float vy = tk + 1 < left ? lds_f32(tsv + 4u * (uint32_t)((tk + 1) * sh.hc)) : 0.f;
+                const bool sx = tk < left && !(WIN && tk >= hl && tk < hh);
+                const bool sy = tk + 1 < left && !(WIN && tk + 1 >= hl && tk + 1 < hh);
+                const float vx = sx ? lds_f32(tsv + 4u * (uint32_t)(tk * sh.hc)) : 0.f;
+                const float vy = sy ? lds_f32(tsv + 4u * (uint32_t)((tk + 1) * sh.hc)) : 0.f;
                 pr[jn][0] *= vx;
                 pr[jn][1] *= vy;
                 pr[jn][2] *= vx;
@@ -1259,7 +1333,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 w1 = lds128(chunk_addr(vreg, u1, r, sh.row_bytes));
                 uint4 w2 = lds128(chunk_addr(vreg, u2, r, sh.row_bytes));
                 uint4 w3 = lds128(chunk_addr(vreg, u3, r, sh.row_bytes));
-                if (left < SUB) zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                if constexpr (WIN) {
+                  if (edge) zero_hidden_rows(w0, w1, w2, w3, 16 * kt + 2 * q, left, hl, hh);
+                } else if (left < SUB) {
+                  zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                }
                 const uint32_t A[4] = {w0.x, w0.y, w0.z, w0.w}, B[4] = {w1.x, w1.y, w1.z, w1.w};
                 const uint32_t C[4] = {w2.x, w2.y, w2.z, w2.w}, E[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
@@ -1281,7 +1359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint2 w1 = lds64(chunk_addr(vreg, u1, c, sh.row_bytes) + half);
                 uint2 w2 = lds64(chunk_addr(vreg, u2, c, sh.row_bytes) + half);
                 uint2 w3 = lds64(chunk_addr(vreg, u3, c, sh.row_bytes) + half);
-                if (left < SUB) zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                if constexpr (WIN) {
+                  if (edge) zero_hidden_rows(w0, w1, w2, w3, 16 * kt + 2 * q, left, hl, hh);
+                } else if (left < SUB) {
+                  zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                }
                 const uint32_t A[2] = {w0.x, w0.y}, B[2] = {w1.x, w1.y};
                 const uint32_t C[2] = {w2.x, w2.y}, E[2] = {w3.x, w3.y};
 #pragma unroll
@@ -1305,7 +1387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   uint4 w1 = lds128(chunk_addr(reg, u1, r, sh.row_bytes));
                   uint4 w2 = lds128(chunk_addr(reg, u2, r, sh.row_bytes));
                   uint4 w3 = lds128(chunk_addr(reg, u3, r, sh.row_bytes));
-                  if (left < SUB) zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                  if constexpr (WIN) {
+                    if (edge) zero_hidden_rows(w0, w1, w2, w3, 16 * kt + 2 * q, left, hl, hh);
+                  } else if (left < SUB) {
+                    zero_rows_past_end(w0, w1, w2, w3, 16 * kt + 2 * q, left);
+                  }
                   const uint32_t A[4] = {w0.x, w0.y, w0.z, w0.w}, B[4] = {w1.x, w1.y, w1.z, w1.w};
                   const uint32_t C[4] = {w2.x, w2.y, w2.z, w2.w}, E[4] = {w3.x, w3.y, w3.z, w3.w};
 #pragma unroll
@@ -1523,9 +1609,9 @@ struct Maps {
 // CAUSAL: multi-token queries (q_len > 1) without per-token scales; the
 // per-token-scale kernels fold the causal limit into their ragged-end test.
 template <int KVT, typename QT, int D, bool TOK, int QROWS = 16, bool CAUSAL = false,
-          bool FLIP = false>
+          bool FLIP = false, bool WIN = false>
 cudaError_t launch_t(const Params& p, const Shape& sh, const Maps& m, cudaStream_t stream) {
-  auto kern = mma_split_kernel<KVT, QT, D, TOK, QROWS, CAUSAL, FLIP>;
+  auto kern = mma_split_kernel<KVT, QT, D, TOK, QROWS, CAUSAL, FLIP, WIN>;
   static std::atomic<unsigned long long> limit_set{0};
   cudaError_t e = ensure_smem_limit(kern, kSmemBudget, &limit_set);
   if (e != cudaSuccess) return e;
@@ -1568,8 +1654,26 @@ cudaError_t launch_8bit(const Params& p, const Shape& sh, const Maps& m, cudaStr
 
 
 
+// With a window (one query token): all 16 Q rows, 8, or the FLIP form.
+template <int KVT, typename QT, int D, bool TOK>
+cudaError_t launch_window_t(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st) {
+  if constexpr (D == 128)
+    if (sh.flip) return launch_t<KVT, QT, D, TOK, 8, false, true, true>(p, sh, m, st);
+  return sh.qrows == 8 ? launch_t<KVT, QT, D, TOK, 8, false, false, true>(p, sh, m, st)
+                       : launch_t<KVT, QT, D, TOK, 16, false, false, true>(p, sh, m, st);
+}
+
+template <int KVT, typename QT, bool TOK>
+cudaError_t launch_window(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st) {
+  return p.head_dim == 128 ? launch_window_t<KVT, QT, 128, TOK>(p, sh, m, st)
+                           : launch_window_t<KVT, QT, 64, TOK>(p, sh, m, st);
+}
+
 // Per cache format (one translation unit each): launches the split kernel
 // variant for p's query dtype, head_dim, scale kind and q_len.
+cudaError_t launch_window_e4m3(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);
+cudaError_t launch_window_i8(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);
+cudaError_t launch_window_16bit(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);
 cudaError_t launch_e4m3(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);
 cudaError_t launch_i8(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);
 cudaError_t launch_16bit(const Params& p, const Shape& sh, const Maps& m, cudaStream_t st);

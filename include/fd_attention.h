@@ -300,6 +300,38 @@ fd_status fd_decode_attention_append(const void *q, const void *k_new, const voi
                                      void *workspace, size_t workspace_bytes, fd_stream_t stream);
 
 /*
+ * One decode step whose queries see a sliding window and the first tokens: the
+ * query of sequence b, at position seq_len[b] - 1, attends to the tokens t with
+ *     t >= seq_len[b] - window   or   t < sinks,
+ * with the definition of fd_decode_attention over these.  With k_new the step's
+ * new token is appended first, as by fd_decode_attention_append (q_len = 1);
+ * without (k_new, v_new and positions NULL) the caches hold it and are only
+ * read.
+ *
+ * Block-table entries of pages none of whose tokens the query sees are not
+ * used, so such pages may have been given away (fd_assign_pages does that) and
+ * their entries may hold anything.  Rows of hidden tokens have no effect,
+ * whatever bits they hold; in a contiguous cache they must lie inside it (they
+ * share tiles with visible ones).
+ *
+ * window     >= 1 (1: the query's own token); longer than a sequence: all of it.
+ * sinks      >= 0.
+ * FD_KERNEL_AUTO and FD_KERNEL_MMA only (the mma.sync kernel runs), else
+ * FD_ERR_UNSUPPORTED.  Workspace, other arguments and errors are those of
+ * fd_decode_attention_append.
+ */
+fd_status fd_decode_attention_window(const void *q, const void *k_new, const void *v_new,
+                                     void *k_cache, void *v_cache, const int32_t *kv_start_idx,
+                                     const int32_t *block_table, int block_table_stride,
+                                     const int32_t *positions, const int32_t *seq_len,
+                                     int64_t kv_rows, int batch, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int page_size, int window,
+                                     int sinks, float softmax_scale, float k_scale, float v_scale,
+                                     fd_scale_kind scale_kind, float *k_scales, float *v_scales,
+                                     fd_dtype q_dtype, fd_dtype kv_dtype, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, fd_stream_t stream);
+
+/*
  * Same computation as fd_decode_attention, for callers that cannot allocate
  * device memory (for example code running inside a framework that does not
  * expose its allocator, or under a fixed memory budget).  The pages have no
@@ -498,6 +530,27 @@ fd_status fd_prefill_attention(const void *q, int64_t q_stride, const void *k_ca
                                const float *v_scales, fd_dtype q_dtype, fd_dtype kv_dtype,
                                void *out, float *lse, void *workspace, size_t workspace_bytes,
                                fd_stream_t stream);
+
+/*
+ * fd_prefill_attention with a sliding window and first tokens: the new token at
+ * position p attends to the tokens t <= p with t > p - window or t < sinks.
+ * window and sinks, and what is said of hidden tokens' pages and rows, as for
+ * fd_decode_attention_window (a page is hidden when no new token of its
+ * sequence sees any of its tokens); every other argument, the workspace and the
+ * errors as for fd_prefill_attention.
+ */
+fd_status fd_prefill_attention_window(const void *q, int64_t q_stride, const void *k_cache,
+                                      const void *v_cache, const int32_t *kv_start_idx,
+                                      const int32_t *block_table, int block_table_stride,
+                                      const int32_t *q_start, const int32_t *seq_len,
+                                      int64_t num_tokens, int64_t kv_rows, int batch,
+                                      int num_q_heads, int num_kv_heads, int head_dim,
+                                      int page_size, int window, int sinks, float softmax_scale,
+                                      float k_scale, float v_scale, fd_scale_kind scale_kind,
+                                      const float *k_scales, const float *v_scales,
+                                      fd_dtype q_dtype, fd_dtype kv_dtype, void *out, float *lse,
+                                      void *workspace, size_t workspace_bytes,
+                                      fd_stream_t stream);
 
 /*
  * Synchronises `stream`, reads and clears the workspace's sticky device-error
