@@ -68,6 +68,7 @@ EXPORTED = [
     "fd_debug_set_wait_limit", "fd_debug_plan_segments",
     "fd_rotary_table", "fd_append_kv_packed", "fd_read_kv", "fd_prefill_workspace_bytes",
     "fd_prefill_attention", "fd_decode_attention_window", "fd_prefill_attention_window",
+    "fd_append_kv_normed",
 ]
 
 
@@ -159,6 +160,11 @@ def load_library(path: Optional[str] = None):
         lib.fd_prefill_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, vp, vp, i64, i64, i32,
                                              i32, i32, i32, i32, f32, f32, f32, i32, vp, vp, i32,
                                              i32, vp, vp, vp, sz, vp]
+        lib.fd_append_kv_normed.restype = i32
+        lib.fd_append_kv_normed.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp,
+                                            i64, i64, i32, i32, i32, i32, i32, vp, i64, i32, i32,
+                                            vp, vp, i32, f32, vp, i32, i64, ctypes.c_char_p, f32,
+                                            f32, i32, vp, vp, i32, i32, vp, sz, vp]
         lib.fd_decode_attention_window.restype = i32
         lib.fd_decode_attention_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i64,
                                                    i32, i32, i32, i32, i32, i32, i32, f32, f32,
@@ -441,6 +447,37 @@ def fd_append_kv_packed(q, q_stride: int, q_out, k_new, v_new, kv_stride: int, k
         workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_append_kv_packed")
+    return st
+
+
+def fd_append_kv_normed(q, q_stride: int, q_out, k_new, v_new, kv_stride: int, k_cache, v_cache,
+                        kv_start_idx, block_table, q_start, positions, num_tokens: int,
+                        kv_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                        page_size: int, rotary, rot_dim: int, interleaved: bool, q_norm, k_norm,
+                        norm_f32: bool, norm_eps: float, axis_positions, pair_axis: bytes,
+                        k_scale: float, v_scale: float, scale_kind: int, k_scales, v_scales,
+                        workspace, stream=None, new_dtype: Optional[int] = None,
+                        kv_dtype: Optional[int] = None, check: bool = True) -> int:
+    """fd_append_kv_packed with norms of query and key heads (weights
+    ``q_norm`` / ``k_norm``, or None) and rotary positions on several axes
+    (``axis_positions`` int32 [axes, tokens], or None; ``pair_axis``: each
+    pair's axis, one byte per pair)."""
+    st = (_lib or load_library()).fd_append_kv_normed(
+        None if q is None else q.data_ptr(), q_stride, None if q is None else q_out.data_ptr(),
+        k_new.data_ptr(), v_new.data_ptr(), kv_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(kv_start_idx), _ptr(block_table), 0 if block_table is None else block_table.shape[1],
+        q_start.data_ptr(), positions.data_ptr(), num_tokens, kv_rows, positions.shape[0],
+        num_q_heads, num_kv_heads, head_dim, page_size, _ptr(rotary),
+        0 if rotary is None else rotary.shape[0], rot_dim, 1 if interleaved else 0, _ptr(q_norm),
+        _ptr(k_norm), 1 if norm_f32 else 0, norm_eps, _ptr(axis_positions),
+        0 if axis_positions is None else axis_positions.shape[0],
+        0 if axis_positions is None else axis_positions.stride(0), pair_axis, k_scale, v_scale,
+        scale_kind, _ptr(k_scales), _ptr(v_scales),
+        _q_dtype(k_new) if new_dtype is None else new_dtype,
+        _kv_dtype(k_cache) if kv_dtype is None else kv_dtype,
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_append_kv_normed")
     return st
 
 
@@ -880,6 +917,34 @@ def rotary_table(positions: int, rot_dim: int, *, theta: float = 10000.0, scalin
     return out
 
 
+def _norms_and_axes(q, k_new, D: int, at: int, rotary, q_norm, k_norm, axis_positions, pair_axes):
+    """Checks of append_kv's norms and axes: (weights are fp32, axes as bytes)."""
+    if q_norm is not None and q is None:
+        raise ValueError("q_norm needs q")
+    norm = q_norm if q_norm is not None else k_norm
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None and (w.shape != (D,) or w.dtype not in (k_new.dtype, torch.float32) or
+                              w.dtype != norm.dtype or not w.is_contiguous()):
+            raise ValueError(f"{name} must be dense [{D}] of {k_new.dtype} or float32, both norms "
+                             f"alike, got {w.dtype} {tuple(w.shape)}")
+    _same_device(at, q_norm, k_norm, axis_positions)
+    axes = b""
+    if axis_positions is not None:
+        if rotary is None or pair_axes is None:
+            raise ValueError("axis_positions needs rotary and pair_axes")
+        shape, n = axis_positions.shape, k_new.shape[0]
+        if len(shape) != 2 or shape[1] != n or axis_positions.dtype != torch.int32 or \
+                (n > 1 and axis_positions.stride(1) != 1) or axis_positions.stride(0) < n:
+            raise ValueError(f"axis_positions must be int32 [axes, {n}] with dense rows, got "
+                             f"{axis_positions.dtype} {tuple(shape)}")
+        axes = pair_axes if isinstance(pair_axes, bytes) else bytes(list(pair_axes))
+        if len(axes) != rotary.shape[1] // 2 or max(axes, default=0) >= shape[0]:
+            raise ValueError(f"pair_axes must be {rotary.shape[1] // 2} numbers below {shape[0]}")
+    elif pair_axes is not None:
+        raise ValueError("pair_axes needs axis_positions")
+    return norm is not None and norm.dtype == torch.float32, axes
+
+
 def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
               v_cache: torch.Tensor, q_start: torch.Tensor, positions: torch.Tensor, *,
               q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -888,7 +953,10 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
               block_table: Optional[torch.Tensor] = None, k_scale: float = 1.0,
               v_scale: float = 1.0, k_scales: Optional[torch.Tensor] = None,
               v_scales: Optional[torch.Tensor] = None,
-              workspace: Optional[torch.Tensor] = None, stream=None):
+              workspace: Optional[torch.Tensor] = None, stream=None,
+              q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+              norm_eps: float = 1e-6, axis_positions: Optional[torch.Tensor] = None,
+              pair_axes=None):
     """Writes packed new tokens ([tokens, KVH, D], sequence b's at
     ``q_start[b]`` .. ``q_start[b + 1]`` - 1, the first of them at position
     ``positions[b]``) into a contiguous or paged cache, quantised for 8-bit
@@ -898,7 +966,15 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
     first, as pairs half of that apart or, with ``interleaved``, neighbouring
     ones.  Returns the turned queries (``q_out``, fresh unless given; q itself
     is allowed), or None without ``q``.  k_new, v_new and q may be slices of
-    one wider projection."""
+    one wider projection.
+
+    ``q_norm`` / ``k_norm`` ([D], of k_new's dtype or fp32; either may be
+    missing) norm every query / key head before the rotation:
+    x / sqrt(mean(x^2) + norm_eps) * weight.  With ``axis_positions`` (int32
+    [axes, tokens], at most 4 axes) and ``pair_axes`` (each rotary pair's axis,
+    ``rotary.shape[1] / 2`` whole numbers on the host) pair i turns by position
+    ``axis_positions[pair_axes[i], token]`` (time, height and width of an image
+    patch, say); ``positions`` still says where a token is cached."""
     kv_rows, KVH, D, P = _cache_sizes(k_cache, v_cache, kv_start_idx, block_table)
     dev, at = k_cache.device, k_cache.get_device()
     n = k_new.shape[0]
@@ -929,15 +1005,29 @@ def append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
         if rotary.dim() != 2 or rotary.dtype != torch.float32 or not rotary.is_contiguous():
             raise ValueError("rotary must be a dense fp32 [positions, rot_dim] table")
         rot = rotary.shape[1]
+    extra = q_norm is not None or k_norm is not None or axis_positions is not None
+    norm_f32 = False
+    if extra:
+        norm_f32, pair_axes = _norms_and_axes(q, k_new, D, at, rotary, q_norm, k_norm,
+                                              axis_positions, pair_axes)
+    elif pair_axes is not None:
+        raise ValueError("pair_axes needs axis_positions")
     with _on(dev, stream):
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
         if workspace is None:
             workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
-        fd_append_kv_packed(q, qs, q_out, k_new, v_new, ks, k_cache, v_cache, kv_start_idx,
-                            block_table, q_start, positions, n, kv_rows, QH, KVH, D, P, rotary,
-                            rot, interleaved, k_scale, v_scale, kind, k_scales, v_scales,
-                            workspace)
+        if extra:
+            fd_append_kv_normed(q, qs, q_out, k_new, v_new, ks, k_cache, v_cache, kv_start_idx,
+                                block_table, q_start, positions, n, kv_rows, QH, KVH, D, P, rotary,
+                                rot, interleaved, q_norm, k_norm, norm_f32, norm_eps,
+                                axis_positions, pair_axes, k_scale, v_scale, kind, k_scales,
+                                v_scales, workspace)
+        else:
+            fd_append_kv_packed(q, qs, q_out, k_new, v_new, ks, k_cache, v_cache, kv_start_idx,
+                                block_table, q_start, positions, n, kv_rows, QH, KVH, D, P, rotary,
+                                rot, interleaved, k_scale, v_scale, kind, k_scales, v_scales,
+                                workspace)
     return q_out
 
 
@@ -995,15 +1085,19 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                       rotary: Optional[torch.Tensor] = None, interleaved: bool = False,
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None, stream=None,
-                      window: Optional[int] = None, sinks: int = 0):
+                      window: Optional[int] = None, sinks: int = 0,
+                      q_norm: Optional[torch.Tensor] = None,
+                      k_norm: Optional[torch.Tensor] = None, norm_eps: float = 1e-6,
+                      axis_positions: Optional[torch.Tensor] = None, pair_axes=None):
     """Attention of packed new tokens ``q`` [tokens, QH, D] (sequence b's at
     ``q_start[b]`` .. ``q_start[b + 1]`` - 1: the last of its ``seq_len[b]``
     tokens, causal) over a contiguous or paged cache; returns (out, lse).
     With ``k_new`` / ``v_new`` [tokens, KVH, D] and ``positions`` the new tokens
-    are first written into the caches by ``append_kv`` (queries and keys turned
-    by ``rotary`` if given); ``seq_len`` counts them.  Arguments are checked
-    before anything is written.  With ``rotary``, tokens that ``append_kv``
-    leaves alone have no turned query: their rows of ``out`` and ``lse`` are
+    are first written into the caches by ``append_kv`` (queries and keys normed
+    by ``q_norm`` / ``k_norm`` and turned by ``rotary`` if given, on axes if
+    given); ``seq_len`` counts them.  Arguments are checked before anything is
+    written.  With ``rotary`` or ``q_norm``, tokens that ``append_kv`` leaves
+    alone have no such query: their rows of ``out`` and ``lse`` are
     undefined (zero and -inf where ``seq_len`` gives them no key).  Without
     ``k_new`` the caches hold the new tokens already and ``q`` is taken as it
     is.  With ``window`` a token sees the last ``window`` keys up to its own and
@@ -1029,6 +1123,10 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         raise ValueError("give k_new, v_new and positions, or none of them")
     if rotary is not None and k_new is None:
         raise ValueError("rotary turns queries together with new keys: give k_new")
+    if k_new is None and (q_norm is not None or k_norm is not None or
+                          axis_positions is not None or pair_axes is not None):
+        raise ValueError("norms and axes belong to new keys: give k_new")
+    fresh = rotary is not None or q_norm is not None   # append_kv makes the queries attended with
     if k_new is not None and k_new.shape[0] != n:
         raise ValueError(f"k_new must have q's {n} tokens, got {k_new.shape[0]}")
     if softmax_scale is None:
@@ -1060,14 +1158,16 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         if k_new is not None:
             # a call that the attention refuses leaves the caches as they were:
             # its checks (of no tokens) come before the append
-            if rotary is None and _overlap(out, q):
+            if not fresh and _overlap(out, q):
                 raise ValueError("out must not overlap q")
             attend(q, qs, 0)
             turned = append_kv(k_new, v_new, k_cache, v_cache, q_start, positions,
-                               q=q if rotary is not None else None, rotary=rotary,
+                               q=q if fresh else None, rotary=rotary,
                                interleaved=interleaved, kv_start_idx=kv_start_idx,
                                block_table=block_table, k_scale=k_scale, v_scale=v_scale,
-                               k_scales=k_scales, v_scales=v_scales, workspace=workspace)
+                               k_scales=k_scales, v_scales=v_scales, workspace=workspace,
+                               q_norm=q_norm, k_norm=k_norm, norm_eps=norm_eps,
+                               axis_positions=axis_positions, pair_axes=pair_axes)
             if turned is not None:
                 q, qs = turned, QH * D
         attend(q, qs, n)

@@ -66,6 +66,8 @@ __device__ __forceinline__ void check_starts(const Placement& pl, const int32_t*
   }
 }
 
+constexpr int kMaxRotDim = 128;
+
 struct AppendPacked {
   Placement at;
   const void *q, *k_new, *v_new;
@@ -78,6 +80,15 @@ struct AppendPacked {
   int scale_kind;
   float *k_scales, *v_scales;
   int new_dtype, kv_dtype;
+  // norms of heads (weights [head_dim] of new_dtype, or fp32 with norm_f32)
+  const void *q_norm, *k_norm;
+  int norm_f32;
+  float norm_eps;
+  // positions [num_axes] rows of axis_stride, and the axis of every pair
+  int num_axes;
+  long long axis_stride;
+  const int32_t* axis_positions;
+  uint8_t pair_axis[kMaxRotDim / 2];
 };
 
 struct ReadKv {
@@ -93,7 +104,6 @@ struct ReadKv {
 };
 
 // The scaled frequencies as fixed-point turns per position (2^64 = one turn).
-constexpr int kMaxRotDim = 128;
 struct RotaryTable {
   float* table;
   long long positions;

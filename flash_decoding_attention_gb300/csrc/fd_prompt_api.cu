@@ -129,17 +129,28 @@ fd_status fd_rotary_table(float* table, int64_t positions, int rot_dim, double t
              : FD_ERR_CUDA;
 }
 
-fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, const void* k_new,
-                              const void* v_new, int64_t kv_stride, void* k_cache, void* v_cache,
-                              const int32_t* kv_start_idx, const int32_t* block_table,
-                              int block_table_stride, const int32_t* q_start,
-                              const int32_t* positions, int64_t num_tokens, int64_t kv_rows,
-                              int batch, int num_q_heads, int num_kv_heads, int head_dim,
-                              int page_size, const float* rotary, int64_t rotary_positions,
-                              int rot_dim, int interleaved, float k_scale, float v_scale,
-                              fd_scale_kind scale_kind, float* k_scales, float* v_scales,
-                              fd_dtype new_dtype, fd_dtype kv_dtype, void* workspace,
-                              size_t workspace_bytes, fd_stream_t stream) {
+// What fd_append_kv_normed has beside the packed append's arguments.
+struct AppendExtra {
+  const void *q_norm, *k_norm;
+  int norm_f32;
+  float norm_eps;
+  const int32_t* axis_positions;
+  int num_axes;
+  int64_t axis_stride;
+  const uint8_t* pair_axis;
+};
+
+static fd_status append_impl(const void* q, int64_t q_stride, void* q_out, const void* k_new,
+                             const void* v_new, int64_t kv_stride, void* k_cache, void* v_cache,
+                             const int32_t* kv_start_idx, const int32_t* block_table,
+                             int block_table_stride, const int32_t* q_start,
+                             const int32_t* positions, int64_t num_tokens, int64_t kv_rows,
+                             int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                             int page_size, const float* rotary, int64_t rotary_positions,
+                             int rot_dim, int interleaved, float k_scale, float v_scale,
+                             fd_scale_kind scale_kind, float* k_scales, float* v_scales,
+                             fd_dtype new_dtype, fd_dtype kv_dtype, void* workspace,
+                             size_t workspace_bytes, fd_stream_t stream, const AppendExtra& x) {
   const fd_status chk = check_placement(
       k_cache, v_cache, kv_start_idx, block_table, block_table_stride, q_start, num_tokens,
       kv_rows, batch, num_kv_heads, head_dim, page_size, scale_kind, k_scales, v_scales, new_dtype,
@@ -161,6 +172,21 @@ fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, cons
   if (rotary) {
     if (!aligned(rotary, 16) || rotary_positions <= 0) return FD_ERR_INVALID_ARG;
     if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return FD_ERR_UNSUPPORTED;
+  }
+  if (x.q_norm || x.k_norm) {
+    if (x.q_norm && !q) return FD_ERR_INVALID_ARG;
+    const size_t elem = x.norm_f32 ? 4 : 2;
+    if (!aligned(x.q_norm, elem) || !aligned(x.k_norm, elem)) return FD_ERR_INVALID_ARG;
+    if (!std::isfinite(x.norm_eps) || !(x.norm_eps > 0.f)) return FD_ERR_INVALID_ARG;
+  }
+  if (x.num_axes != 0) {
+    if (x.num_axes < 0 || x.num_axes > 4) return FD_ERR_UNSUPPORTED;
+    if (!rotary || !x.pair_axis) return FD_ERR_INVALID_ARG;
+    if ((!x.axis_positions && num_tokens > 0) || !aligned(x.axis_positions, 4) ||
+        x.axis_stride < num_tokens || x.axis_stride >= kMaxPacked)
+      return FD_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i)
+      if (x.pair_axis[i] >= x.num_axes) return FD_ERR_INVALID_ARG;
   }
   if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return FD_ERR_INVALID_ARG;
   if (kv_elem_bytes(kv_dtype) == 1 && !(k_scale > 0.f && v_scale > 0.f)) return FD_ERR_INVALID_ARG;
@@ -206,9 +232,62 @@ fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, cons
   p.v_scales = v_scales;
   p.new_dtype = new_dtype;
   p.kv_dtype = kv_dtype;
+  p.q_norm = x.q_norm;
+  p.k_norm = x.k_norm;
+  p.norm_f32 = x.norm_f32 ? 1 : 0;
+  p.norm_eps = x.norm_eps;
+  if (x.num_axes > 0) {
+    p.num_axes = x.num_axes;
+    p.axis_stride = x.axis_stride;
+    p.axis_positions = x.axis_positions;
+    std::memcpy(p.pair_axis, x.pair_axis, rot_dim / 2);
+  }
   return launch_append_packed(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FD_OK
              : FD_ERR_CUDA;
+}
+
+fd_status fd_append_kv_packed(const void* q, int64_t q_stride, void* q_out, const void* k_new,
+                              const void* v_new, int64_t kv_stride, void* k_cache, void* v_cache,
+                              const int32_t* kv_start_idx, const int32_t* block_table,
+                              int block_table_stride, const int32_t* q_start,
+                              const int32_t* positions, int64_t num_tokens, int64_t kv_rows,
+                              int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                              int page_size, const float* rotary, int64_t rotary_positions,
+                              int rot_dim, int interleaved, float k_scale, float v_scale,
+                              fd_scale_kind scale_kind, float* k_scales, float* v_scales,
+                              fd_dtype new_dtype, fd_dtype kv_dtype, void* workspace,
+                              size_t workspace_bytes, fd_stream_t stream) {
+  return append_impl(q, q_stride, q_out, k_new, v_new, kv_stride, k_cache, v_cache, kv_start_idx,
+                     block_table, block_table_stride, q_start, positions, num_tokens, kv_rows,
+                     batch, num_q_heads, num_kv_heads, head_dim, page_size, rotary,
+                     rotary_positions, rot_dim, interleaved, k_scale, v_scale, scale_kind,
+                     k_scales, v_scales, new_dtype, kv_dtype, workspace, workspace_bytes, stream,
+                     AppendExtra{});
+}
+
+fd_status fd_append_kv_normed(const void* q, int64_t q_stride, void* q_out, const void* k_new,
+                              const void* v_new, int64_t kv_stride, void* k_cache, void* v_cache,
+                              const int32_t* kv_start_idx, const int32_t* block_table,
+                              int block_table_stride, const int32_t* q_start,
+                              const int32_t* positions, int64_t num_tokens, int64_t kv_rows,
+                              int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                              int page_size, const float* rotary, int64_t rotary_positions,
+                              int rot_dim, int interleaved, const void* q_norm, const void* k_norm,
+                              int norm_f32, float norm_eps, const int32_t* axis_positions,
+                              int num_axes, int64_t axis_stride, const uint8_t* pair_axis,
+                              float k_scale, float v_scale, fd_scale_kind scale_kind,
+                              float* k_scales, float* v_scales, fd_dtype new_dtype,
+                              fd_dtype kv_dtype, void* workspace, size_t workspace_bytes,
+                              fd_stream_t stream) {
+  const AppendExtra x{q_norm,   k_norm,      norm_f32,  norm_eps, axis_positions,
+                      num_axes, axis_stride, pair_axis};
+  return append_impl(q, q_stride, q_out, k_new, v_new, kv_stride, k_cache, v_cache, kv_start_idx,
+                     block_table, block_table_stride, q_start, positions, num_tokens, kv_rows,
+                     batch, num_q_heads, num_kv_heads, head_dim, page_size, rotary,
+                     rotary_positions, rot_dim, interleaved, k_scale, v_scale, scale_kind,
+                     k_scales, v_scales, new_dtype, kv_dtype, workspace, workspace_bytes, stream,
+                     x);
 }
 
 fd_status fd_read_kv(const void* k_cache, const void* v_cache, const int32_t* kv_start_idx,

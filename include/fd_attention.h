@@ -462,6 +462,48 @@ fd_status fd_append_kv_packed(const void *q, int64_t q_stride, void *q_out, cons
                               size_t workspace_bytes, fd_stream_t stream);
 
 /*
+ * fd_append_kv_packed with norms of query and key heads, and with rotary
+ * positions on several axes.  In the same pass, before the rotation, a head x
+ * of q becomes
+ *     x_d / sqrt(sum_d x_d^2 / head_dim + norm_eps) * q_norm[d],
+ * a head of k_new the same with k_norm; either may be NULL (that tensor is not
+ * normed).  Values are not normed.  The sum of squares is the exact one rounded
+ * to fp32; the products, the quotient 1 / sqrt and the rotation are single fp32
+ * operations, and nothing is rounded to 16 bits in between.  (A sum of squares
+ * beyond fp32's range is infinite: finite elements become zero.)
+ *
+ * q_norm, k_norm  device arrays [head_dim] of new_dtype, or of fp32 with
+ *             norm_f32 non-zero; q_norm needs q.
+ * norm_eps    finite, > 0 (ignored without q_norm and k_norm).
+ * axis_positions  device int32 [num_axes], axis_stride apart: entry i of axis a
+ *             is packed token i's position on it.  Pair i of the rotation takes
+ *             row axis_positions[pair_axis[i]] of the table instead of the
+ *             token's place in its sequence, which still decides its cache row.
+ *             A token with an entry outside [0, rotary_positions) is skipped and
+ *             recorded as FD_ERR_DEVICE_BOUNDS.
+ * num_axes    0 (no axes: as fd_append_kv_packed) .. 4.
+ * axis_stride at least num_tokens, < 2^31.
+ * pair_axis   HOST array of rot_dim / 2 axes, each < num_axes; read during the
+ *             call.  Runs of pairs for one axis and pairs taking turns are both
+ *             ways to fill it.
+ */
+fd_status fd_append_kv_normed(const void *q, int64_t q_stride, void *q_out,
+                              const void *k_new, const void *v_new, int64_t kv_stride,
+                              void *k_cache, void *v_cache, const int32_t *kv_start_idx,
+                              const int32_t *block_table, int block_table_stride,
+                              const int32_t *q_start, const int32_t *positions,
+                              int64_t num_tokens, int64_t kv_rows, int batch,
+                              int num_q_heads, int num_kv_heads, int head_dim,
+                              int page_size, const float *rotary, int64_t rotary_positions,
+                              int rot_dim, int interleaved, const void *q_norm,
+                              const void *k_norm, int norm_f32, float norm_eps,
+                              const int32_t *axis_positions, int num_axes,
+                              int64_t axis_stride, const uint8_t *pair_axis, float k_scale,
+                              float v_scale, fd_scale_kind scale_kind, float *k_scales,
+                              float *v_scales, fd_dtype new_dtype, fd_dtype kv_dtype,
+                              void *workspace, size_t workspace_bytes, fd_stream_t stream);
+
+/*
  * Reads cached tokens back as packed 16-bit rows: packed row i of sequence b
  * (out_start[b] <= i < out_start[b + 1]) receives token
  * first[b] + i - out_start[b] of that sequence,
