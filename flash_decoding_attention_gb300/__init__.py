@@ -17,7 +17,7 @@ import ctypes
 import math
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -68,7 +68,7 @@ EXPORTED = [
     "fd_debug_set_wait_limit", "fd_debug_plan_segments",
     "fd_rotary_table", "fd_append_kv_packed", "fd_read_kv", "fd_prefill_workspace_bytes",
     "fd_prefill_attention", "fd_decode_attention_window", "fd_prefill_attention_window",
-    "fd_append_kv_normed",
+    "fd_append_kv_normed", "fd_assign_pages", "fd_assign_pages_workspace_bytes",
 ]
 
 
@@ -160,6 +160,11 @@ def load_library(path: Optional[str] = None):
         lib.fd_prefill_attention.argtypes = [vp, i64, vp, vp, vp, vp, i32, vp, vp, i64, i64, i32,
                                              i32, i32, i32, i32, f32, f32, f32, i32, vp, vp, i32,
                                              i32, vp, vp, vp, sz, vp]
+        lib.fd_assign_pages_workspace_bytes.restype = sz
+        lib.fd_assign_pages_workspace_bytes.argtypes = [i32]
+        lib.fd_assign_pages.restype = i32
+        lib.fd_assign_pages.argtypes = [vp, i32, vp, vp, vp, i64, vp, i32, i32, i32, i32, vp, vp,
+                                        vp, vp, vp, vp, vp, i64, vp, sz, vp]
         lib.fd_append_kv_normed.restype = i32
         lib.fd_append_kv_normed.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp,
                                             i64, i64, i32, i32, i32, i32, i32, vp, i64, i32, i32,
@@ -498,6 +503,26 @@ def fd_read_kv(k_cache, v_cache, kv_start_idx, block_table, out_start, first, nu
         workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if check and st != FD_OK:
         raise FdError(st, "fd_read_kv")
+    return st
+
+
+def fd_assign_pages_workspace_bytes(batch: int) -> int:
+    return int(load_library().fd_assign_pages_workspace_bytes(int(batch)))
+
+
+def fd_assign_pages(block_table, seq_len, new_tokens, free_pages, free_count, page_size: int,
+                    window: int, sinks: int, released, seq_len_out, free_count_out, released_out,
+                    q_start, positions, slots, workspace, stream=None, check: bool = True) -> int:
+    """Hands pages to growing sequences and takes those of ended ones back."""
+    st = (_lib or load_library()).fd_assign_pages(
+        block_table.data_ptr(), block_table.shape[1], seq_len.data_ptr(), new_tokens.data_ptr(),
+        free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), seq_len.shape[0],
+        page_size, window, sinks, _ptr(released), seq_len_out.data_ptr(),
+        free_count_out.data_ptr(), _ptr(released_out), q_start.data_ptr(), positions.data_ptr(),
+        _ptr(slots), 0 if slots is None else slots.shape[0], workspace.data_ptr(),
+        workspace.nbytes, _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_assign_pages")
     return st
 
 
@@ -872,6 +897,94 @@ def _layout_index(kv_start_idx, block_table, batch: int, at: int) -> None:
         _index("block_table", block_table, batch, at, 2)
     else:
         _index("kv_start_idx", kv_start_idx, batch, at)
+
+
+class PageStep(NamedTuple):
+    """What assign_pages says of a step; every entry is on the device."""
+    q_start: torch.Tensor              # int32 [B + 1]: where each sequence's packed tokens begin
+    positions: torch.Tensor            # int32 [B]: of its first new token; -1: not served
+    seq_len: torch.Tensor              # int32 [B]: cached tokens with the new ones
+    free_count: torch.Tensor           # int32 [1]: pages left on the stack
+    released: Optional[torch.Tensor]   # int32 [B]: first column not given back (with a window)
+    slots: Optional[torch.Tensor]      # int64 [num_slots]: cache row of every packed token, or -1
+
+
+def alloc_page_workspace(batch: int, device=None) -> torch.Tensor:
+    """Workspace of assign_pages for ``batch`` sequences; keep it from call to call."""
+    n = fd_assign_pages_workspace_bytes(batch)
+    if n == 0:
+        raise FdError(FD_ERR_INVALID_ARG, "fd_assign_pages_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, *,
+                 num_slots: int = 0, window: Optional[int] = None, sinks: int = 0,
+                 released: Optional[torch.Tensor] = None,
+                 seq_len_out: Optional[torch.Tensor] = None,
+                 free_count_out: Optional[torch.Tensor] = None,
+                 released_out: Optional[torch.Tensor] = None,
+                 q_start: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 slots: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> PageStep:
+    """One step's page bookkeeping on the device: sequence b's ``seq_len[b]``
+    cached tokens become ``seq_len[b] + new_tokens[b]`` (int32 [B] both; a
+    negative number ends the sequence), pages come from and go back to the stack
+    ``free_pages[:free_count]``, and ``block_table`` [B, columns] is updated in
+    place.  Returns what the packed calls take: q_start, positions (-1 where
+    there were too few pages, or the sequence has ended) and the new seq_len;
+    with ``num_slots`` (or ``slots``) also the cache row of every packed token.
+
+    With ``window`` (and ``sinks``) pages that no later token sees go back as
+    well; ``released`` (int32 [B], zeros for new sequences) is kept from step to
+    step.  The ``_out`` arrays default to fresh ones and may be the inputs
+    themselves."""
+    if not block_table.is_cuda:
+        raise ValueError(f"the block table must be on a GPU, got {block_table.device}")
+    dev, at = block_table.device, block_table.get_device()
+    batch = seq_len.shape[0]
+    _index("block_table", block_table, batch, at, 2)
+    _index("seq_len", seq_len, batch, at)
+    _index("new_tokens", new_tokens, batch, at)
+    _index("free_pages", free_pages, free_pages.shape[0], at)
+    _index("free_count", free_count, 1, at)
+    if window is not None:
+        _window_sizes(window, sinks)
+        if released is None:
+            raise ValueError("a window needs released, the columns given back so far")
+        _index("released", released, batch, at)
+    elif sinks or released is not None or released_out is not None:
+        raise ValueError("sinks and released belong to a window: give window")
+    for name, t, n in (("seq_len_out", seq_len_out, batch), ("free_count_out", free_count_out, 1),
+                       ("released_out", released_out, batch), ("q_start", q_start, batch + 1),
+                       ("positions", positions, batch)):
+        if t is not None:
+            _index(name, t, n, at)
+    if slots is not None and (slots.dtype != torch.int64 or slots.dim() != 1 or
+                              not slots.is_contiguous() or num_slots not in (0, slots.shape[0])):
+        raise ValueError(f"slots must be dense int64 [{num_slots}], got {slots.dtype} "
+                         f"{tuple(slots.shape)}")
+    _same_device(at, slots, workspace)
+    with _on(dev, stream):
+        i32 = dict(dtype=torch.int32, device=dev)
+        if seq_len_out is None:
+            seq_len_out = torch.empty(batch, **i32)
+        if free_count_out is None:
+            free_count_out = torch.empty(1, **i32)
+        if released_out is None and window is not None:
+            released_out = torch.empty(batch, **i32)
+        if q_start is None:
+            q_start = torch.empty(batch + 1, **i32)
+        if positions is None:
+            positions = torch.empty(batch, **i32)
+        if slots is None and num_slots:
+            slots = torch.empty(num_slots, dtype=torch.int64, device=dev)
+        if workspace is None:
+            workspace = alloc_page_workspace(batch, dev)
+        fd_assign_pages(block_table, seq_len, new_tokens, free_pages, free_count, page_size,
+                        window or 0, sinks, released, seq_len_out, free_count_out, released_out,
+                        q_start, positions, slots, workspace)
+    return PageStep(q_start, positions, seq_len_out, free_count_out, released_out, slots)
 
 
 def alloc_prefill_workspace(head_dim: int, device=None) -> torch.Tensor:

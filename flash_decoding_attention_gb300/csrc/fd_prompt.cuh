@@ -145,6 +145,35 @@ struct PrefillLayout {
 };
 PrefillLayout prefill_layout(int head_dim, int sms);
 
+struct PageRec {
+  int L, held;   // cached tokens, pages held
+  int need;      // pages handed out; -1: its tokens are not served
+  int keep, lo;  // columns that go back: [0, keep), then from lo on
+};
+
+struct PageTotals {
+  long long count, avail;   // of the stack: before, and with what returns
+  long long back, handed;   // pages
+};
+
+struct AssignPages {
+  int32_t *table, *free_pages;
+  const int32_t *seq_len, *new_tokens, *free_count, *released;
+  int32_t *seq_len_out, *free_count_out, *released_out, *q_start, *positions;
+  long long* slots;
+  long long num_slots, capacity;
+  int batch, stride, page_shift;
+  int window, keep;   // 0: none; columns [0, keep) hold first tokens and stay
+  WsHeader* ws;
+  // workspace of the two-launch form: what each sequence gives and takes, and
+  // the sums before it
+  PageTotals* totals;
+  PageRec* rec;
+  int32_t *back, *handed;
+};
+
+size_t assign_pages_bytes(int batch);
+cudaError_t launch_assign_pages(AssignPages p, int sms, cudaStream_t stream);
 cudaError_t launch_append_packed(const AppendPacked& p, int sms, cudaStream_t stream);
 cudaError_t launch_read_kv(const ReadKv& p, int sms, cudaStream_t stream);
 cudaError_t launch_rotary_table(const RotaryTable& p, int sms, cudaStream_t stream);

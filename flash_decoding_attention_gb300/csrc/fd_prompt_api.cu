@@ -338,6 +338,67 @@ fd_status fd_read_kv(const void* k_cache, const void* v_cache, const int32_t* kv
              : FD_ERR_CUDA;
 }
 
+size_t fd_assign_pages_workspace_bytes(int batch) {
+  return batch > 0 && batch <= (1 << 24) ? assign_pages_bytes(batch) : 0;
+}
+
+fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const int32_t* seq_len,
+                          const int32_t* new_tokens, int32_t* free_pages, int64_t free_capacity,
+                          const int32_t* free_count, int batch, int page_size, int window,
+                          int sinks, const int32_t* released, int32_t* seq_len_out,
+                          int32_t* free_count_out, int32_t* released_out, int32_t* q_start,
+                          int32_t* positions, int64_t* slots, int64_t num_slots, void* workspace,
+                          size_t workspace_bytes, fd_stream_t stream) {
+  if (!block_table || !seq_len || !new_tokens || !free_pages || !free_count || !seq_len_out ||
+      !free_count_out || !q_start || !positions || !workspace)
+    return FD_ERR_INVALID_ARG;
+  if (batch <= 0 || batch > (1 << 24) || block_table_stride <= 0) return FD_ERR_INVALID_ARG;
+  if (free_capacity <= 0 || free_capacity >= kMaxPacked) return FD_ERR_INVALID_ARG;
+  if ((int64_t)batch * block_table_stride >= kMaxPacked) return FD_ERR_UNSUPPORTED;
+  if (!is_pow2(page_size) || page_size > 256) return FD_ERR_UNSUPPORTED;
+  if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return FD_ERR_INVALID_ARG;
+  if ((window > 0) != (released != nullptr) || (window > 0) != (released_out != nullptr))
+    return FD_ERR_INVALID_ARG;
+  if (num_slots < 0 || num_slots >= kMaxPacked || (!slots && num_slots > 0))
+    return FD_ERR_INVALID_ARG;
+  for (const int32_t* a : {(const int32_t*)block_table, seq_len, new_tokens,
+                           (const int32_t*)free_pages, free_count, released,
+                           (const int32_t*)seq_len_out, (const int32_t*)free_count_out,
+                           (const int32_t*)released_out, (const int32_t*)q_start,
+                           (const int32_t*)positions})
+    if (!aligned(a, 4)) return FD_ERR_INVALID_ARG;
+  if (!aligned(slots, 8) || !aligned(workspace, 256)) return FD_ERR_INVALID_ARG;
+  if (workspace_bytes < assign_pages_bytes(batch)) return FD_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = current_sms();
+  if (sms <= 0) return FD_ERR_CUDA;
+  AssignPages p;
+  std::memset(&p, 0, sizeof(p));
+  p.table = block_table;
+  p.stride = block_table_stride;
+  p.seq_len = seq_len;
+  p.new_tokens = new_tokens;
+  p.free_pages = free_pages;
+  p.capacity = free_capacity;
+  p.free_count = free_count;
+  p.released = released;
+  p.seq_len_out = seq_len_out;
+  p.free_count_out = free_count_out;
+  p.released_out = released_out;
+  p.q_start = q_start;
+  p.positions = positions;
+  static_assert(sizeof(long long) == sizeof(int64_t), "slots");
+  p.slots = reinterpret_cast<long long*>(slots);
+  p.num_slots = num_slots;
+  p.batch = batch;
+  p.page_shift = log2i(page_size);
+  p.window = window;
+  p.keep = (int)(((int64_t)sinks + page_size - 1) / page_size);
+  p.ws = static_cast<WsHeader*>(workspace);
+  return launch_assign_pages(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FD_OK
+             : FD_ERR_CUDA;
+}
+
 size_t fd_prefill_workspace_bytes(int head_dim) {
   if (head_dim != 64 && head_dim != 128) return 0;
   const int sms = current_sms();

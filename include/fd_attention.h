@@ -528,6 +528,70 @@ fd_status fd_read_kv(const void *k_cache, const void *v_cache, const int32_t *kv
                      fd_dtype out_dtype, void *k_out, void *v_out, void *workspace,
                      size_t workspace_bytes, fd_stream_t stream);
 
+/* Scratch bytes fd_assign_pages needs (host function); 0 for an invalid batch. */
+size_t fd_assign_pages_workspace_bytes(int batch);
+
+/*
+ * Pages of one step's requests: grows and shrinks the block tables of a batch by
+ * its requests' new tokens, on the device, and says where the packed new tokens
+ * go.  In the words of the packed calls above: it makes q_start, positions and
+ * seq_len for them.
+ *
+ * Sequence b has L = seq_len[b] tokens cached (negative: 0) in the first
+ * ceil(L / page_size) columns of its row of the table, and gets
+ * n = new_tokens[b] new ones; n < 0 says that it has ended.  Free pages are a
+ * stack, free_pages[0 .. free_count[0]).
+ *
+ * Pages that go back:
+ *   an ended sequence's pages;
+ *   with a window (> 0), of a sequence that goes on the pages that neither its
+ *   new tokens nor later ones see: columns c with c * page_size >= sinks and
+ *   (c + 1) * page_size <= L - window + 1.
+ *   released[b] is the first column that has not gone back so far (0 for a new
+ *   sequence; columns below ceil(sinks / page_size) only go when the sequence
+ *   ends), released_out[b] the one after this call.  The attention entry points
+ *   with this window and these sinks do not use the entries of pages that are
+ *   gone, nor does this one; they are left in the table.
+ * They are put on the stack in order of sequences, then columns.  A page must
+ * belong to one sequence alone (prefix pages that several rows name are not for
+ * this call).  Ids are moved as they are.
+ *
+ * Pages handed out, from the top of the stack with those on it: in order of
+ * sequences, then columns, ceil((L + n) / page_size) - ceil(L / page_size) for
+ * each sequence, as long as they last.  A sequence is served when it needs no
+ * page, or when the pages wanted up to and with it do not pass those there are
+ * (so behind the first that is refused, only such as need none).  A served
+ * sequence has positions[b] = L and seq_len_out[b] = L + n; an ended one -1 and
+ * 0; a refused one -1 and L: the packed append leaves its tokens alone, and it
+ * may ask again.  A sequence whose pages do not fit its row of the table, or
+ * whose tokens do not fit the slots (or end beyond 2^31 - 1, where q_start
+ * stays), is refused and recorded as FD_ERR_DEVICE_BOUNDS, as is a stack that
+ * overflows (its last pages are lost).
+ *
+ * block_table  int32 [batch, block_table_stride], updated: only the columns of
+ *              pages handed out are written. Fewer than 2^31 entries.
+ * free_pages   int32 [free_capacity], updated: entries from free_count on are
+ *              written by pages that go back, others never (a page handed out
+ *              stays where it was, behind the new count).
+ * page_size    power of two in [1, 256].
+ * window, sinks  0, 0: no window; then released and released_out are NULL.
+ * seq_len_out, free_count_out [1], released_out  the state after the call; each
+ *              may be the same array as the one before it.
+ * q_start      int32 [batch + 1]: running sum of max(new_tokens, 0), refused
+ *              sequences' tokens included.
+ * slots        int64 [num_slots], or NULL with 0: entry i is the cache row of
+ *              packed token i, -1 if it is not served, and -1 behind the last.
+ * workspace    >= fd_assign_pages_workspace_bytes(batch), 256-byte aligned.
+ * No array may overlap another, other than the pairs named.
+ */
+fd_status fd_assign_pages(int32_t *block_table, int block_table_stride, const int32_t *seq_len,
+                          const int32_t *new_tokens, int32_t *free_pages, int64_t free_capacity,
+                          const int32_t *free_count, int batch, int page_size, int window,
+                          int sinks, const int32_t *released, int32_t *seq_len_out,
+                          int32_t *free_count_out, int32_t *released_out, int32_t *q_start,
+                          int32_t *positions, int64_t *slots, int64_t num_slots,
+                          void *workspace, size_t workspace_bytes, fd_stream_t stream);
+
 /* Scratch bytes fd_prefill_attention needs on the current device (host
  * function), for any batch, lengths and head counts; 0 for an invalid
  * head_dim. */
