@@ -174,6 +174,7 @@ struct AssignPages {
 
 size_t assign_pages_bytes(int batch);
 cudaError_t launch_assign_pages(AssignPages p, int sms, cudaStream_t stream);
+cudaError_t launch_append_normed(const AppendPacked& p, int sms, cudaStream_t stream);
 cudaError_t launch_append_packed(const AppendPacked& p, int sms, cudaStream_t stream);
 cudaError_t launch_read_kv(const ReadKv& p, int sms, cudaStream_t stream);
 cudaError_t launch_rotary_table(const RotaryTable& p, int sms, cudaStream_t stream);
