@@ -1021,17 +1021,23 @@ __device__ __forceinline__ void fixers(const Prefill& p, Walk<false, WIN> walk, 
         if (!wait_warp(c, p, &c.full[slot], (uint32_t)((e / NS) & 1), 20)) return;
         if (kv == 1 && sight.fix(seg, j)) {
           const int k0 = sight.key(seg, j), valid = sight.valid(seg, j);
-          // rows before it are seen by all (with a window it is asked of each)
-          const int from = WIN ? 0 : max(0, sight.unseen - k0);
+          // rows from here on are not seen by all; with a window also those of a
+          // first range [lo, hi), which is passed in front of them
+          const int from = max(0, min(kTile, sight.unseen - k0));
+          int lo = 0, early = 0;
+          if constexpr (WIN) {
+            lo = max(0, sight.sinks - k0);
+            early = max(0, min(from, sight.any - k0) - lo);
+          }
           uint8_t* v = base + SH::kOffSlot + (size_t)slot * SH::kSlot;
           bool found = false;
-          const int items = (kTile - from) * 8;
+          const int items = (early + kTile - from) * 8;
 #pragma unroll
           for (int d = 0; d < D / 64; ++d) {
 #pragma unroll 2
             for (int i = ft; i < items; i += 64) {
-              const int r = from + (i >> 3);
-              if (WIN && r < valid && !sight.partly(k0 + r)) continue;
+              int r = from + (i >> 3);
+              if constexpr (WIN) r = (i >> 3) < early ? lo + (i >> 3) : r - early;
               uint4* at = reinterpret_cast<uint4*>(v + d * (kTile * 128) + r * 128 + (i & 7) * 16);
               if (r >= valid || sight.hidden(k0 + r)) {
                 *at = make_uint4(0, 0, 0, 0);
@@ -1385,15 +1391,28 @@ struct Softmax {
     }
   }
   // off the straight path: the sign of the scale, and -inf for keys that the
-  // row does not see (from `left` of the 32 on, and [hl, hh) with a window)
-  __device__ __forceinline__ void exclude(float (&x)[32], int left, int hl, int hh) const {
+  // row does not see (from `left` of the 32 on)
+  __device__ __forceinline__ void exclude(float (&x)[32], int left) const {
     if (!TOK && sc <= 0.f) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = sc == 0.f ? 0.f : -x[i];
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      x[i] = i < left && !(WIN && i >= hl && i < hh) ? x[i] : -INFINITY;
+    for (int i = 0; i < 32; ++i) x[i] = i < left ? x[i] : -INFINITY;
+  }
+
+  // The same with a window: `seen` has a bit for every key that the row sees.
+  __device__ __forceinline__ void exclude_but(float (&x)[32], unsigned seen) const {
+    if (!TOK && sc <= 0.f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = sc == 0.f ? 0.f : -x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = seen & (1u << i) ? x[i] : -INFINITY;
+  }
+  // bits 0 .. n - 1
+  static __device__ __forceinline__ unsigned low_bits(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
   }
   __device__ __forceinline__ static void row_max(const float (&x)[32], float (&mx)[4]) {
 #pragma unroll
@@ -1489,11 +1508,28 @@ struct Softmax {
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         float x[32];
+        // with a window, most of an edge tile's blocks of 32 keys are seen or
+        // hidden by all rows of the warp, which lie few tokens apart
+        unsigned seen = 0;
+        if constexpr (WIN) {
+          seen = low_bits(left - 32 * k) & (low_bits(hl - 32 * k) | ~low_bits(hh - 32 * k));
+          if (!TOK && sc > 0.f && __all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+          if (__all_sync(0xffffffffu, seen == 0u)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = -INFINITY;
+            tmem_st32<128>(tS + 32 * k, x);
+            continue;
+          }
+        }
         fetch(tS, x, k);
         tmem_wait_ld();
         arrived(x);
         if constexpr (TOK) key_scales(x, ks + 32 * k);
-        if (!TOK || !whole) exclude(x, left - 32 * k, hl - 32 * k, hh - 32 * k);
+        if constexpr (WIN) {
+          if (!TOK || !whole) exclude_but(x, seen);
+        } else {
+          if (!TOK || !whole) exclude(x, left - 32 * k);
+        }
         tmem_st32<128>(tS + 32 * k, x);
         if constexpr (TOK) row_max(x, mx);
       }
@@ -1603,7 +1639,12 @@ struct Softmax {
     // streams of the two partial slots, for the merge
     int4 used0 = make_int4(-1, 0, 0, 0), used1 = used0;
     bool dead = false;
-    for (; !dead && walk.next(p, seg); sn += seg.te > seg.tb) {
+    // with a window, whose segments are short, the next one is walked to while
+    // the last product of the present one runs
+    Seg ahead;
+    bool more = WIN && walk.next(p, ahead);
+    for (; !dead && (WIN ? more : walk.next(p, seg)); sn += seg.te > seg.tb) {
+      if constexpr (WIN) seg = ahead;
       const int qt = seg.solo ? 0 : X;                     // query tile of this half
       const int tok0 = (2 * seg.m + qt) * p.tile_tokens;   // its first token
       const int live_rows = min(p.tile_tokens, max(0, seg.n - tok0)) * p.group;
@@ -1655,6 +1696,7 @@ struct Softmax {
       if (dead) break;
       n += seg.te - seg.tb;
       // ---------------------------------------------------------- segment end
+      if constexpr (WIN) more = walk.next(p, ahead);
       const bool any = first < te;   // O of this half was accumulated
       if (any) {
         if (!wait_warp(c, p, &c.o_full[X], (uint32_t)(segs & 1), 15)) {
@@ -1721,8 +1763,34 @@ struct Softmax {
         const long long out_at = ((long long)(seg.q0 + tok0 + rtok) * p.num_q_heads +
                                   (long long)seg.h * p.group + rhead) * D;
         const bool sectors = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        const bool plain = WIN && seg.complete && !swap && !nonfinite && any;
+        if (plain) {   // the usual end of a short segment: loads ahead of stores
+          float o[2][32];
+          tmem_ld32<128>(tO, o[0]);
+          const uint64_t q2 = pack2(osc, osc);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            tmem_wait_ld();
+            arrived(o[k & 1]);
+            if (k + 1 < D / 32) tmem_ld32<128>(tO + 32 * (k + 1), o[(k + 1) & 1]);
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = unpack2(mul2(pack2(o[k & 1][2 * i], o[k & 1][2 * i + 1]), q2));
+              v[i] = pack16<BF16>(x.x, x.y);
+            }
+            if (mine) {
+              uint16_t* to = static_cast<uint16_t*>(p.out) + out_at + 32 * k;
+              store32(to, make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7]),
+                      sectors);
+              store32(to + 16, make_uint4(v[8], v[9], v[10], v[11]),
+                      make_uint4(v[12], v[13], v[14], v[15]), sectors);
+            }
+            __syncwarp();
+          }
+        }
 #pragma unroll(D == 64 ? 2 : 1)
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = plain ? D : 0; c0 < D; c0 += 32) {
           float o[32];
           if (any && warp_live) {
             tmem_ld32<128>(tO + c0, o);
