@@ -18,9 +18,11 @@
 // is read (columns that are held, entries below the old count) is never written
 // in the same call.
 //
-// What bounds it: latency.  A step of few tokens runs in one block, its sums in
-// shared memory (one launch); others in two launches, the plan in one block and
-// the fill on all SMs, the second launched as a programmatic dependent.
+// What bounds it: latency.  Small steps run in one block, its sums in shared
+// memory (one launch); others in two launches, the plan in one block and the fill
+// on all SMs, the second launched as a programmatic dependent.  1024 requests
+// with 690000 new tokens (7 MB) take 16.3 us, 5 to 6 of them the plan (19.9 with
+// the sums searched in global memory and the kinds of items one after the other).
 #include "fd_prompt.cuh"
 
 namespace fd {
@@ -28,7 +30,12 @@ namespace {
 
 constexpr int kThreads = 1024;      // of the plan's block
 constexpr int kFillThreads = 256;
-constexpr int kFusedSlots = 8192;   // a block fills as many slots as fast as a second launch
+// One block fills a slot or moves a page about every nanosecond; a second launch
+// costs 1.2 to 1.8 us and fills on all SMs.  One token each of 64 sequences:
+// 5.2 us in one launch, 6.4 in two; of 1024: 8.0 and 9.7; four each: 12.6 and
+// 9.5.  128 ended sequences of 8000 tokens: 60 us and 7.4, so one launch is kept
+// for tables that hold few pages to give back.
+constexpr int kFusedSlots = 2048, kFusedEntries = 4096;
 
 using Rec = PageRec;
 using Totals = PageTotals;
@@ -49,6 +56,20 @@ __device__ __forceinline__ int owner(const int32_t* start, int batch, long long 
   return lo;
 }
 
+// The same for i = first + lane of a whole warp: one search for the warp's first
+// (32 probes at a time), which serves the lanes of the same sequence.
+__device__ __forceinline__ int owner_in_warp(const int32_t* start, int batch, long long first) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && start[at] <= first);
+    lo += (31 - __clz(below)) * step;   // (start[lo] <= first: never empty)
+    hi = min(hi, lo + step);
+  }
+  return first + lane < start[lo + 1] ? lo : owner(start, batch, first + lane);
+}
+
 // Page r of those that go back.
 __device__ __forceinline__ int returned(const AssignPages& p, const Sums& s, long long r) {
   const int b = owner(s.back, p.batch, r);
@@ -64,20 +85,29 @@ __device__ __forceinline__ int handed(const AssignPages& p, const Sums& s, const
   return i < t.count ? p.free_pages[i] : returned(p, s, i - t.count);
 }
 
-// (table and stack are read and written by one launch: plain loads)
+// One range of items, so that no thread passes one kind after the other: slots
+// (whole warps of them), pages handed out, pages that go back.  (Table and stack
+// are read and written by one launch: plain loads.)
 __device__ __forceinline__ void fill(const AssignPages& p, const Sums& s, const Totals& t,
                                      long long first, long long step) {
-  for (long long r = first; r < t.back; r += step)
-    if (t.count + r < p.capacity) p.free_pages[t.count + r] = returned(p, s, r);
-  for (long long k = first; k < t.handed; k += step) {
-    const int b = owner(s.handed, p.batch, k);
-    p.table[(long long)b * p.stride + s.rec[b].held + (k - s.handed[b])] = handed(p, s, t, k);
-  }
-  const long long tokens = s.tokens[p.batch];
-  for (long long i = first; i < p.num_slots; i += step) {
+  const long long tokens = s.tokens[p.batch], slots = (p.num_slots + 31) / 32 * 32;
+  const long long items = slots + t.handed + t.back;
+  for (long long i = first; i - (threadIdx.x & 31) < items; i += step) {
+    if (i >= slots) {
+      const long long k = i - slots, r = k - t.handed;
+      if (k < t.handed) {
+        const int b = owner(s.handed, p.batch, k);
+        p.table[(long long)b * p.stride + s.rec[b].held + (k - s.handed[b])] = handed(p, s, t, k);
+      } else if (r < t.back && t.count + r < p.capacity) {
+        p.free_pages[t.count + r] = returned(p, s, r);
+      }
+      continue;
+    }
     long long slot = -1;
+    // (lane 0's item is a multiple of 32)
+    const long long w = i - (threadIdx.x & 31);
+    const int b = w < tokens ? owner_in_warp(s.tokens, p.batch, w) : 0;
     if (i < tokens) {
-      const int b = owner(s.tokens, p.batch, i);
       const Rec& x = s.rec[b];
       if (x.need >= 0) {
         const int pos = x.L + (int)(i - s.tokens[b]);
@@ -88,7 +118,7 @@ __device__ __forceinline__ void fill(const AssignPages& p, const Sums& s, const 
           slot = ((long long)page << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
       }
     }
-    p.slots[i] = slot;
+    if (i < p.num_slots) p.slots[i] = slot;
   }
 }
 
@@ -246,11 +276,26 @@ __global__ void __launch_bounds__(kThreads) assign_pages_plan(const __grid_const
   if (threadIdx.x == 0) *p.totals = t;
 }
 
+// LOCAL: at most kThreads sequences, whose sums are searched in shared memory.
+template <bool LOCAL>
 __global__ void __launch_bounds__(kFillThreads) assign_pages_fill(const __grid_constant__ AssignPages p) {
+  __shared__ Rec rec[LOCAL ? kThreads : 1];
+  __shared__ int32_t sums[3][LOCAL ? kThreads + 1 : 1];
   wait_prior_grid();
   const Totals t = *p.totals;
-  fill(p, Sums{p.rec, p.back, p.handed, p.q_start}, t,
-       (long long)blockIdx.x * kFillThreads + threadIdx.x, (long long)gridDim.x * kFillThreads);
+  Sums s{p.rec, p.back, p.handed, p.q_start};
+  if constexpr (LOCAL) {
+    for (int b = threadIdx.x; b <= p.batch; b += kFillThreads) {
+      if (b < p.batch) rec[b] = s.rec[b];
+      sums[0][b] = s.back[b];
+      sums[1][b] = s.handed[b];
+      sums[2][b] = s.tokens[b];
+    }
+    s = Sums{rec, sums[0], sums[1], sums[2]};
+    __syncthreads();
+  }
+  fill(p, s, t, (long long)blockIdx.x * kFillThreads + threadIdx.x,
+       (long long)gridDim.x * kFillThreads);
 }
 
 struct Layout {
@@ -272,7 +317,8 @@ Layout layout(int batch) {
 size_t assign_pages_bytes(int batch) { return layout(batch).total; }
 
 cudaError_t launch_assign_pages(AssignPages p, int sms, cudaStream_t stream) {
-  if (p.batch <= kThreads && p.slots && p.num_slots <= kFusedSlots) {
+  if (p.batch <= kThreads && p.slots && p.num_slots <= kFusedSlots &&
+      (long long)p.batch * p.stride <= kFusedEntries) {
     assign_pages_fused<<<1, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
   }
@@ -294,7 +340,8 @@ cudaError_t launch_assign_pages(AssignPages p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, assign_pages_fill, p);
+  return p.batch <= kThreads ? cudaLaunchKernelEx(&cfg, assign_pages_fill<true>, p)
+                             : cudaLaunchKernelEx(&cfg, assign_pages_fill<false>, p);
 }
 
 }  // namespace fd

@@ -356,6 +356,29 @@ __device__ __forceinline__ uint2 widen8x4(uint32_t w) {
   }
 }
 
+// The same for the window kernels, where int8 as bf16 takes eight instructions
+// in place of fourteen: with m the low seven bits, 128 + m is 0x43 above m, and
+// code = (128 + m) - (128 or, with the sign bit set, 256), which is 0x43 above
+// 0x00 or 0x80, the sign bit itself.
+template <int KVT, bool BF16, bool WIN>
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  if constexpr (WIN && KVT == FD_I8 && BF16) {
+    const uint32_t m = w & 0x7F7F7F7Fu, s = w & 0x80808080u;
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a = __byte_perm(m, 0x43u, i ? 0x4342 : 0x4140);
+      const uint32_t b = __byte_perm(s, 0x43u, i ? 0x4342 : 0x4140);
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&b));
+      r[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    return make_uint2(r[0], r[1]);
+  } else {
+    return widen8x4<KVT, BF16>(w);
+  }
+}
+
 // Four int8 codes -> two registers of f16 pairs holding code + 1152 (the
 // sign flip and byte permutation of widen8x4 without its subtraction).  The
 // FLIP form with f16 queries feeds K and V this way: a second product per
@@ -987,8 +1010,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       mma16816<false>(st[mt], ka.x, kb.x, ka.y, kb.y, qb.x, qb.y);
                       mma16816<false>(st[mt], kNeg1152, kNeg1152, kNeg1152, kNeg1152, qb.x, qb.y);
                     } else {
-                      const uint2 ka = widen8x4<KVT, BF16>(w[2 * mt][kk]);       // token r
-                      const uint2 kb = widen8x4<KVT, BF16>(w[2 * mt + 1][kk]);   // token r + 8
+                      const uint2 ka = widen4<KVT, BF16, WIN>(w[2 * mt][kk]);       // token r
+                      const uint2 kb = widen4<KVT, BF16, WIN>(w[2 * mt + 1][kk]);   // token r + 8
                       mma16816<BF16>(st[mt], ka.x, kb.x, ka.y, kb.y, qb.x, qb.y);
                     }
                   }
@@ -1130,10 +1153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         h01 = widen_i8x4_biased(hi01);
                         h89 = widen_i8x4_biased(hi89);
                       } else {
-                        l01 = widen8x4<KVT, BF16>(lo01);
-                        l89 = widen8x4<KVT, BF16>(lo89);
-                        h01 = widen8x4<KVT, BF16>(hi01);
-                        h89 = widen8x4<KVT, BF16>(hi89);
+                        l01 = widen4<KVT, BF16, WIN>(lo01);
+                        l89 = widen4<KVT, BF16, WIN>(lo89);
+                        h01 = widen4<KVT, BF16, WIN>(hi01);
+                        h89 = widen4<KVT, BF16, WIN>(hi89);
                       }
                       mma16816<BF16>(o[2 * wd], l01.x, l01.y, l89.x, l89.y, pb0, pb1);
                       mma16816<BF16>(o[2 * wd + 1], h01.x, h01.y, h89.x, h89.y, pb0, pb1);
@@ -1179,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint4 a = load_qfrag<QROWS>(qf, kk);
 #pragma unroll
                 for (int jn = 0; jn < NJ; ++jn) {
-                  const uint2 kb = widen8x4<KVT, BF16>(w[jn][kk]);
+                  const uint2 kb = widen4<KVT, BF16, WIN>(w[jn][kk]);
                   mma16816<BF16>(s[jn], a.x, a.y, a.z, a.w, kb.x, kb.y);
                 }
               }
@@ -1195,7 +1218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint4 a = load_qfrag<QROWS>(qf, kk);
 #pragma unroll
                 for (int jn = 0; jn < NJ; ++jn) {
-                  const uint2 kb = widen8x4<KVT, BF16>(w[jn][kk]);
+                  const uint2 kb = widen4<KVT, BF16, WIN>(w[jn][kk]);
                   mma16816<BF16>(s[jn], a.x, a.y, a.z, a.w, kb.x, kb.y);
                 }
               }
@@ -1346,8 +1369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t hi01 = __byte_perm(A[wd], B[wd], 0x7362);
                   const uint32_t lo89 = __byte_perm(C[wd], E[wd], 0x5140);
                   const uint32_t hi89 = __byte_perm(C[wd], E[wd], 0x7362);
-                  const uint2 l01 = widen8x4<KVT, BF16>(lo01), l89 = widen8x4<KVT, BF16>(lo89);
-                  const uint2 h01 = widen8x4<KVT, BF16>(hi01), h89 = widen8x4<KVT, BF16>(hi89);
+                  const uint2 l01 = widen4<KVT, BF16, WIN>(lo01), l89 = widen4<KVT, BF16, WIN>(lo89);
+                  const uint2 h01 = widen4<KVT, BF16, WIN>(hi01), h89 = widen4<KVT, BF16, WIN>(hi89);
                   mma16816<BF16>(o[4 * wd + 0], pa0, pa1, pa2, pa3, l01.x, l89.x);
                   mma16816<BF16>(o[4 * wd + 1], pa0, pa1, pa2, pa3, l01.y, l89.y);
                   mma16816<BF16>(o[4 * wd + 2], pa0, pa1, pa2, pa3, h01.x, h89.x);
@@ -1372,8 +1395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t hi01 = __byte_perm(A[wd], B[wd], 0x7362);
                   const uint32_t lo89 = __byte_perm(C[wd], E[wd], 0x5140);
                   const uint32_t hi89 = __byte_perm(C[wd], E[wd], 0x7362);
-                  const uint2 l01 = widen8x4<KVT, BF16>(lo01), l89 = widen8x4<KVT, BF16>(lo89);
-                  const uint2 h01 = widen8x4<KVT, BF16>(hi01), h89 = widen8x4<KVT, BF16>(hi89);
+                  const uint2 l01 = widen4<KVT, BF16, WIN>(lo01), l89 = widen4<KVT, BF16, WIN>(lo89);
+                  const uint2 h01 = widen4<KVT, BF16, WIN>(hi01), h89 = widen4<KVT, BF16, WIN>(hi89);
                   mma16816<BF16>(o[4 * wd + 0], pa0, pa1, pa2, pa3, l01.x, l89.x);
                   mma16816<BF16>(o[4 * wd + 1], pa0, pa1, pa2, pa3, l01.y, l89.y);
                   mma16816<BF16>(o[4 * wd + 2], pa0, pa1, pa2, pa3, h01.x, h89.x);
