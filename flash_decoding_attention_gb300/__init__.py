@@ -476,7 +476,8 @@ def fd_append_kv_normed(q, q_stride: int, q_out, k_new, v_new, kv_stride: int, k
         0 if rotary is None else rotary.shape[0], rot_dim, 1 if interleaved else 0, _ptr(q_norm),
         _ptr(k_norm), 1 if norm_f32 else 0, norm_eps, _ptr(axis_positions),
         0 if axis_positions is None else axis_positions.shape[0],
-        0 if axis_positions is None else axis_positions.stride(0), pair_axis, k_scale, v_scale,
+        0 if axis_positions is None else max(axis_positions.stride(0), num_tokens), pair_axis,
+        k_scale, v_scale,
         scale_kind, _ptr(k_scales), _ptr(v_scales),
         _q_dtype(k_new) if new_dtype is None else new_dtype,
         _kv_dtype(k_cache) if kv_dtype is None else kv_dtype,
@@ -752,8 +753,9 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 
 
 def _window_sizes(window, sinks) -> None:
-    if window < 1 or sinks < 0:
-        raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")
+    if not (1 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError(f"window must be at least 1 and sinks at least 0 (both below 2^31), got "
+                         f"{window} and {sinks}")
 
 
 def _decode_window(q, k_cache, v_cache, seq_len, kv_start_idx, block_table, softmax_scale, k_scale,
@@ -941,6 +943,8 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
     themselves."""
     if not block_table.is_cuda:
         raise ValueError(f"the block table must be on a GPU, got {block_table.device}")
+    if not 1 <= page_size <= 256:
+        raise ValueError(f"page_size must be a power of two in [1, 256], got {page_size}")
     dev, at = block_table.device, block_table.get_device()
     batch = seq_len.shape[0]
     _index("block_table", block_table, batch, at, 2)
@@ -1047,7 +1051,8 @@ def _norms_and_axes(q, k_new, D: int, at: int, rotary, q_norm, k_norm, axis_posi
             raise ValueError("axis_positions needs rotary and pair_axes")
         shape, n = axis_positions.shape, k_new.shape[0]
         if len(shape) != 2 or shape[1] != n or axis_positions.dtype != torch.int32 or \
-                (n > 1 and axis_positions.stride(1) != 1) or axis_positions.stride(0) < n:
+                (n > 1 and axis_positions.stride(1) != 1) or \
+                (shape[0] > 1 and axis_positions.stride(0) < n):
             raise ValueError(f"axis_positions must be int32 [axes, {n}] with dense rows, got "
                              f"{axis_positions.dtype} {tuple(shape)}")
         axes = pair_axes if isinstance(pair_axes, bytes) else bytes(list(pair_axes))

@@ -426,8 +426,8 @@ static fd_status decode_impl(const void* q, const void* k_cache, const void* v_c
   p.q_len = q_len;
   if (window) {
     p.window = window;
-    // more first tokens than any sequence has are all of them
-    p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+    // (so that whole tiles of them are still an int; no cache holds more)
+    p.sinks = sinks < 0x7fffff00 ? sinks : 0x7fffff00;
     p.sink_tokens = (p.sinks + c.tile - 1) / c.tile * c.tile;
     p.win_align = !paged ? 1 : page_size < c.tile ? page_size : c.tile;
   }

@@ -462,8 +462,8 @@ static fd_status prefill_impl(const void* q, int64_t q_stride, const void* k_cac
   p.q_dtype = q_dtype;
   p.kv_dtype = kv_dtype;
   p.window = window;
-  // more first tokens than any sequence has are all of them
-  p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  // (so that whole tiles of them are still an int; longer sequences are refused)
+  p.sinks = sinks < 0x7fffff00 ? sinks : 0x7fffff00;
   p.wait_ns = wait_limit_ns();
   p.starve = starve_switch();
   p.grid = sms;

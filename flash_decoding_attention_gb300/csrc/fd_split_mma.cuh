@@ -650,7 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             win_hi = min(pg_lo + kPageWindow, last);
             __syncwarp();
             for (int k = lane; k < win_hi - win_lo; k += 32)
-              sm.pages[k] = __ldg(p.block_table + (long long)b * p.bt_stride + win_lo + k);
+              sm.pages[k] = WIN && win_lo + k >= p.bt_stride
+                                ? -1
+                                : __ldg(p.block_table + (long long)b * p.bt_stride + win_lo + k);
             __syncwarp();
           }
         }

@@ -308,6 +308,8 @@ fd_status fd_decode_attention_append(const void *q, const void *k_new, const voi
  * without (k_new, v_new and positions NULL) the caches hold it and are only
  * read.
  *
+ * A sequence longer than its row of the block table is recorded as
+ * FD_ERR_DEVICE_BOUNDS, and the tiles past the row's end are absent.
  * Block-table entries of pages none of whose tokens the query sees are not
  * used, so such pages may have been given away (fd_assign_pages does that) and
  * their entries may hold anything.  Rows of hidden tokens have no effect,

@@ -205,6 +205,33 @@ def test_decode_rows_outside_the_cache():
     assert fda.fd_check_device_error(wsp) == (fda.FD_ERR_DEVICE_BOUNDS, -7)
 
 
+def test_decode_sequences_longer_than_their_row_of_the_table():
+    """What lies past the row's end is absent and recorded, the first tokens are
+    seen; the next sequence's entries, which follow in memory, are not read."""
+    fda = lib()
+    for page, d in ((16, 128), (2, 64), (64, 128)):
+        bt = ref.Batch([1, 1], [8 * page - 1, 5], 2, d, "f16", page, seed=1)
+        f = ref.Filled(bt, seed=1)
+        q = _queries(bt, 16, "f16", 1)
+        want, wlse = wref.attention(f, q, 16, d ** -0.5, 7, 3)
+        ws = fda.alloc_workspace(2, 16, 2, d)
+        kw = f.device(DEV)
+        args = (q.to(DEV), kw.pop("k_cache"), kw.pop("v_cache"))
+        out, lse = fda.decode_attention(
+            *args, torch.tensor([4000 * page, 6], dtype=torch.int32, device=DEV), window=7, sinks=3,
+            workspace=ws, **kw, **bt.index(DEV))
+        torch.cuda.synchronize()
+        assert fda.fd_check_device_error(ws)[0] == fda.FD_ERR_DEVICE_BOUNDS
+        s = torch.einsum("hd,khd->hk", q[0].double(),
+                         f.val["k"][bt.rows_of(0, 0, 3)].repeat_interleave(8, 1)) / d ** 0.5
+        only = torch.einsum("hk,khd->hd", s.softmax(-1),
+                            f.val["v"][bt.rows_of(0, 0, 3)].repeat_interleave(8, 1))
+        tol = (2.0 ** -11 + 2.0 ** -18) * 5.5 + 2.0 ** -11 * only.abs()
+        assert torch.all((out[0].double().cpu() - only).abs() <= tol)
+        tol = (2.0 ** -11 + 2.0 ** -18) * 5.5 + 2.0 ** -11 * want[1].abs()
+        assert torch.all((out[1].double().cpu() - want[1]).abs() <= tol)
+
+
 def test_forced_kernels():
     fda = lib()
     bt = ref.Batch([1, 1], [80, 300], 2, 128, "e4m3", 0, seed=1)

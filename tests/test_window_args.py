@@ -73,7 +73,8 @@ def test_wrapper_refusals():
         fda.decode_attention(q, k, k, i, kv_start_idx=i, sinks=4)
     with pytest.raises(ValueError, match="give window"):
         fda.prefill_attention(q, k, k, t(3, dtype=torch.int32), i, kv_start_idx=i, sinks=4)
-    for bad in (dict(window=0), dict(window=-5), dict(window=3, sinks=-1)):
+    for bad in (dict(window=0), dict(window=-5), dict(window=3, sinks=-1),
+                dict(window=(1 << 32) + 5), dict(window=3, sinks=1 << 32)):
         with pytest.raises(ValueError, match="window must be"):
             fda.decode_attention(q, k, k, i, kv_start_idx=i, **bad)
         with pytest.raises(ValueError, match="window must be"):
