@@ -15,19 +15,28 @@
 // element for the sum.
 //
 // An axis only changes which row of the table a pair's cosine and sine come from.
-// A block gathers them for its few tokens into shared memory first.
+// A block gathers them for its few tokens into shared memory first.  Blocks are
+// small, so that some look their tokens up while others work.
 //
-// Everything is read and written once: DRAM traffic is the floor.
+// Everything is read and written once: DRAM traffic is the floor.  21000 tokens of
+// 32 query and 8 KV heads of 128, bf16 into bf16 with both norms (528 MB both
+// ways), take 113 us, 4.7 TB/s (the plain append 6.0): issue slots are two thirds
+// busy, a third of them with the exact sum and the division, and 24 warps an SM
+// do not hide the rest.  Without norms (64 registers, 32 warps) 10000 tokens of 16
+// and 4 heads (123 MB) take 27 us, 4.6 TB/s; 64 tokens 4.7 us, a launch and five
+// dependent loads.  What did not pay: 128 registers and four heads in flight (171
+// us for those 528 MB), 64 and spills (131), persistent blocks with a warp that
+// looks tokens up for the others (136).
 #include "fd_append_packed.cuh"
 
 namespace fd {
 namespace {
 
-constexpr int kThreads = 256;    // of a block at most
+constexpr int kThreads = 128;    // of a block at most (256: 1 to 4 % slower)
 // Blocks of that size on an SM: 80 registers a thread, or 64 with axes alone
 template <bool NORM>
-constexpr int kBlocks = NORM ? 3 : 4;
-constexpr int kMaxTokens = 8;    // of a block
+constexpr int kBlocks = NORM ? 6 : 8;
+constexpr int kMaxTokens = 4;    // of a block
 constexpr int kMaxAxes = 4;
 
 // Eight 16-bit elements <-> four pairs of fp32.
@@ -357,13 +366,12 @@ cudaError_t launch_d(const AppendPacked& p, int sms, cudaStream_t stream) {
   // Blocks enough to fill the SMs: several tokens a block when there are many,
   // several blocks a token when there are few.
   const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  // (four blocks of the usual six warps fit an SM: tokens a block so that its
-  // share of them is a whole number of rounds)
-  const int room = 4 * sms, rounds = (int)(((long long)p.tokens + room * kMaxTokens - 1) /
-                                           (room * kMaxTokens));
-  const int per_block = (int)(((long long)p.tokens + (long long)rounds * room - 1) /
-                              ((long long)rounds * room));
-  const int blocks = (p.tokens + per_block - 1) / per_block;
+  // (as many tokens a block as make a whole number of rounds of the GPU)
+  const bool norm = p.q_norm || p.k_norm;
+  const long long room = (norm ? kBlocks<true> : kBlocks<false>) * sms;
+  const long long rounds = (p.tokens + room * kMaxTokens - 1) / (room * kMaxTokens);
+  const int per_block = (int)((p.tokens + rounds * room - 1) / (rounds * room));
+  const int blocks = (int)(((long long)p.tokens + per_block - 1) / per_block);
   const int warps_token = (heads * (D / 16) + 31) / 32;   // warps of one token
   int parts = blocks >= 4 * sms ? 1 : (4 * sms + blocks - 1) / blocks;
   const int most = (warps_token + 3) / 4;                 // parts of four warps at least
@@ -373,7 +381,6 @@ cudaError_t launch_d(const AppendPacked& p, int sms, cudaStream_t stream) {
   const int passes = (warps_part + kThreads / 32 - 1) / (kThreads / 32);
   const int warps = (warps_part + passes - 1) / passes;
   const dim3 grid((unsigned)blocks, (unsigned)parts);
-  const bool norm = p.q_norm || p.k_norm;
   const auto kern = p.interleaved ? (norm ? append_normed_kernel<XT, KVT, D, true, true>
                                           : append_normed_kernel<XT, KVT, D, true, false>)
                                   : (norm ? append_normed_kernel<XT, KVT, D, false, true>
