@@ -559,7 +559,8 @@ def _own(s):
             s["workspace"] = fda.alloc_page_workspace(c["batch"])
         step = fda.assign_pages(s["block_table"], s["seq_len"], s["new_tokens"], s["free_pages"],
                                 s["free_count"], c["page"], num_slots=s["slots"],
-                                window=c["window"] or None, sinks=c["sinks"],
+                                window=c["window"] or None,
+                                sinks=c["sinks"] if c["window"] else 0,
                                 released=s["released"], workspace=s["workspace"])
         res = {"q_start": step.q_start, "positions": step.positions, "seq_len": step.seq_len,
                "free_count": step.free_count, "block_table": s["block_table"],
