@@ -20,7 +20,7 @@
 //
 // Everything is read and written once: DRAM traffic is the floor.  21000 tokens of
 // 32 query and 8 KV heads of 128, bf16 into bf16 with both norms (528 MB both
-// ways), take 113 us, 4.7 TB/s (the plain append 6.0): issue slots are two thirds
+// ways), take 110 us, 4.8 TB/s (the plain append 6.0): issue slots are two thirds
 // busy, a third of them with the exact sum and the division, and 24 warps an SM
 // do not hide the rest.  Without norms (64 registers, 32 warps) 10000 tokens of 16
 // and 4 heads (123 MB) take 27 us, 4.6 TB/s; 64 tokens 4.7 us, a launch and five
@@ -99,7 +99,7 @@ __device__ __forceinline__ float norm_factor(const uint64_t* a, const uint64_t* 
   }
   // past fp32's range (or with a NaN) the errors are NaN: the sum is what it is
   const float sum = fabsf(s) < INFINITY ? __fadd_rn(s, e) : s;
-  return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / D), eps)));
+  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / D), eps)));
 }
 
 // a + b and a - b of two products, each rounded by itself (ptxas 13.0 fuses a
@@ -136,11 +136,11 @@ __device__ __forceinline__ void rotate(uint64_t* a, uint64_t* b, const float* cs
       }
     }
   } else {
-    const float* at = cs + 8 * u;
+    const float* at = cs + 4 * u;   // (see turn_at)
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(at + 2 * i);
-      const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(at + half + 2 * i);
+      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(at + i * half / 4);
+      const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(at + half + i * half / 4);
       const uint64_t x0 = a[i], y0 = b[i], x1 = a[i + 1], y1 = b[i + 1];
       a[i] = difference_apart(mul2(x0, c.x), mul2(y0, s.x));
       b[i] = sum_apart(mul2(y0, c.x), mul2(x0, s.x));
@@ -148,6 +148,15 @@ __device__ __forceinline__ void rotate(uint64_t* a, uint64_t* b, const float* cs
       b[i + 1] = sum_apart(mul2(y1, c.y), mul2(x1, s.y));
     }
   }
+}
+
+// Where a pair's cosine lies among the token's (its sine as far behind them): a
+// thread's eight pairs half the rotated part apart are two quads, whose first
+// ones lie behind one another and so do the second ones (read 16 bytes a lane
+// without bank conflicts).
+template <bool INTERLEAVED>
+__device__ __forceinline__ int turn_at(int pair, int half) {
+  return INTERLEAVED ? pair : ((pair >> 2) & 1) * (half / 2) + ((pair >> 3) << 2) + (pair & 3);
 }
 
 struct TokenAt {
@@ -267,8 +276,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<NORM>)
     if (at[k].row < 0) continue;
     const int axis = p.num_axes > 0 ? p.pair_axis[pair] : 0;
     const float* row = p.rotary + (long long)at[k].pos[axis] * p.rot_dim + pair;
-    turns_of[k][pair] = __ldg(row);
-    turns_of[k][half + pair] = __ldg(row + half);
+    const int to = turn_at<INTERLEAVED>(pair, half);
+    turns_of[k][to] = __ldg(row);
+    turns_of[k][half + to] = __ldg(row + half);
   }
   __syncthreads();
 
