@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<NORM>)
         const int e = k < 4 ? ea + 2 * k : eb + 2 * (k - 4);
         float2 v;
         if (p.norm_f32) {
-          v = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(norm) + e));
+          // (one by one: weights may start at any element of a larger array)
+          const float* x = static_cast<const float*>(norm) + e;
+          v = make_float2(__ldg(x), __ldg(x + 1));
         } else {
           const XT* x = static_cast<const XT*>(norm) + e;
           v = make_float2(QType<XT>::to_f32(x[0]), QType<XT>::to_f32(x[1]));

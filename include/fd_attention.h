@@ -475,7 +475,7 @@ fd_status fd_append_kv_packed(const void *q, int64_t q_stride, void *q_out, cons
  * beyond fp32's range is infinite: finite elements become zero.)
  *
  * q_norm, k_norm  device arrays [head_dim] of new_dtype, or of fp32 with
- *             norm_f32 non-zero; q_norm needs q.
+ *             norm_f32 non-zero, aligned to their elements; q_norm needs q.
  * norm_eps    finite, > 0 (ignored without q_norm and k_norm).
  * axis_positions  device int32 [num_axes], axis_stride apart: entry i of axis a
  *             is packed token i's position on it.  Pair i of the rotation takes

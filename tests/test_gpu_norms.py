@@ -190,6 +190,31 @@ def test_rows_at_the_ends_of_the_range():
         assert torch.all(kc == 0)
 
 
+@pytest.mark.parametrize("wt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_weights_inside_a_larger_array(wt, at):
+    """Weights that start at any element give what the same ones by themselves do."""
+    fda = lib()
+    bt = ref.Batch([9, 40], [0, 3], 2, 128, "bf16", 16, seed=5)
+    g = torch.Generator().manual_seed(at)
+    q, k = (torch.randn((bt.tokens, h, 128), generator=g).to(torch.bfloat16).to(DEV)
+            for h in (4, 2))
+    room = torch.randn((2, 128 + at), generator=g).to(wt).to(DEV)
+    wq, wk = room.reshape(-1)[at:at + 128], room.reshape(-1)[at + 128:at + 256]
+    assert wq.data_ptr() % 16 == at * wt.itemsize
+    got = []
+    for a, b in ((wq, wk), (wq.clone(), wk.clone())):
+        kc, vc = (torch.zeros(bt.shape(), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        ws = fda.alloc_prefill_workspace(128)
+        out = fda.append_kv(k, k, kc, vc, torch.from_numpy(bt.q_start).to(DEV),
+                            torch.tensor([0, 3], dtype=torch.int32, device=DEV), q=q,
+                            q_norm=a, k_norm=b, workspace=ws, **bt.index(DEV))
+        _ok(fda, ws)
+        got.append((out, kc, vc))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_in_place_queries():
     fda = lib()
     g = torch.Generator().manual_seed(1)
