@@ -369,6 +369,32 @@ fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const in
     if (!aligned(a, 4)) return FD_ERR_INVALID_ARG;
   if (!aligned(slots, 8) || !aligned(workspace, 256)) return FD_ERR_INVALID_ARG;
   if (workspace_bytes < assign_pages_bytes(batch)) return FD_ERR_WORKSPACE_TOO_SMALL;
+  // Arrays lie apart, but for a state that takes the old one's place (starts
+  // overwritten by another array would send the fill outside the table).
+  const struct {
+    const void* at;
+    int64_t bytes;
+    int old;   // entry whose array this one may be
+  } all[] = {
+      {seq_len, 4ll * batch, -1},
+      {new_tokens, 4ll * batch, -1},
+      {free_count, 4, -1},
+      {released, 4ll * batch, -1},
+      {block_table, 4ll * batch * block_table_stride, -1},   // from here on written
+      {free_pages, 4 * free_capacity, -1},
+      {seq_len_out, 4ll * batch, 0},
+      {free_count_out, 4, 2},
+      {released_out, 4ll * batch, 3},
+      {q_start, 4 * (batch + 1ll), -1},
+      {positions, 4ll * batch, -1},
+      {slots, 8 * num_slots, -1},
+      {workspace, (int64_t)assign_pages_bytes(batch), -1},
+  };
+  for (int i = 4; i < (int)(sizeof(all) / sizeof(all[0])); ++i)
+    for (int j = 0; j < i; ++j)
+      if (all[i].at && all[j].at && !(all[i].old == j && all[i].at == all[j].at) &&
+          all[i].bytes > 0 && overlap(all[i].at, all[i].bytes, all[j].at, all[j].bytes, 0, 1))
+        return FD_ERR_INVALID_ARG;
   const int sms = current_sms();
   if (sms <= 0) return FD_ERR_CUDA;
   AssignPages p;

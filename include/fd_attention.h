@@ -584,7 +584,7 @@ size_t fd_assign_pages_workspace_bytes(int batch);
  * slots        int64 [num_slots], or NULL with 0: entry i is the cache row of
  *              packed token i, -1 if it is not served, and -1 behind the last.
  * workspace    >= fd_assign_pages_workspace_bytes(batch), 256-byte aligned.
- * No array may overlap another, other than the pairs named.
+ * No array may overlap another, other than the pairs named (FD_ERR_INVALID_ARG).
  */
 fd_status fd_assign_pages(int32_t *block_table, int block_table_stride, const int32_t *seq_len,
                           const int32_t *new_tokens, int32_t *free_pages, int64_t free_capacity,

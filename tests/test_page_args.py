@@ -40,6 +40,21 @@ def test_refusals(c, over, status):
     assert _call(c, **over) == status
 
 
+WIN = dict(win=4, sinks=1, rel=0xC000, ro=0xD000)
+
+
+@pytest.mark.parametrize("over", [
+    dict(qs=0x2000), dict(qs=0x2004), dict(pos=0x8008), dict(pos=0x3000), dict(slo=0x3000),
+    dict(slo=0x2004), dict(slo=0x6000, pos=0x6004), dict(co=0x2000), dict(co=0x3004),
+    dict(slots=0x8000), dict(slots=0x1000 - 8), dict(free=0x101C), dict(free=0x9000 - 396),
+    dict(bt=0x4000), dict(ws=0x8000, qs=0x8400), dict(count=0x418C), dict(co=0x418C),
+    dict(WIN, ro=0x2000), dict(WIN, ro=0xC004), dict(WIN, slo=0xC000), dict(WIN, qs=0xD004),
+])
+def test_arrays_lie_apart(c, over):
+    """Two written arrays, or a written and a read one, that share an element."""
+    assert _call(c, **over) == 1
+
+
 def test_workspace_bytes(c):
     assert c.fd_assign_pages_workspace_bytes(0) == 0
     assert c.fd_assign_pages_workspace_bytes((1 << 24) + 1) == 0
