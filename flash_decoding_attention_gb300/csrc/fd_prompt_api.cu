@@ -174,7 +174,7 @@ static fd_status append_impl(const void* q, int64_t q_stride, void* q_out, const
     if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return FD_ERR_UNSUPPORTED;
   }
   if (x.q_norm || x.k_norm) {
-    if (x.q_norm && !q) return FD_ERR_INVALID_ARG;
+    if (x.q_norm && !q && num_tokens > 0) return FD_ERR_INVALID_ARG;
     const size_t elem = x.norm_f32 ? 4 : 2;
     if (!aligned(x.q_norm, elem) || !aligned(x.k_norm, elem)) return FD_ERR_INVALID_ARG;
     if (!std::isfinite(x.norm_eps) || !(x.norm_eps > 0.f)) return FD_ERR_INVALID_ARG;

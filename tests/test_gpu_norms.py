@@ -282,6 +282,24 @@ def test_the_prompt_call_norms_and_turns_on_axes():
         assert not torch.equal(q2, q)
 
 
+def test_a_step_without_tokens():
+    """Norms, axes and a window with nothing to do: empty results, caches as they were."""
+    fda = lib()
+    kc, vc = (torch.full((16, 2, 64), 3.0, dtype=torch.float16, device=DEV) for _ in range(2))
+    q, k = (torch.zeros((0, h, 64), dtype=torch.float16, device=DEV) for h in (4, 2))
+    w, tab = torch.ones(64, dtype=torch.float16, device=DEV), fda.rotary_table(16, 32)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    starts, zeros = torch.zeros(3, **i32), torch.zeros(2, **i32)
+    kw = dict(q_norm=w, k_norm=w, rotary=tab, axis_positions=torch.zeros((2, 0), **i32),
+              pair_axes=[0, 1] * 8, kv_start_idx=torch.tensor([0, 8], **i32))
+    assert fda.append_kv(k, k, kc, vc, starts, zeros, q=q, **kw).shape == (0, 4, 64)
+    for window in (None, 5):
+        out, lse = fda.prefill_attention(q, kc, vc, starts, zeros, k_new=k, v_new=k,
+                                         positions=zeros, window=window, **kw)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert torch.all(kc == 3) and torch.all(vc == 3)
+
+
 def test_append_in_a_graph_and_on_another_stream():
     fda = lib()
     n, i32 = 50, dict(dtype=torch.int32, device=DEV)

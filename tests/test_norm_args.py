@@ -44,6 +44,8 @@ def test_refusals(c, over, status):
 def test_nothing_to_do_is_ok(c):
     assert _append(c, n=0) == 0
     assert _append(c, n=0, ap=None, ast=0) == 0
+    # (a tensor of no tokens has no address)
+    assert _append(c, n=0, q=None, qo=None, kn=None, vn=None, ap=None, ast=0) == 0
 
 
 def test_wrapper_refusals():
