@@ -68,7 +68,8 @@ EXPORTED = [
     "fd_debug_set_wait_limit", "fd_debug_plan_segments",
     "fd_rotary_table", "fd_append_kv_packed", "fd_read_kv", "fd_prefill_workspace_bytes",
     "fd_prefill_attention", "fd_decode_attention_window", "fd_prefill_attention_window",
-    "fd_append_kv_normed", "fd_assign_pages", "fd_assign_pages_workspace_bytes",
+    "fd_append_kv_normed", "fd_assign_pages", "fd_assign_pages_attended",
+    "fd_assign_pages_workspace_bytes",
 ]
 
 
@@ -165,6 +166,9 @@ def load_library(path: Optional[str] = None):
         lib.fd_assign_pages.restype = i32
         lib.fd_assign_pages.argtypes = [vp, i32, vp, vp, vp, i64, vp, i32, i32, i32, i32, vp, vp,
                                         vp, vp, vp, vp, vp, i64, vp, sz, vp]
+        lib.fd_assign_pages_attended.restype = i32
+        lib.fd_assign_pages_attended.argtypes = (lib.fd_assign_pages.argtypes[:19] + [vp] +
+                                                 lib.fd_assign_pages.argtypes[19:])
         lib.fd_append_kv_normed.restype = i32
         lib.fd_append_kv_normed.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, i32, vp, vp,
                                             i64, i64, i32, i32, i32, i32, i32, vp, i64, i32, i32,
@@ -527,6 +531,23 @@ def fd_assign_pages(block_table, seq_len, new_tokens, free_pages, free_count, pa
     return st
 
 
+def fd_assign_pages_attended(block_table, seq_len, new_tokens, free_pages, free_count,
+                             page_size: int, window: int, sinks: int, released, seq_len_out,
+                             free_count_out, released_out, q_start, positions, slots, attend_len,
+                             workspace, stream=None, check: bool = True) -> int:
+    """fd_assign_pages with the attention's lengths (``attend_len``, or None)."""
+    st = (_lib or load_library()).fd_assign_pages_attended(
+        block_table.data_ptr(), block_table.shape[1], seq_len.data_ptr(), new_tokens.data_ptr(),
+        free_pages.data_ptr(), free_pages.shape[0], free_count.data_ptr(), seq_len.shape[0],
+        page_size, window, sinks, _ptr(released), seq_len_out.data_ptr(),
+        free_count_out.data_ptr(), _ptr(released_out), q_start.data_ptr(), positions.data_ptr(),
+        _ptr(slots), 0 if slots is None else slots.shape[0], _ptr(attend_len),
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
+    if check and st != FD_OK:
+        raise FdError(st, "fd_assign_pages_attended")
+    return st
+
+
 def fd_prefill_workspace_bytes(head_dim: int) -> int:
     return int(load_library().fd_prefill_workspace_bytes(int(head_dim)))
 
@@ -702,7 +723,8 @@ def decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ``positions`` holds the first new token's index.  With ``window`` the query
     sees its sequence's last ``window`` tokens, itself among them, and the first
     ``sinks`` ones (3-d ``q`` only; several query tokens with a window are
-    ``prefill_attention``'s)."""
+    ``prefill_attention``'s); behind ``assign_pages``, ``seq_len`` is its
+    ``attend_len``."""
     if window is not None:
         return _decode_window(q, k_cache, v_cache, seq_len, kv_start_idx, block_table,
                               softmax_scale, k_scale, v_scale, workspace, out, lse, stream,
@@ -909,6 +931,7 @@ class PageStep(NamedTuple):
     free_count: torch.Tensor           # int32 [1]: pages left on the stack
     released: Optional[torch.Tensor]   # int32 [B]: first column not given back (with a window)
     slots: Optional[torch.Tensor]      # int64 [num_slots]: cache row of every packed token, or -1
+    attend_len: Optional[torch.Tensor]   # int32 [B]: seq_len for this step's attention (with a window)
 
 
 def alloc_page_workspace(batch: int, device=None) -> torch.Tensor:
@@ -928,7 +951,7 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
                  released_out: Optional[torch.Tensor] = None,
                  q_start: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
                  slots: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                 stream=None) -> PageStep:
+                 stream=None, attend_len: Optional[torch.Tensor] = None) -> PageStep:
     """One step's page bookkeeping on the device: sequence b's ``seq_len[b]``
     cached tokens become ``seq_len[b] + new_tokens[b]`` (int32 [B] both; a
     negative number ends the sequence), pages come from and go back to the stack
@@ -939,7 +962,10 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
 
     With ``window`` (and ``sinks``) pages that no later token sees go back as
     well; ``released`` (int32 [B], zeros for new sequences) is kept from step to
-    step.  The ``_out`` arrays default to fresh ones and may be the inputs
+    step.  Pages that earlier tokens still see may be among them, so the step's
+    attention takes ``attend_len`` as its lengths: those of the served sequences
+    with new tokens, 0 of refused, ended and idle ones, whose rows it leaves zero
+    (lse -inf).  (Without a window it is made only where given.)  The ``_out`` arrays default to fresh ones and may be the inputs
     themselves."""
     if not block_table.is_cuda:
         raise ValueError(f"the block table must be on a GPU, got {block_table.device}")
@@ -961,7 +987,7 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
         raise ValueError("sinks and released belong to a window: give window")
     for name, t, n in (("seq_len_out", seq_len_out, batch), ("free_count_out", free_count_out, 1),
                        ("released_out", released_out, batch), ("q_start", q_start, batch + 1),
-                       ("positions", positions, batch)):
+                       ("positions", positions, batch), ("attend_len", attend_len, batch)):
         if t is not None:
             _index(name, t, n, at)
     if slots is not None and (slots.dtype != torch.int64 or slots.dim() != 1 or
@@ -975,8 +1001,11 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
             seq_len_out = torch.empty(batch, **i32)
         if free_count_out is None:
             free_count_out = torch.empty(1, **i32)
-        if released_out is None and window is not None:
-            released_out = torch.empty(batch, **i32)
+        if window is not None:
+            if released_out is None:
+                released_out = torch.empty(batch, **i32)
+            if attend_len is None:
+                attend_len = torch.empty(batch, **i32)
         if q_start is None:
             q_start = torch.empty(batch + 1, **i32)
         if positions is None:
@@ -985,10 +1014,12 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
             slots = torch.empty(num_slots, dtype=torch.int64, device=dev)
         if workspace is None:
             workspace = alloc_page_workspace(batch, dev)
-        fd_assign_pages(block_table, seq_len, new_tokens, free_pages, free_count, page_size,
-                        window or 0, sinks, released, seq_len_out, free_count_out, released_out,
-                        q_start, positions, slots, workspace)
-    return PageStep(q_start, positions, seq_len_out, free_count_out, released_out, slots)
+        fd_assign_pages_attended(block_table, seq_len, new_tokens, free_pages, free_count,
+                                 page_size, window or 0, sinks, released, seq_len_out,
+                                 free_count_out, released_out, q_start, positions, slots,
+                                 attend_len, workspace)
+    return PageStep(q_start, positions, seq_len_out, free_count_out, released_out, slots,
+                    attend_len)
 
 
 def alloc_prefill_workspace(head_dim: int, device=None) -> torch.Tensor:
@@ -1219,7 +1250,9 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     undefined (zero and -inf where ``seq_len`` gives them no key).  Without
     ``k_new`` the caches hold the new tokens already and ``q`` is taken as it
     is.  With ``window`` a token sees the last ``window`` keys up to its own and
-    the sequence's first ``sinks`` ones."""
+    the sequence's first ``sinks`` ones; behind ``assign_pages``, ``seq_len`` is
+    its ``attend_len``, which keeps refused sequences' tokens from pages that are
+    gone."""
     if window is not None:
         _window_sizes(window, sinks)
     elif sinks:

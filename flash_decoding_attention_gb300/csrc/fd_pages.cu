@@ -240,6 +240,9 @@ __device__ __forceinline__ Totals plan(const AssignPages& p, const Sums& s, long
       p.positions[b] = granted ? x.rec.L : -1;
       p.seq_len_out[b] = x.n < 0 ? 0 : granted ? (int)x.total : x.rec.L;
       if (p.window) p.released_out[b] = x.released;
+      // (what goes back with a window is what tokens from L on do not see:
+      // sequences without any in this step are not for its attention)
+      if (p.attend_len) p.attend_len[b] = granted && x.n > 0 ? (int)x.total : 0;
     }
     tokens += all_tokens;
     back += all_back;

@@ -160,6 +160,7 @@ struct AssignPages {
   int32_t *table, *free_pages;
   const int32_t *seq_len, *new_tokens, *free_count, *released;
   int32_t *seq_len_out, *free_count_out, *released_out, *q_start, *positions;
+  int32_t* attend_len;   // or null
   long long* slots;
   long long num_slots, capacity;
   int batch, stride, page_shift;

@@ -349,6 +349,22 @@ fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const in
                           int32_t* free_count_out, int32_t* released_out, int32_t* q_start,
                           int32_t* positions, int64_t* slots, int64_t num_slots, void* workspace,
                           size_t workspace_bytes, fd_stream_t stream) {
+  return fd_assign_pages_attended(block_table, block_table_stride, seq_len, new_tokens, free_pages,
+                                  free_capacity, free_count, batch, page_size, window, sinks,
+                                  released, seq_len_out, free_count_out, released_out, q_start,
+                                  positions, slots, num_slots, nullptr, workspace,
+                                  workspace_bytes, stream);
+}
+
+fd_status fd_assign_pages_attended(int32_t* block_table, int block_table_stride,
+                                   const int32_t* seq_len, const int32_t* new_tokens,
+                                   int32_t* free_pages, int64_t free_capacity,
+                                   const int32_t* free_count, int batch, int page_size, int window,
+                                   int sinks, const int32_t* released, int32_t* seq_len_out,
+                                   int32_t* free_count_out, int32_t* released_out,
+                                   int32_t* q_start, int32_t* positions, int64_t* slots,
+                                   int64_t num_slots, int32_t* attend_len, void* workspace,
+                                   size_t workspace_bytes, fd_stream_t stream) {
   if (!block_table || !seq_len || !new_tokens || !free_pages || !free_count || !seq_len_out ||
       !free_count_out || !q_start || !positions || !workspace)
     return FD_ERR_INVALID_ARG;
@@ -365,7 +381,7 @@ fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const in
                            (const int32_t*)free_pages, free_count, released,
                            (const int32_t*)seq_len_out, (const int32_t*)free_count_out,
                            (const int32_t*)released_out, (const int32_t*)q_start,
-                           (const int32_t*)positions})
+                           (const int32_t*)positions, (const int32_t*)attend_len})
     if (!aligned(a, 4)) return FD_ERR_INVALID_ARG;
   if (!aligned(slots, 8) || !aligned(workspace, 256)) return FD_ERR_INVALID_ARG;
   if (workspace_bytes < assign_pages_bytes(batch)) return FD_ERR_WORKSPACE_TOO_SMALL;
@@ -388,6 +404,7 @@ fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const in
       {q_start, 4 * (batch + 1ll), -1},
       {positions, 4ll * batch, -1},
       {slots, 8 * num_slots, -1},
+      {attend_len, 4ll * batch, -1},
       {workspace, (int64_t)assign_pages_bytes(batch), -1},
   };
   for (int i = 4; i < (int)(sizeof(all) / sizeof(all[0])); ++i)
@@ -412,6 +429,7 @@ fd_status fd_assign_pages(int32_t* block_table, int block_table_stride, const in
   p.released_out = released_out;
   p.q_start = q_start;
   p.positions = positions;
+  p.attend_len = attend_len;
   static_assert(sizeof(long long) == sizeof(int64_t), "slots");
   p.slots = reinterpret_cast<long long*>(slots);
   p.num_slots = num_slots;

@@ -311,8 +311,8 @@ fd_status fd_decode_attention_append(const void *q, const void *k_new, const voi
  * A sequence longer than its row of the block table is recorded as
  * FD_ERR_DEVICE_BOUNDS, and the tiles past the row's end are absent.
  * Block-table entries of pages none of whose tokens the query sees are not
- * used, so such pages may have been given away (fd_assign_pages does that) and
- * their entries may hold anything.  Rows of hidden tokens have no effect,
+ * used, so such pages may have been given away (fd_assign_pages does that; see
+ * there for sequences that it refuses) and their entries may hold anything.  Rows of hidden tokens have no effect,
  * whatever bits they hold; in a contiguous cache they must lie inside it (they
  * share tiles with visible ones).
  *
@@ -553,7 +553,12 @@ size_t fd_assign_pages_workspace_bytes(int batch);
  *   sequence; columns below ceil(sinks / page_size) only go when the sequence
  *   ends), released_out[b] the one after this call.  The attention entry points
  *   with this window and these sinks do not use the entries of pages that are
- *   gone, nor does this one; they are left in the table.
+ *   gone for tokens at L and later, nor does this one; they are left in the
+ *   table.  Earlier tokens see further back: a refused sequence's n tokens,
+ *   which an attention call given seq_len_out takes for those at L - n .. L - 1,
+ *   and a decode query of a sequence without new tokens, at L - 1.  With a window
+ *   the step's attention is therefore given fd_assign_pages_attended's attend_len
+ *   as its seq_len wherever a sequence may be refused or has no new tokens.
  * They are put on the stack in order of sequences, then columns.  A page must
  * belong to one sequence alone (prefix pages that several rows name are not for
  * this call).  Ids are moved as they are.
@@ -593,6 +598,26 @@ fd_status fd_assign_pages(int32_t *block_table, int block_table_stride, const in
                           int32_t *free_count_out, int32_t *released_out, int32_t *q_start,
                           int32_t *positions, int64_t *slots, int64_t num_slots,
                           void *workspace, size_t workspace_bytes, fd_stream_t stream);
+
+/*
+ * fd_assign_pages that also says how many tokens of each sequence this step's
+ * attention looks at:
+ *
+ * attend_len   int32 [batch], or NULL: L + n of a served sequence with n > 0 new
+ *              tokens, 0 of every other.  As seq_len of the attention calls it
+ *              leaves refused, ended and idle sequences without a key: their
+ *              output rows are zero with lse = -inf, and none of their entries
+ *              of the block table is used.
+ */
+fd_status fd_assign_pages_attended(int32_t *block_table, int block_table_stride,
+                                   const int32_t *seq_len, const int32_t *new_tokens,
+                                   int32_t *free_pages, int64_t free_capacity,
+                                   const int32_t *free_count, int batch, int page_size,
+                                   int window, int sinks, const int32_t *released,
+                                   int32_t *seq_len_out, int32_t *free_count_out,
+                                   int32_t *released_out, int32_t *q_start, int32_t *positions,
+                                   int64_t *slots, int64_t num_slots, int32_t *attend_len,
+                                   void *workspace, size_t workspace_bytes, fd_stream_t stream);
 
 /* Scratch bytes fd_prefill_attention needs on the current device (host
  * function), for any batch, lengths and head counts; 0 for an invalid
