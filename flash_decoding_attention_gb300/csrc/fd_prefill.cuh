@@ -1232,9 +1232,10 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true, WIN> w
   constexpr int NS = SH::kSlots;
   static_assert(NS % 2 == 0, "K tiles lie in the even slots");
   const int lane = threadIdx.x & 31, t = threadIdx.x - kFixWarp0 * 32;
-  // page of key k of the stream, or -1 behind the last key of the segment
-  auto page_of = [&](const Seg& g, int j, int k) -> int {
-    if (j >= g.te || k >= g.end) return -1;
+  // page of key k of the stream, or -1 behind the last key of the segment, and
+  // where no row sees the key (its page may be gone)
+  auto page_of = [&](const Seg& g, const Sight<WIN>& sight, int j, int k) -> int {
+    if (j >= g.te || k >= g.end || sight.hidden(k)) return -1;
     if (!p.at.block_table) return 0;
     const int col = k >> p.at.page_shift;
     return col < p.at.bt_stride
@@ -1262,12 +1263,12 @@ __device__ __forceinline__ void token_scales(const Prefill& p, Walk<true, WIN> w
           ks[i] = __ldg(p.k_scales + row * p.num_kv_heads + seg.h);
           vs[i] = __ldg(p.v_scales + row * p.num_kv_heads + seg.h);
         }
-        page[i] = page_of(seg, j + 1, next + t + 64 * i);
+        page[i] = page_of(seg, sight, j + 1, next + t + 64 * i);
       }
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      page[i] = page_of(seg, seg.tb, sight.key(seg, seg.tb) + t + 64 * i);
+      page[i] = page_of(seg, sight, seg.tb, sight.key(seg, seg.tb) + t + 64 * i);
     if (seg.te > seg.tb) load(seg.tb);
     for (int j = seg.tb; j < seg.te; ++j, ++n) {
       float k[2], v[2];

@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (sh.gather || (TOK && !sh.scale_tma)) {
           // the tile's per-token scales of its hc heads, element by element
-          // (rows past the end, or outside the cache, read as zero); then
+          // (rows past the end, hidden, or outside the cache, read as zero); then
           // every lane's copies complete on the stage's "full" barrier
           const int stg = (int)(n % S);
           float* dk = scl + (size_t)stg * (sh.scale_bytes / 4);
@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tt = idx / sh.hc, h = idx - tt * sh.hc;
             const int t = t0 + tt;
             long long row = -1;
-            if (tt < valid) {
+            if (tt < valid && !(WIN && wv.hides(t, 1))) {
               row = p.block_table
                         ? ((long long)sm.pages[(t >> p.page_shift) - win_lo] << p.page_shift) +
                               (t & (p.page_size - 1))
