@@ -7,11 +7,13 @@
 // part; a head's D / 16 threads sit in one warp, so the norm and the per-token
 // scale are warp reductions.
 //
-// A square of a 16-bit element is exact in fp32, and their sum is kept as two
-// floats (the rounding error of every addition is added up beside it), so that it
-// is the exact sum rounded once whatever the order of the additions: the codes
-// stay reproducible, where a plain fp32 sum would move a value next to a border
-// to either side.  The arithmetic runs on packed pairs, 3.5 instructions an
+// A square of a 16-bit element is exact in fp32 (from 2^-149 up), and their sum is
+// kept as two floats: the rounding error of every addition, itself exact, is added
+// up beside it.  What the second float's own additions lose is below 2^-40 of the
+// sum (a thread's 8 additions a lane lose 8 * 2^-24 of errors up to 8 * 2^-24, the
+// tree's some 100 * 2^-48), so that the sum rounds like the exact one unless that
+// lies as near to the middle of two floats: a plain fp32 sum would move every
+// value next to a border of the codes to either side.  The arithmetic runs on packed pairs, 3.5 instructions an
 // element for the sum.
 //
 // An axis only changes which row of the table a pair's cosine and sine come from.
@@ -21,7 +23,7 @@
 // Everything is read and written once: DRAM traffic is the floor.  21000 tokens of
 // 32 query and 8 KV heads of 128, bf16 into bf16 with both norms (528 MB both
 // ways), take 110 us, 4.8 TB/s (the plain append 6.0): issue slots are two thirds
-// busy, a third of them with the exact sum and the division, and 24 warps an SM
+// busy, a third of them with the two-float sum and the division, and 24 warps an SM
 // do not hide the rest.  Without norms (64 registers, 32 warps) 10000 tokens of 16
 // and 4 heads (123 MB) take 27 us, 4.6 TB/s; 64 tokens 4.7 us, a launch and five
 // dependent loads.  What did not pay: 128 registers and four heads in flight (171
@@ -61,8 +63,8 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {   // a - b, o
   return fma2(b, pack2(-1.f, -1.f), a);
 }
 
-// (s, e) += x^2: s + e keeps the exact sum.  The error of an addition is itself
-// a float, found by four more operations (Knuth's two-sum; x^2 is exact, so the
+// (s, e) += x^2: s + e keeps the sum (but for e's own roundings, 2^-24 of it).
+// The error of an addition is itself a float, found by four more operations (Knuth's two-sum; x^2 is exact, so the
 // multiplications fold into the additions).
 __device__ __forceinline__ void add_square(uint64_t& s, uint64_t& e, uint64_t x) {
   const uint64_t t = fma2(x, x, s), w = sub2(s, t);

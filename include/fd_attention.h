@@ -469,10 +469,13 @@ fd_status fd_append_kv_packed(const void *q, int64_t q_stride, void *q_out, cons
  * of q becomes
  *     x_d / sqrt(sum_d x_d^2 / head_dim + norm_eps) * q_norm[d],
  * a head of k_new the same with k_norm; either may be NULL (that tensor is not
- * normed).  Values are not normed.  The sum of squares is the exact one rounded
- * to fp32; the products, the quotient 1 / sqrt and the rotation are single fp32
- * operations, and nothing is rounded to 16 bits in between.  (A sum of squares
- * beyond fp32's range is infinite: finite elements become zero.)
+ * normed).  Values are not normed.  The sum of squares is known to 2^-40 of
+ * itself and then rounded to fp32 once: it is the exact sum rounded, unless that
+ * lies so near the middle of two fp32 numbers, where it may be either of them
+ * (and depend on the elements' places).  The products, the quotient 1 / sqrt and
+ * the rotation are single fp32 operations, and nothing is rounded to 16 bits in
+ * between.  (A sum of squares beyond fp32's range is infinite: finite elements
+ * become zero.  Squares below 2^-149 are rounded to a multiple of it.)
  *
  * q_norm, k_norm  device arrays [head_dim] of new_dtype, or of fp32 with
  *             norm_f32 non-zero, aligned to their elements; q_norm needs q.
