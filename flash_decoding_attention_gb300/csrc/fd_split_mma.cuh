@@ -821,7 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f0 = wn.token(f0);
                 f1 = wn.token(f1);
               }
-              const int pg0 = f0 >> p.page_shift, pg1 = f1 >> p.page_shift;
+              const int pg0 = f0 >> p.page_shift;
+              int pg1 = f1 >> p.page_shift;
+              // (a sequence longer than its row of the table: nothing past the row)
+              if constexpr (WIN) pg1 = min(pg1, p.bt_stride - 1);
               if (lane < kPageWindow / 32 && pg0 + 32 * lane <= pg1)
                 prefetch_l2(p.block_table + (long long)bn * p.bt_stride + pg0 + 32 * lane);
             }
