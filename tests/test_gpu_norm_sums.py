@@ -1,5 +1,5 @@
 """GPU tests of the normed append's sum of squares next to the middle of two fp32
-numbers, and of the signs of extreme elements."""
+numbers."""
 import numpy as np
 import pytest
 import torch
