@@ -998,18 +998,18 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
     with _on(dev, stream):
         i32 = dict(dtype=torch.int32, device=dev)
         if seq_len_out is None:
-            seq_len_out = torch.empty(batch, **i32)
+            seq_len_out = torch.empty_like(seq_len)
         if free_count_out is None:
             free_count_out = torch.empty(1, **i32)
         if window is not None:
             if released_out is None:
-                released_out = torch.empty(batch, **i32)
+                released_out = torch.empty_like(seq_len)
             if attend_len is None:
-                attend_len = torch.empty(batch, **i32)
+                attend_len = torch.empty_like(seq_len)
         if q_start is None:
             q_start = torch.empty(batch + 1, **i32)
         if positions is None:
-            positions = torch.empty(batch, **i32)
+            positions = torch.empty_like(seq_len)
         if slots is None and num_slots:
             slots = torch.empty(num_slots, dtype=torch.int64, device=dev)
         if workspace is None:
