@@ -24,7 +24,9 @@
 // 32 query and 8 KV heads of 128, bf16 into bf16 with both norms (528 MB both
 // ways), take 110 us, 4.8 TB/s (the plain append 6.0): issue slots are two thirds
 // busy, a third of them with the two-float sum and the division, and 24 warps an SM
-// do not hide the rest.  Without norms (64 registers, 32 warps) 10000 tokens of 16
+// do not hide the rest.  (That is what this kernel executes, 354 instructions a
+// thread for 16 elements, not a bound: a thread fetches and packs its weights
+// anew for every head.)  Without norms (64 registers, 32 warps) 10000 tokens of 16
 // and 4 heads (123 MB) take 27 us, 4.6 TB/s; 64 tokens 4.7 us, a launch and five
 // dependent loads.  What did not pay: 128 registers and four heads in flight (171
 // us for those 528 MB), 64 and spills (131), persistent blocks with a warp that

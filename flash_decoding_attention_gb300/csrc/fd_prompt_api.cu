@@ -1,6 +1,6 @@
 // fd_prompt_api.cu -- the prompt path's entry points: argument checks and
-// launches of fd_rotary_table, fd_append_kv_packed, fd_read_kv and
-// fd_prefill_attention.
+// launches of fd_rotary_table, fd_append_kv_packed, fd_append_kv_normed,
+// fd_read_kv, fd_assign_pages, fd_prefill_attention and their variants.
 #include <cmath>
 #include <cstring>
 

@@ -359,7 +359,8 @@ __device__ __forceinline__ uint2 widen8x4(uint32_t w) {
 // The same for the window kernels, where int8 as bf16 takes eight instructions
 // in place of fourteen: with m the low seven bits, 128 + m is 0x43 above m, and
 // code = (128 + m) - (128 or, with the sign bit set, 256), which is 0x43 above
-// 0x00 or 0x80, the sign bit itself.
+// 0x00 or 0x80, the sign bit itself.  (The same bits; the windowless kernels have
+// not been measured with it and keep the form their figures were taken with.)
 template <int KVT, bool BF16, bool WIN>
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
   if constexpr (WIN && KVT == FD_I8 && BF16) {
@@ -540,7 +541,7 @@ struct Shared {
 // ones that are hidden are treated like those past a segment's end.  A box
 // all of whose rows are hidden is not loaded: its page may be gone.  64 sequences
 // of 256 .. 32768 e4m3 keys (64/8 heads, pages of 64) with a window of 4096 and 4
-// first tokens, 329 MB, take 59 us, 5.6 TB/s of a measured copy's 6.7 (the whole
+// first tokens, 329 MB, take 59 to 60 us, 5.5 TB/s of a measured copy's 6.7 (the whole
 // sequences are 771 MB).
 template <int KVT, typename QT, int D, bool TOK, int QROWS, bool CAUSAL, bool FLIP = false,
           bool WIN = false>
