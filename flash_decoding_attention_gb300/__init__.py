@@ -923,15 +923,20 @@ def _layout_index(kv_start_idx, block_table, batch: int, at: int) -> None:
         _index("kv_start_idx", kv_start_idx, batch, at)
 
 
-class PageStep(NamedTuple):
-    """What assign_pages says of a step; every entry is on the device."""
+class _PageArrays(NamedTuple):
     q_start: torch.Tensor              # int32 [B + 1]: where each sequence's packed tokens begin
     positions: torch.Tensor            # int32 [B]: of its first new token; -1: not served
     seq_len: torch.Tensor              # int32 [B]: cached tokens with the new ones
     free_count: torch.Tensor           # int32 [1]: pages left on the stack
     released: Optional[torch.Tensor]   # int32 [B]: first column not given back (with a window)
     slots: Optional[torch.Tensor]      # int64 [num_slots]: cache row of every packed token, or -1
-    attend_len: Optional[torch.Tensor]   # int32 [B]: seq_len for this step's attention (with a window)
+
+
+class PageStep(_PageArrays):
+    """What assign_pages says of a step; every entry is on the device.
+    ``attend_len`` (int32 [B], with a window or where asked for) is seq_len for
+    this step's attention; it is an attribute beside the tuple's six entries."""
+    attend_len: Optional[torch.Tensor] = None
 
 
 def alloc_page_workspace(batch: int, device=None) -> torch.Tensor:
@@ -1018,8 +1023,9 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
                                  page_size, window or 0, sinks, released, seq_len_out,
                                  free_count_out, released_out, q_start, positions, slots,
                                  attend_len, workspace)
-    return PageStep(q_start, positions, seq_len_out, free_count_out, released_out, slots,
-                    attend_len)
+    step = PageStep(q_start, positions, seq_len_out, free_count_out, released_out, slots)
+    step.attend_len = attend_len
+    return step
 
 
 def alloc_prefill_workspace(head_dim: int, device=None) -> torch.Tensor:

@@ -34,6 +34,8 @@ def test_lengths_of_many_kinds(B, window):
         assert own is None or got.attend_len is own
         assert got.attend_len.tolist() == _lengths(got, new)
         assert any(got.attend_len.tolist()) or B == 5
+        q_start, _, seq, _, _, _ = got           # the tuple's entries are the arrays of the state
+        assert q_start is got.q_start and seq is got.seq_len
     if not window:
         assert s.step([0] * B)[0].attend_len is None
 
