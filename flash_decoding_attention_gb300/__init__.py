@@ -970,8 +970,8 @@ def assign_pages(block_table: torch.Tensor, seq_len: torch.Tensor, new_tokens: t
     step.  Pages that earlier tokens still see may be among them, so the step's
     attention takes ``attend_len`` as its lengths: those of the served sequences
     with new tokens, 0 of refused, ended and idle ones, whose rows it leaves zero
-    (lse -inf).  (Without a window it is made only where given.)  The ``_out`` arrays default to fresh ones and may be the inputs
-    themselves."""
+    (lse -inf).  (Without a window it is made only where given.)  The ``_out``
+    arrays default to fresh ones and may be the inputs themselves."""
     if not block_table.is_cuda:
         raise ValueError(f"the block table must be on a GPU, got {block_table.device}")
     if not 1 <= page_size <= 256:

@@ -13,8 +13,8 @@
 // sum (a thread's 8 additions a lane lose 8 * 2^-24 of errors up to 8 * 2^-24, the
 // tree's some 100 * 2^-48), so that the sum rounds like the exact one unless that
 // lies as near to the middle of two floats: a plain fp32 sum would move every
-// value next to a border of the codes to either side.  The arithmetic runs on packed pairs, 3.5 instructions an
-// element for the sum.
+// value next to a border of the codes to either side.  The arithmetic runs on
+// packed pairs, 3.5 instructions an element for the sum.
 //
 // An axis only changes which row of the table a pair's cosine and sine come from.
 // A block gathers them for its few tokens into shared memory first.  Blocks are
@@ -66,8 +66,8 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {   // a - b, o
 }
 
 // (s, e) += x^2: s + e keeps the sum (but for e's own roundings, 2^-24 of it).
-// The error of an addition is itself a float, found by four more operations (Knuth's two-sum; x^2 is exact, so the
-// multiplications fold into the additions).
+// The error of an addition is itself a float, found by four more operations
+// (Knuth's two-sum; x^2 is exact, so the multiplications fold into the additions).
 __device__ __forceinline__ void add_square(uint64_t& s, uint64_t& e, uint64_t x) {
   const uint64_t t = fma2(x, x, s), w = sub2(s, t);
   e = add2(e, add2(sub2(s, add2(t, w)), fma2(x, x, w)));

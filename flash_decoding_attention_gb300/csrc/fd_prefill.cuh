@@ -60,10 +60,11 @@
 // counts: 16384 bf16 tokens of 32/8 heads take 1.07 ms with a window of 8192 (1.54
 // PFLOP/s) and 289 us with 1024 (0.92), 9 tiles of 1.38 us a segment beside 6 us
 // of masks, last product, epilogue and restart, which nothing overlaps because
-// both query tiles of a pair begin and end on the same keys.  An edge tile is put right in
-// tensor memory in those blocks of 32 keys that some row of the warp sees and some
-// does not (3.7 -> 2.2 us for a first tile), the next segment is walked to under
-// the last product, and the usual epilogue loads ahead of its stores (2.5 -> 1.4).
+// both query tiles of a pair begin and end on the same keys.  An edge tile is put
+// right in tensor memory in those blocks of 32 keys that some row of the warp sees
+// and some does not (3.7 -> 2.2 us for a first tile), the next segment is walked to
+// under the last product, and the usual epilogue loads ahead of its stores (2.5 ->
+// 1.4).
 //
 // Roundings below 32 bits: P to the query's 16-bit type (the tensor cores
 // take 16-bit operands; an error of half a step of each probability, the

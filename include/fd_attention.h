@@ -312,9 +312,9 @@ fd_status fd_decode_attention_append(const void *q, const void *k_new, const voi
  * FD_ERR_DEVICE_BOUNDS, and the tiles past the row's end are absent.
  * Block-table entries of pages none of whose tokens the query sees are not
  * used, so such pages may have been given away (fd_assign_pages does that; see
- * there for sequences that it refuses) and their entries may hold anything.  Rows of hidden tokens have no effect,
- * whatever bits they hold; in a contiguous cache they must lie inside it (they
- * share tiles with visible ones).
+ * there for sequences that it refuses) and their entries may hold anything.
+ * Rows of hidden tokens have no effect, whatever bits they hold; in a contiguous
+ * cache they must lie inside it (they share tiles with visible ones).
  *
  * window     >= 1 (1: the query's own token); longer than a sequence: all of it.
  * sinks      >= 0.
